@@ -35,6 +35,9 @@ EXPORTED_SYMBOLS = (
     "coat_e4m3_encode", "coat_e4m3_decode", "coat_fp8_quantize_act",
     "coat_fp8_gemm_group_quant", "coat_fp8_gemm_bf16", "coat_status_string",
     "coat_last_hip_error", "coat_abi_version",
+    "coat_fp8_rms_norm", "coat_fp8_rms_norm_bwd", "coat_fp8_rms_norm_bwd_workspace",
+    "coat_fp8_swiglu", "coat_fp8_swiglu_bwd", "coat_fp8_qk_norm_rope",
+    "coat_fp8_qk_norm_rope_bwd", "coat_fp8_qk_norm_rope_bwd_workspace",
 )
 
 
@@ -61,6 +64,49 @@ class AdamWHParams(ctypes.Structure):
                 ("group_size", ctypes.c_int32)]
 
 
+_vp, _f32, _i32, _i64 = ctypes.c_void_p, ctypes.c_float, ctypes.c_int32, ctypes.c_int64
+
+
+def _fields(spec: str):
+    """(name, type) pairs from "type: name name ..., type: name ..."."""
+    types = {"ptr": _vp, "f32": _f32, "i32": _i32, "i64": _i64}
+    return [(name, types[kind.strip()]) for part in spec.split(",")
+            for kind, names in [part.split(":")] for name in names.split()]
+
+
+class RMSNormArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: x residual weight residual_out y y_codes y_amax codes scales rstd, "
+                       "i64: rows cols, f32: eps y_scale, i32: group_size")
+
+
+class RMSNormBwdArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: dy codes scales rstd weight d_residual dx dw workspace, "
+                       "i64: workspace_bytes rows cols, i32: group_size accumulate")
+
+
+class SwigluArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: gate_up codes scales h h_codes h_amax, i64: rows cols, f32: h_scale, "
+                       "i32: group_size")
+
+
+class QkShape(ctypes.Structure):
+    _fields_ = _fields("i64: tokens table_rows, i32: q_heads k_heads head_dim rot_dim interleaved "
+                       "group_size")
+
+
+class QkNormRopeArgs(ctypes.Structure):
+    _fields_ = [("shape", QkShape)] + _fields(
+        "ptr: q k, i64: q_stride k_stride, ptr: q_weight k_weight cos sin positions q_out k_out, "
+        "i64: q_out_stride k_out_stride, ptr: codes scales rstd, f32: eps")
+
+
+class QkNormRopeBwdArgs(ctypes.Structure):
+    _fields_ = [("shape", QkShape)] + _fields(
+        "ptr: dq_out dk_out, i64: dq_out_stride dk_out_stride, ptr: codes scales rstd q_weight "
+        "k_weight cos sin positions dq dk, i64: dq_stride dk_stride, ptr: dq_weight dk_weight "
+        "workspace, i64: workspace_bytes, i32: accumulate")
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -85,6 +131,18 @@ def _load(path: str = LIB_PATH):
     lib.coat_fp8_gemm_group_quant.argtypes = [vp, vp, f32, f32, i64, i64, i64, i32, vp, vp, vp, vp]
     lib.coat_fp8_gemm_bf16.restype = ctypes.c_int
     lib.coat_fp8_gemm_bf16.argtypes = [vp, vp, f32, f32, i64, i64, i64, vp, vp]
+    for name, args in (("rms_norm", RMSNormArgs), ("rms_norm_bwd", RMSNormBwdArgs),
+                       ("swiglu", SwigluArgs), ("qk_norm_rope", QkNormRopeArgs),
+                       ("qk_norm_rope_bwd", QkNormRopeBwdArgs)):
+        fn = getattr(lib, f"coat_fp8_{name}")
+        fn.restype = ctypes.c_int
+        fn.argtypes = [ctypes.POINTER(args), vp]
+    lib.coat_fp8_swiglu_bwd.restype = ctypes.c_int
+    lib.coat_fp8_swiglu_bwd.argtypes = [vp, vp, vp, i64, i64, i32, vp, vp]
+    lib.coat_fp8_rms_norm_bwd_workspace.restype = i64
+    lib.coat_fp8_rms_norm_bwd_workspace.argtypes = [i64, i64]
+    lib.coat_fp8_qk_norm_rope_bwd_workspace.restype = i64
+    lib.coat_fp8_qk_norm_rope_bwd_workspace.argtypes = [i64, i64, i64]
     lib.coat_status_string.restype = ctypes.c_char_p
     lib.coat_status_string.argtypes = [ctypes.c_int]
     lib.coat_last_hip_error.restype = ctypes.c_char_p
@@ -351,3 +409,239 @@ def gemm_bf16(a: torch.Tensor, b: torch.Tensor, a_scale: float, b_scale: float,
     _on_device(a=a, b=b, c_bf16=c_bf16)
     _check(lib.coat_fp8_gemm_bf16(_ptr(a), _ptr(b), a_scale, b_scale, M, N, K, _ptr(c_bf16),
                                   _stream(stream)))
+
+
+# ------------------------------------------------- activation checkpoints
+
+def _shape2(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    return t.shape
+
+
+def _opt(t, name: str, dtypes, min_numel: int):
+    if t is not None:
+        _need(t, name, dtypes, min_numel)
+
+
+def _groups(cols: int, group_size: int) -> int:
+    return cols // group_size if group_size > 0 else 0
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, *, y: Optional[torch.Tensor] = None,
+             y_codes: Optional[torch.Tensor] = None, y_scale: float = 1.0,
+             y_amax: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+             residual_out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
+             scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+             group_size: int = 128, stream=None):
+    """RMS norm of h = x (+ residual, written to residual_out) into y (BF16)
+    and/or y_codes (E4M3 under the one scale y_scale; y_amax is raised to the
+    largest |y|).  codes and scales, if given, receive h's checkpoint and rstd
+    the rows' reciprocal root mean squares, for rms_norm_bwd."""
+    rows, cols = _shape2(x, "x")
+    n = rows * cols
+    _need(x, "x", BF16_DTYPES, 0)
+    _need(weight, "weight", BF16_DTYPES, cols)
+    _opt(residual, "residual", BF16_DTYPES, n)
+    _opt(residual_out, "residual_out", BF16_DTYPES, n)
+    _opt(y, "y", BF16_DTYPES, n)
+    _opt(y_codes, "y_codes", CODE_DTYPES, n)
+    _opt(y_amax, "y_amax", F32_DTYPES, 1)
+    _opt(codes, "codes", CODE_DTYPES, n)
+    _opt(scales, "scales", F32_DTYPES, rows * _groups(cols, group_size))
+    _opt(rstd, "rstd", F32_DTYPES, rows)
+    _on_device(x=x, weight=weight, residual=residual, residual_out=residual_out, y=y, y_codes=y_codes,
+               y_amax=y_amax, codes=codes, scales=scales, rstd=rstd)
+    a = RMSNormArgs(_ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(y_codes),
+                    _ptr(y_amax), _ptr(codes), _ptr(scales), _ptr(rstd), rows, cols, eps, y_scale,
+                    group_size)
+    _check(lib.coat_fp8_rms_norm(ctypes.byref(a), _stream(stream)))
+
+
+def rms_norm_bwd_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace rms_norm_bwd needs for a weight gradient."""
+    return _workspace_bytes(lib.coat_fp8_rms_norm_bwd_workspace(rows, cols))
+
+
+def _workspace_bytes(n: int) -> int:
+    if n < 0:
+        _check(COAT_ERR_INVALID_VALUE)
+    return n
+
+
+def _workspace(workspace, need: bool, nbytes: int):
+    """Address and size of the workspace: a byte count of `nbytes` is required
+    where `need`."""
+    if workspace is None:
+        if need and nbytes > 0:
+            raise ValueError(f"workspace is required ({nbytes} bytes)")
+        return None, 0
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous torch.Tensor")
+    have = workspace.numel() * workspace.element_size()
+    if need and have < nbytes:
+        raise ValueError(f"workspace holds {have} bytes, needs at least {nbytes}")
+    return workspace.data_ptr(), have
+
+
+def rms_norm_bwd(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, rstd: torch.Tensor,
+                 weight: torch.Tensor, dx: torch.Tensor, dw: Optional[torch.Tensor] = None, *,
+                 d_residual: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 accumulate: bool = False, group_size: int = 128, stream=None):
+    """Gradient of rms_norm from its checkpoint: dx (BF16, d_residual added if
+    given) and, if given, dw (FP32, written or accumulated; needs
+    rms_norm_bwd_workspace(rows, cols) bytes of workspace)."""
+    rows, cols = _shape2(dy, "dy")
+    n = rows * cols
+    _need(dy, "dy", BF16_DTYPES, 0)
+    _need(codes, "codes", CODE_DTYPES, n)
+    _need(scales, "scales", F32_DTYPES, rows * _groups(cols, group_size))
+    _need(rstd, "rstd", F32_DTYPES, rows)
+    _need(weight, "weight", BF16_DTYPES, cols)
+    _need(dx, "dx", BF16_DTYPES, n)
+    _opt(dw, "dw", F32_DTYPES, cols)
+    _opt(d_residual, "d_residual", BF16_DTYPES, n)
+    need = dw is not None
+    ws, ws_bytes = _workspace(workspace, need, rms_norm_bwd_workspace(rows, cols) if need else 0)
+    _on_device(dy=dy, codes=codes, scales=scales, rstd=rstd, weight=weight, dx=dx, dw=dw,
+               d_residual=d_residual, workspace=workspace)
+    a = RMSNormBwdArgs(_ptr(dy), _ptr(codes), _ptr(scales), _ptr(rstd), _ptr(weight), _ptr(d_residual),
+                       _ptr(dx), _ptr(dw), ws, ws_bytes, rows, cols, group_size, int(accumulate))
+    _check(lib.coat_fp8_rms_norm_bwd(ctypes.byref(a), _stream(stream)))
+
+
+def swiglu(codes: Optional[torch.Tensor], scales: Optional[torch.Tensor], *,
+           gate_up: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+           h_codes: Optional[torch.Tensor] = None, h_scale: float = 1.0,
+           h_amax: Optional[torch.Tensor] = None, group_size: int = 128, stream=None):
+    """Gated activation gate * sigmoid(gate) * up of rows that hold the gates,
+    then the ups, into h (BF16) or h_codes (E4M3 under the one scale h_scale;
+    h_amax is raised to the largest |h|).  The input is the checkpoint codes,
+    scales; or gate_up (BF16), whose checkpoint is then written to codes and
+    scales if they are given."""
+    rows, wide = _shape2(codes if gate_up is None else gate_up, "codes" if gate_up is None else "gate_up")
+    if wide % 2:
+        raise ValueError("a row holds the gates and as many ups: its length is even")
+    cols = wide // 2
+    _opt(gate_up, "gate_up", BF16_DTYPES, 0)
+    _opt(codes, "codes", CODE_DTYPES, rows * wide)
+    _opt(scales, "scales", F32_DTYPES, 2 * rows * _groups(cols, group_size))
+    _opt(h, "h", BF16_DTYPES, rows * cols)
+    _opt(h_codes, "h_codes", CODE_DTYPES, rows * cols)
+    _opt(h_amax, "h_amax", F32_DTYPES, 1)
+    _on_device(gate_up=gate_up, codes=codes, scales=scales, h=h, h_codes=h_codes, h_amax=h_amax)
+    a = SwigluArgs(_ptr(gate_up), _ptr(codes), _ptr(scales), _ptr(h), _ptr(h_codes), _ptr(h_amax), rows,
+                   cols, h_scale, group_size)
+    _check(lib.coat_fp8_swiglu(ctypes.byref(a), _stream(stream)))
+
+
+def swiglu_bwd(dh: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, d_gate_up: torch.Tensor,
+               group_size: int = 128, stream=None):
+    """Gradient of swiglu from its checkpoint: d_gate_up (BF16), the gates'
+    gradients first in each row."""
+    rows, cols = _shape2(dh, "dh")
+    _need(dh, "dh", BF16_DTYPES, 0)
+    _need(codes, "codes", CODE_DTYPES, 2 * rows * cols)
+    _need(scales, "scales", F32_DTYPES, 2 * rows * _groups(cols, group_size))
+    _need(d_gate_up, "d_gate_up", BF16_DTYPES, 2 * rows * cols)
+    _on_device(dh=dh, codes=codes, scales=scales, d_gate_up=d_gate_up)
+    _check(lib.coat_fp8_swiglu_bwd(_ptr(dh), _ptr(codes), _ptr(scales), rows, cols, group_size,
+                                   _ptr(d_gate_up), _stream(stream)))
+
+
+def _heads(t: torch.Tensor, name: str, like=None):
+    """(tokens, heads, head_dim, token stride) of a tensor of heads, which may
+    be part of a packed projection: only the token stride is free."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be a 3-D (tokens, heads, head_dim) tensor")
+    if t.dtype not in BF16_DTYPES:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected one of {BF16_DTYPES}")
+    tokens, heads, dim = t.shape
+    if like is not None and tuple(t.shape) != tuple(like.shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    stride = t.stride(0) if tokens > 1 else heads * dim
+    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)
+                      or stride < heads * dim):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return tokens, heads, dim, stride
+
+
+def _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, group_size, names):
+    tokens, q_heads, dim, _ = _heads(q, names[0])
+    k_tokens, k_heads, k_dim, _ = _heads(k, names[1])
+    if k_tokens != tokens or k_dim != dim:
+        raise ValueError(f"{names[0]} and {names[1]} disagree on tokens or head_dim")
+    table_rows, half = _shape2(cos, "cos")
+    if tuple(_shape2(sin, "sin")) != (table_rows, half):
+        raise ValueError("cos and sin differ in shape")
+    _need(cos, "cos", F32_DTYPES, 0)
+    _need(sin, "sin", F32_DTYPES, 0)
+    _need(q_weight, "q_weight", BF16_DTYPES, dim)
+    _need(k_weight, "k_weight", BF16_DTYPES, dim)
+    _need(positions, "positions", (torch.int64,), tokens)
+    return QkShape(tokens, table_rows, q_heads, k_heads, dim, 2 * half, int(interleaved), group_size)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
+                 eps: float, cos: torch.Tensor, sin: torch.Tensor, positions: torch.Tensor,
+                 q_out: torch.Tensor, k_out: torch.Tensor, *, codes: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                 interleaved: bool = False, group_size: int = 128, stream=None):
+    """RMS norm of every head of q and k (tokens x heads x head_dim, possibly
+    parts of one packed projection) and their rotation by row positions[token]
+    of cos and sin (rows x rot_dim/2, FP32) into q_out and k_out, which may be
+    q and k.  codes, scales and rstd, if given, receive the checkpoint (the
+    query heads of a token, then its key heads).  Tokens whose position is
+    outside the tables are padding and get zeros."""
+    s = _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, group_size, ("q", "k"))
+    q_stride, k_stride = _heads(q, "q")[3], _heads(k, "k")[3]
+    q_out_stride, k_out_stride = _heads(q_out, "q_out", q)[3], _heads(k_out, "k_out", k)[3]
+    rows = s.tokens * (s.q_heads + s.k_heads)
+    _opt(codes, "codes", CODE_DTYPES, rows * s.head_dim)
+    _opt(scales, "scales", F32_DTYPES, rows * _groups(s.head_dim, group_size))
+    _opt(rstd, "rstd", F32_DTYPES, rows)
+    _on_device(q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos=cos, sin=sin, positions=positions,
+               q_out=q_out, k_out=k_out, codes=codes, scales=scales, rstd=rstd)
+    a = QkNormRopeArgs(s, _ptr(q), _ptr(k), q_stride, k_stride, _ptr(q_weight), _ptr(k_weight), _ptr(cos),
+                       _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out), q_out_stride, k_out_stride,
+                       _ptr(codes), _ptr(scales), _ptr(rstd), eps)
+    _check(lib.coat_fp8_qk_norm_rope(ctypes.byref(a), _stream(stream)))
+
+
+def qk_norm_rope_bwd_workspace(tokens: int, heads: int, head_dim: int) -> int:
+    """Bytes of workspace qk_norm_rope_bwd needs for weight gradients (heads:
+    queries and keys)."""
+    return _workspace_bytes(lib.coat_fp8_qk_norm_rope_bwd_workspace(tokens, heads, head_dim))
+
+
+def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, codes: torch.Tensor,
+                     scales: torch.Tensor, rstd: torch.Tensor, q_weight: torch.Tensor,
+                     k_weight: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
+                     positions: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor,
+                     dq_weight: Optional[torch.Tensor] = None, dk_weight: Optional[torch.Tensor] = None,
+                     *, workspace: Optional[torch.Tensor] = None, accumulate: bool = False,
+                     interleaved: bool = False, group_size: int = 128, stream=None):
+    """Gradient of qk_norm_rope from its checkpoint: dq and dk (BF16; they may
+    be dq_out and dk_out) and, if given, dq_weight and dk_weight (FP32,
+    written or accumulated; need qk_norm_rope_bwd_workspace bytes)."""
+    s = _qk_shape(dq_out, dk_out, q_weight, k_weight, cos, sin, positions, interleaved, group_size,
+                  ("dq_out", "dk_out"))
+    dq_out_stride, dk_out_stride = _heads(dq_out, "dq_out")[3], _heads(dk_out, "dk_out")[3]
+    dq_stride, dk_stride = _heads(dq, "dq", dq_out)[3], _heads(dk, "dk", dk_out)[3]
+    heads = s.q_heads + s.k_heads
+    _need(codes, "codes", CODE_DTYPES, s.tokens * heads * s.head_dim)
+    _need(scales, "scales", F32_DTYPES, s.tokens * heads * _groups(s.head_dim, group_size))
+    _need(rstd, "rstd", F32_DTYPES, s.tokens * heads)
+    _opt(dq_weight, "dq_weight", F32_DTYPES, s.head_dim)
+    _opt(dk_weight, "dk_weight", F32_DTYPES, s.head_dim)
+    need = dq_weight is not None
+    ws, ws_bytes = _workspace(workspace, need, qk_norm_rope_bwd_workspace(s.tokens, heads, s.head_dim)
+                              if need else 0)
+    _on_device(dq_out=dq_out, dk_out=dk_out, codes=codes, scales=scales, rstd=rstd, q_weight=q_weight,
+               k_weight=k_weight, cos=cos, sin=sin, positions=positions, dq=dq, dk=dk,
+               dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace)
+    a = QkNormRopeBwdArgs(s, _ptr(dq_out), _ptr(dk_out), dq_out_stride, dk_out_stride, _ptr(codes),
+                          _ptr(scales), _ptr(rstd), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
+                          _ptr(positions), _ptr(dq), _ptr(dk), dq_stride, dk_stride, _ptr(dq_weight),
+                          _ptr(dk_weight), ws, ws_bytes, int(accumulate))
+    _check(lib.coat_fp8_qk_norm_rope_bwd(ctypes.byref(a), _stream(stream)))

@@ -1,0 +1,446 @@
+// coat_norm.hip -- gfx950 kernels and C ABI of the RMS norm with an E4M3
+// checkpoint of its input, and of its backward pass.
+//
+// Sources (see include/coat_fp8.h for the full citations):
+//   [P1] COAT paper review (xllm-io.github.io), section 三: the input of a
+//        non-linear layer is kept in E4M3 per 1xG group for the backward
+//        pass (混合粒度激活量化); the input of a linear layer is E4M3 under
+//        one scale per tensor; COAT LLaMA's BeforeAttention and MLPResidual
+//        take the residual sum and the norm together.
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "coat_elem.h"
+
+using namespace coat;
+
+namespace {
+
+// ------------------------------------------------------------ forward
+//
+//   h = bf16(x + residual),  rstd = (mean(h^2) + eps)^-1/2,  y = h rstd w
+//
+// One block takes one row at a time and keeps it in registers: chunk i of
+// thread t is the eight columns from 8 (t + kThreads i), so every byte is
+// read and written once.  The weight's chunks stay in registers over the
+// rows of a block, and the next row is loaded before the current one is
+// reduced.  The sum of squares is FP32: eight values of a lane in order,
+// then lanes, then waves (LDS, two slots in turn, one barrier a row).  A
+// checkpoint group lies on G/8 neighbouring lanes of one 16-lane DPP row.
+
+constexpr int64_t kMaxCols = 32768;
+
+struct NormParams {
+  const uint16_t* x;
+  const uint16_t* residual;
+  const uint16_t* weight;
+  uint16_t* sum;
+  uint16_t* y;
+  uint8_t* y_codes;
+  float* y_amax;
+  uint8_t* codes;
+  float* scales;
+  float* rstd;
+  int64_t rows;
+  int32_t cols;
+  int32_t group_shift;   // log2(group_size)
+  float eps, inv_y_scale, inv_cols;
+};
+
+// The block's sum of v (every thread gets it).  `slot` alternates between
+// calls: a wave can be at most one barrier ahead of another.
+template <int kThreads>
+__device__ __forceinline__ float block_sum(float v, int slot) {
+  v = lanes_sum<64>(v);
+  if constexpr (kThreads > 64) {
+    constexpr int kWaves = kThreads / 64;
+    __shared__ float part[2][kWaves];
+    if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = part[slot][0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += part[slot][w];
+  }
+  return v;
+}
+
+template <int kThreads, int kC>
+__global__ __launch_bounds__(kThreads) void rms_norm_kernel(const NormParams p) {
+  const int t = threadIdx.x;
+  const int cols = p.cols, lanes = 1 << (p.group_shift - 3);
+  bool ok[kC];
+  int col[kC];
+  uint4 w[kC], next[kC], nres[kC];
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    col[i] = 8 * (t + kThreads * i);
+    ok[i] = col[i] < cols;
+    w[i] = next[i] = nres[i] = make_uint4(0, 0, 0, 0);
+  }
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+      if (ok[i]) {
+        next[i] = load_stream16(p.x + row * cols + col[i]);
+        if (p.residual) nres[i] = load_stream16(p.residual + row * cols + col[i]);
+      }
+  };
+  int64_t row = blockIdx.x;
+  load(row);
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+    if (ok[i]) w[i] = *reinterpret_cast<const uint4*>(p.weight + col[i]);
+
+  float top = 0.0f;
+  int slot = 0;
+  for (; row < p.rows; row += gridDim.x, slot ^= 1) {
+    uint4 raw[kC];
+    float ss = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      float f[8];
+      raw[i] = next[i];
+      if (p.residual) {
+        float r[8];
+        unpack8(raw[i], f);
+        unpack8(nres[i], r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] += r[e];
+        raw[i] = pack8(f);   // everything below reads the sum as it is stored
+      }
+      unpack8(raw[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
+    }
+    if (row + gridDim.x < p.rows) load(row + gridDim.x);
+    const float rstd = 1.0f / sqrtf(__builtin_fmaf(block_sum<kThreads>(ss, slot), p.inv_cols, p.eps));
+    if (p.rstd && t == 0) p.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      const int64_t at = row * cols + col[i];
+      if (p.codes) {   // all lanes: groups exchange their maxima
+        float scale;
+        const uint2 c = checkpoint8(raw[i], lanes, scale);
+        if (ok[i]) {
+          store_stream8(p.codes + at, c);
+          if (((t + kThreads * i) & (lanes - 1)) == 0) p.scales[at >> p.group_shift] = scale;
+        }
+      }
+      if (!ok[i]) continue;
+      if (p.sum) store_stream16(p.sum + at, raw[i]);
+      float f[8], g[8];
+      unpack8(raw[i], f);
+      unpack8(w[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
+      if (p.y) store_stream16(p.y + at, pack8(f));
+      if (p.y_codes) {
+        const float m = max_mag(f);
+        top = fmaxf(top, m);
+        uint32_t c[2];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] *= p.inv_y_scale;
+        e4m3_pack(f, m * p.inv_y_scale, c);
+        store_stream8(p.y_codes + at, make_uint2(c[0], c[1]));
+      }
+    }
+  }
+  if (p.y_amax) raise_amax(p.y_amax, top);
+}
+
+// ----------------------------------------------------------- backward
+//
+// With n = code scale rstd (the normalised input as the checkpoint holds it)
+// and dn = dy w:
+//   dx = rstd (dn - n mean(dn n)) (+ d_residual),   dw = sum over rows of dy n
+//
+// The same layout; a block walks rows with a stride and adds dy n of its
+// columns up in registers, in FP32, writing one row of partial sums at its
+// end.  A second launch adds those up in a fixed order, so the result does
+// not depend on timing.
+
+struct NormBwdParams {
+  const uint16_t* dy;
+  const uint8_t* codes;
+  const float* scales;
+  const float* rstd;
+  const uint16_t* weight;
+  const uint16_t* d_residual;
+  uint16_t* dx;
+  float* partials;   // gridDim.x rows of cols, or NULL: no weight gradient
+  int64_t rows;
+  int32_t cols;
+  int32_t group_shift;
+  float inv_cols;
+};
+
+template <int kThreads, int kC>
+__global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const NormBwdParams p) {
+  const int t = threadIdx.x;
+  const int cols = p.cols;
+  bool ok[kC];
+  int col[kC];
+  uint4 w[kC], dyn[kC], drn[kC];
+  uint2 cn[kC];
+  float sn[kC], rn, dw[kC][8];
+#pragma unroll
+  for (int i = 0; i < kC; ++i) {
+    col[i] = 8 * (t + kThreads * i);
+    ok[i] = col[i] < cols;
+    w[i] = dyn[i] = drn[i] = make_uint4(0, 0, 0, 0);
+    cn[i] = make_uint2(0, 0);
+    sn[i] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  }
+  auto load = [&](int64_t row) __attribute__((always_inline)) {
+    rn = p.rstd[row];
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+      if (ok[i]) {
+        const int64_t at = row * cols + col[i];
+        dyn[i] = load_stream16(p.dy + at);
+        cn[i] = load_stream8(p.codes + at);
+        sn[i] = p.scales[at >> p.group_shift];
+        if (p.d_residual) drn[i] = load_stream16(p.d_residual + at);
+      }
+  };
+  int64_t row = blockIdx.x;
+  load(row);
+#pragma unroll
+  for (int i = 0; i < kC; ++i)
+    if (ok[i]) w[i] = *reinterpret_cast<const uint4*>(p.weight + col[i]);
+
+  int slot = 0;
+  for (; row < p.rows; row += gridDim.x, slot ^= 1) {
+    uint4 dr[kC];
+    float n[kC][8], dn[kC][8], dot = 0.0f;
+    const float rstd = rn;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      float g[8];
+      dr[i] = drn[i];
+      unpack8(dyn[i], dn[i]);
+      e4m3_values8(cn[i], n[i]);
+      unpack8(w[i], g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        n[i][e] = n[i][e] * sn[i] * rstd;
+        dw[i][e] = __builtin_fmaf(dn[i][e], n[i][e], dw[i][e]);
+        dn[i][e] *= g[e];
+        dot = __builtin_fmaf(dn[i][e], n[i][e], dot);
+      }
+    }
+    if (row + gridDim.x < p.rows) load(row + gridDim.x);
+    const float mean = block_sum<kThreads>(dot, slot) * p.inv_cols;
+#pragma unroll
+    for (int i = 0; i < kC; ++i) {
+      if (!ok[i]) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dn[i][e] = rstd * __builtin_fmaf(-n[i][e], mean, dn[i][e]);
+      if (p.d_residual) {
+        float r[8];
+        unpack8(dr[i], r);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dn[i][e] += r[e];
+      }
+      store_stream16(p.dx + row * cols + col[i], pack8(dn[i]));
+    }
+  }
+  if (p.partials) {
+    float* out = p.partials + (int64_t)blockIdx.x * cols;
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+      if (ok[i]) {
+        *reinterpret_cast<float4*>(out + col[i]) = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+        *reinterpret_cast<float4*>(out + col[i] + 4) = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+      }
+  }
+}
+
+// Sums `parts` rows of partial sums by column: a block takes 16 columns (64
+// bytes of a row), its 64 slices add every 64th row, and the slices join in
+// the LDS in a fixed order.
+constexpr int kSumCols = 16, kSumSlices = 64;
+
+__global__ __launch_bounds__(kSumCols* kSumSlices) void sum_partials_kernel(const float* partials, int parts,
+                                                                          int64_t cols, float* dst0, int64_t split,
+                                                                          float* dst1, int accumulate) {
+  __shared__ float part[kSumSlices][kSumCols + 1];
+  const int c = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
+  const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
+  float v = 0.0f;
+  if (col < cols)
+    for (int r = slice; r < parts; r += kSumSlices) v += partials[r * cols + col];
+  part[slice][c] = v;
+  __syncthreads();
+#pragma unroll
+  for (int n = kSumSlices / 2; n > 0; n /= 2) {
+    if (slice < n) part[slice][c] += part[slice + n][c];
+    __syncthreads();
+  }
+  if (slice == 0 && col < cols) {
+    float* dst = col < split ? dst0 + col : dst1 + (col - split);
+    *dst = accumulate ? *dst + part[0][c] : part[0][c];
+  }
+}
+
+// Rows of partial sums of the backward pass: two blocks for each of 256
+// compute units.  A constant, so that the workspace and the order of the sums
+// do not depend on the device.
+constexpr int64_t kNormParts = 512;
+
+int64_t norm_parts(int64_t rows) { return rows < kNormParts ? rows : kNormParts; }
+
+struct NormShape {
+  int threads, chunks;
+};
+
+// Threads and chunks of a row: the row in registers, at least one wave.
+NormShape norm_shape(int64_t cols) {
+  if (cols <= 512) return {64, 1};
+  if (cols <= 1024) return {128, 1};
+  if (cols <= 2048) return {256, 1};
+  if (cols <= 4096) return {256, 2};
+  if (cols <= 8192) return {512, 2};
+  if (cols <= 16384) return {1024, 2};
+  return {1024, 4};
+}
+
+const void* norm_kernel_for(NormShape s, bool backward) {
+#define COAT_NORM(T, C)                                                              \
+  if (s.threads == T && s.chunks == C)                                               \
+    return backward ? reinterpret_cast<const void*>(&rms_norm_bwd_kernel<T, C>)      \
+                    : reinterpret_cast<const void*>(&rms_norm_kernel<T, C>);
+  COAT_NORM(64, 1)
+  COAT_NORM(128, 1)
+  COAT_NORM(256, 1)
+  COAT_NORM(256, 2)
+  COAT_NORM(512, 2)
+  COAT_NORM(1024, 2)
+  COAT_NORM(1024, 4)
+#undef COAT_NORM
+  return nullptr;
+}
+
+coat_status_t check_norm_shape(int64_t rows, int64_t cols, int32_t group_size) {
+  if (rows < 0 || cols < 0) return COAT_ERR_INVALID_VALUE;
+  if (!valid_group_size(group_size)) return COAT_ERR_GROUP_SIZE;
+  if (cols % group_size != 0 || cols > kMaxCols) return COAT_ERR_INVALID_VALUE;
+  if (rows > INT64_MAX / 8 / kMaxCols) return COAT_ERR_INVALID_VALUE;
+  return COAT_OK;
+}
+
+}  // namespace
+
+namespace coat {
+
+hipError_t launch_sum_partials(const float* partials, int parts, int64_t cols, float* dst0, int64_t split,
+                               float* dst1, bool accumulate, hipStream_t stream) {
+  int acc = accumulate ? 1 : 0;
+  void* args[] = {&partials, &parts, &cols, &dst0, &split, &dst1, &acc};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&sum_partials_kernel),
+                         dim3((unsigned)((cols + kSumCols - 1) / kSumCols)), dim3(kSumCols * kSumSlices), args, 0,
+                         stream);
+}
+
+}  // namespace coat
+
+extern "C" {
+
+coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* a, hipStream_t stream) {
+  if (!a) return COAT_ERR_NULL_POINTER;
+  const coat_status_t st = check_norm_shape(a->rows, a->cols, a->group_size);
+  if (st != COAT_OK) return st;
+  if (!isfinite(a->eps) || a->eps <= 0.0f) return COAT_ERR_INVALID_VALUE;
+  if (a->y_codes && !(a->y_scale > 0.0f && isfinite(a->y_scale) && isfinite(1.0f / a->y_scale)))
+    return COAT_ERR_INVALID_VALUE;
+  if (a->y_amax && !a->y_codes) return COAT_ERR_INVALID_VALUE;
+  if (a->rows == 0 || a->cols == 0) return COAT_OK;
+  if (!a->x || !a->weight || (!a->y && !a->y_codes)) return COAT_ERR_NULL_POINTER;
+  if (!a->residual != !a->residual_out || !a->codes != !a->scales) return COAT_ERR_NULL_POINTER;
+  if (!aligned(a->x, 16) || !aligned(a->weight, 16) || !aligned(a->residual, 16) || !aligned(a->residual_out, 16) ||
+      !aligned(a->y, 16) || !aligned(a->y_codes, 16) || !aligned(a->codes, 16) || !aligned(a->scales, 4) ||
+      !aligned(a->rstd, 4) || !aligned(a->y_amax, 4))
+    return COAT_ERR_MISALIGNED;
+  NormParams p;
+  memset(&p, 0, sizeof(p));
+  p.x = a->x;
+  p.residual = a->residual;
+  p.weight = a->weight;
+  p.sum = a->residual_out;
+  p.y = a->y;
+  p.y_codes = a->y_codes;
+  p.y_amax = a->y_amax;
+  p.codes = a->codes;
+  p.scales = a->scales;
+  p.rstd = a->rstd;
+  p.rows = a->rows;
+  p.cols = (int32_t)a->cols;
+  p.group_shift = __builtin_ctz((unsigned)a->group_size);
+  p.eps = a->eps;
+  p.inv_y_scale = a->y_codes ? 1.0f / a->y_scale : 0.0f;
+  p.inv_cols = (float)(1.0 / (double)a->cols);
+  int cus = 0;
+  hipError_t e = current_cu_count(&cus);
+  if (e != hipSuccess) return hip_fail(e);
+  const NormShape s = norm_shape(a->cols);
+  const int64_t most = (int64_t)cus * (2048 / s.threads);   // the threads that fit a CU
+  const int64_t blocks = a->rows < most ? a->rows : most;
+  void* args[] = {&p};
+  e = hipLaunchKernel(norm_kernel_for(s, false), dim3((unsigned)blocks), dim3(s.threads), args, 0, stream);
+  return e == hipSuccess ? COAT_OK : hip_fail(e);
+}
+
+int64_t coat_fp8_rms_norm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || cols > kMaxCols) return -1;
+  return norm_parts(rows) * cols * (int64_t)sizeof(float);
+}
+
+coat_status_t coat_fp8_rms_norm_bwd(const coat_rms_norm_bwd_args_t* a, hipStream_t stream) {
+  if (!a) return COAT_ERR_NULL_POINTER;
+  const coat_status_t st = check_norm_shape(a->rows, a->cols, a->group_size);
+  if (st != COAT_OK) return st;
+  if (a->cols == 0 || (a->rows == 0 && (!a->dw || a->accumulate))) return COAT_OK;
+  if (a->dw && !a->workspace && a->rows > 0) return COAT_ERR_NULL_POINTER;
+  if (a->rows > 0 && (!a->dy || !a->codes || !a->scales || !a->rstd || !a->weight || !a->dx))
+    return COAT_ERR_NULL_POINTER;
+  if (!aligned(a->dy, 16) || !aligned(a->codes, 16) || !aligned(a->scales, 4) || !aligned(a->rstd, 4) ||
+      !aligned(a->weight, 16) || !aligned(a->d_residual, 16) || !aligned(a->dx, 16) || !aligned(a->dw, 4) ||
+      !aligned(a->workspace, 16))
+    return COAT_ERR_MISALIGNED;
+  if (a->dw && a->rows > 0 && a->workspace_bytes < coat_fp8_rms_norm_bwd_workspace(a->rows, a->cols))
+    return COAT_ERR_INVALID_VALUE;
+  const int64_t blocks = norm_parts(a->rows);
+  hipError_t e = hipSuccess;
+  if (a->rows > 0) {
+    NormBwdParams p;
+    memset(&p, 0, sizeof(p));
+    p.dy = a->dy;
+    p.codes = a->codes;
+    p.scales = a->scales;
+    p.rstd = a->rstd;
+    p.weight = a->weight;
+    p.d_residual = a->d_residual;
+    p.dx = a->dx;
+    p.partials = a->dw ? (float*)a->workspace : nullptr;
+    p.rows = a->rows;
+    p.cols = (int32_t)a->cols;
+    p.group_shift = __builtin_ctz((unsigned)a->group_size);
+    p.inv_cols = (float)(1.0 / (double)a->cols);
+    const NormShape s = norm_shape(a->cols);
+    void* args[] = {&p};
+    e = hipLaunchKernel(norm_kernel_for(s, true), dim3((unsigned)blocks), dim3(s.threads), args, 0, stream);
+  }
+  // no rows: the sum of no partial sums, zero
+  if (e == hipSuccess && a->dw)
+    e = launch_sum_partials((const float*)a->workspace, (int)blocks, a->cols, a->dw, a->cols, nullptr,
+                            a->accumulate != 0, stream);
+  return e == hipSuccess ? COAT_OK : hip_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,509 @@
+// coat_qk.hip -- gfx950 kernels and C ABI of the RMS norm of query and key
+// heads with the position rotation in the same pass and an E4M3 checkpoint
+// of the heads, and of its backward pass.
+//
+// Sources (see include/coat_fp8.h for the full citations):
+//   [P1] COAT paper review (xllm-io.github.io), section 三: the inputs of
+//        non-linear layers are kept in E4M3 per 1xG group (混合粒度激活量化).
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "coat_elem.h"
+
+using namespace coat;
+
+namespace {
+
+// A head of D values lies on kLanes lanes of a wave, eight values a lane
+// (kLanes the power of two >= D/8, at least 8; lanes past D/8 idle), so a
+// wave works on 64 / kLanes neighbouring heads at once, queries first, then
+// keys.  A wave takes one token and kH such sets of heads: it loads them all
+// before it works on the first, and the token's cosines and sines and both
+// weights once.  kH is 4, or 1 where that would leave the chip empty.
+//
+// Rotation.  Pair j of a head, (a, b), becomes (a cos_j - b sin_j,
+// b cos_j + a sin_j).  Interleaved: (a, b) = values (2j, 2j + 1), inside a
+// lane.  Otherwise values (j, j + rot/2): rot is a multiple of 16, so a whole
+// chunk's partner is the chunk rot/16 lanes away, which sends its BF16 words
+// over (ds_bpermute); the receiver norms them itself.
+// A token whose position is outside the table is padding: everything written
+// for it is zero.
+
+struct QkParams {
+  const uint16_t* q;        // forward: heads; backward: their output gradients
+  const uint16_t* k;
+  int64_t q_stride, k_stride;   // values between tokens
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t q_out_stride, k_out_stride;
+  const uint16_t* q_weight;
+  const uint16_t* k_weight;
+  const float* cos;
+  const float* sin;
+  const int64_t* positions;
+  uint8_t* codes;
+  float* scales;
+  float* rstd;
+  float* partials;          // backward: gridDim.x rows of 2 D, or NULL
+  int64_t tokens, table_rows;
+  int32_t units;            // (token, slab) pairs, < 2^31
+  int32_t slabs;            // slabs of heads of a token
+  int32_t q_heads, heads;
+  int32_t dim, rot;
+  int32_t interleaved;
+  int32_t group_shift;
+  float eps, inv_dim;
+};
+
+// Index of the wave in the launch, the same for all its lanes (so what
+// follows from it is scalar work).
+__device__ __forceinline__ uint32_t wave_index(uint32_t block) {
+  return block * kWavesPerBlock + (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+}
+
+// What a lane keeps of a token: the rotation of its chunk.  `sin` is signed
+// for what the partner's value is multiplied with.
+struct Turn {
+  float cos[8], sin[8];
+  bool live;
+};
+
+__device__ __forceinline__ void load4(const float* p, float* f) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+
+// dir = 1 forward, -1 for the transposed rotation of the backward pass.
+__device__ __forceinline__ Turn load_turn(const QkParams& p, int64_t token, int chunk, float dir) {
+  Turn r;
+  const int64_t pos = p.positions[token];
+  r.live = pos >= 0 && pos < p.table_rows;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    r.cos[e] = 1.0f;
+    r.sin[e] = 0.0f;
+  }
+  if (r.live && 8 * chunk < p.rot) {
+    const int64_t row = pos * (p.rot / 2);
+    if (p.interleaved) {
+      float c[4], s[4];
+      load4(p.cos + row + 4 * chunk, c);
+      load4(p.sin + row + 4 * chunk, s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r.cos[2 * j] = r.cos[2 * j + 1] = c[j];
+        r.sin[2 * j] = -dir * s[j];
+        r.sin[2 * j + 1] = dir * s[j];
+      }
+    } else {
+      const int half = p.rot / 16;   // chunks of half the rotated values
+      const bool second = chunk >= half;
+      const int64_t at = row + 8 * (second ? chunk - half : chunk);
+      load4(p.cos + at, r.cos);
+      load4(p.cos + at + 4, r.cos + 4);
+      load4(p.sin + at, r.sin);
+      load4(p.sin + at + 4, r.sin + 4);
+      const float sign = second ? dir : -dir;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) r.sin[e] *= sign;
+    }
+  }
+  return r;
+}
+
+// Byte address for ds_bpermute of the lane that holds a chunk's partner.
+__device__ __forceinline__ int partner_lane(const QkParams& p, int lane, int chunk) {
+  const int half = p.rot / 16;
+  if (p.interleaved || chunk >= 2 * half) return 4 * lane;
+  return 4 * (chunk < half ? lane + half : lane - half);
+}
+
+__device__ __forceinline__ uint4 from_lane(uint4 v, int addr) {
+  return make_uint4((uint32_t)__builtin_amdgcn_ds_bpermute(addr, (int)v.x), (uint32_t)__builtin_amdgcn_ds_bpermute(addr, (int)v.y),
+                    (uint32_t)__builtin_amdgcn_ds_bpermute(addr, (int)v.z), (uint32_t)__builtin_amdgcn_ds_bpermute(addr, (int)v.w));
+}
+
+// The partner of each value of an interleaved chunk.
+__device__ __forceinline__ void swap_pairs(const float (&f)[8], float (&g)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) g[e] = f[e ^ 1];
+}
+
+__device__ __forceinline__ uint4 load_weight(const uint16_t* w, int chunk, bool on) {
+  return on ? *reinterpret_cast<const uint4*>(w + 8 * chunk) : make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint4 pick(bool key, uint4 q, uint4 k) {
+  return make_uint4(key ? k.x : q.x, key ? k.y : q.y, key ? k.z : q.z, key ? k.w : q.w);
+}
+
+template <int kLanes, int kH>
+__global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_kernel(const QkParams p) {
+  constexpr int kSet = 64 / kLanes;   // heads a wave works on at once
+  const int lane = threadIdx.x & 63, chunk = lane & (kLanes - 1), sub = lane / kLanes;
+  const bool on = 8 * chunk < p.dim;
+  const uint32_t unit = wave_index(blockIdx.x);
+  if (unit >= (uint32_t)p.units) return;
+  const uint32_t token32 = unit / (uint32_t)p.slabs;
+  const int64_t token = token32;
+  const int head0 = (int)(unit - token32 * p.slabs) * (kSet * kH) + sub;
+  uint4 raw[kH];
+#pragma unroll
+  for (int i = 0; i < kH; ++i) {
+    const int head = head0 + kSet * i;
+    raw[i] = make_uint4(0, 0, 0, 0);
+    if (on && head < p.heads)
+      raw[i] = load_stream16(head < p.q_heads ? p.q + token * p.q_stride + (int64_t)head * p.dim + 8 * chunk
+                                              : p.k + token * p.k_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk);
+  }
+  const Turn turn = load_turn(p, token, chunk, 1.0f);
+  const uint4 wq = load_weight(p.q_weight, chunk, on), wk = load_weight(p.k_weight, chunk, on);
+  const int addr = partner_lane(p, lane, chunk), lanes = 1 << (p.group_shift - 3);
+  const uint4 wq_far = from_lane(wq, addr), wk_far = from_lane(wk, addr);
+#pragma unroll
+  for (int i = 0; i < kH; ++i) {
+    const int head = head0 + kSet * i;
+    const bool key = head >= p.q_heads, ok = on && head < p.heads;
+    if (!turn.live) raw[i] = make_uint4(0, 0, 0, 0);
+    float x[8], w[8], far[8], wf[8];
+    unpack8(raw[i], x);
+    float ss = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
+    float rstd = 1.0f / sqrtf(__builtin_fmaf(lanes_sum<kLanes>(ss), p.inv_dim, p.eps));
+    if (!turn.live) rstd = 0.0f;
+    const int64_t row = token * p.heads + head;
+    if (p.codes) {
+      float scale;
+      const uint2 c = checkpoint8(raw[i], lanes, scale);
+      if (ok) {
+        const int64_t at = row * p.dim + 8 * chunk;
+        store_stream8(p.codes + at, c);
+        if ((chunk & (lanes - 1)) == 0) p.scales[at >> p.group_shift] = scale;
+      }
+    }
+    if (p.rstd && ok && chunk == 0) p.rstd[row] = rstd;
+    unpack8(pick(key, wq, wk), w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= rstd * w[e];
+    if (p.interleaved) {
+      swap_pairs(x, far);
+    } else {
+      unpack8(from_lane(raw[i], addr), far);
+      unpack8(pick(key, wq_far, wk_far), wf);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) far[e] *= rstd * wf[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(far[e], turn.sin[e], x[e] * turn.cos[e]);
+    if (ok)
+      store_stream16(key ? p.k_out + token * p.k_out_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk
+                         : p.q_out + token * p.q_out_stride + (int64_t)head * p.dim + 8 * chunk,
+                     pack8(x));
+  }
+}
+
+// Backward.  dy is the output gradient turned back by the same angle; then
+// the norm's gradient with n = code scale rstd:
+//   dn = dy w,  dx = rstd (dn - n mean(dn n)),  dw = sum over tokens and heads of dy n
+// Waves walk (token, slab) units with a stride and keep dy n of their chunk
+// in FP32 registers, queries and keys apart; a block joins its lanes' sums in
+// the LDS in a fixed order and writes one row of partial sums.
+template <int kLanes, int kH>
+__global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const QkParams p) {
+  constexpr int kSet = 64 / kLanes;
+  const int lane = threadIdx.x & 63, chunk = lane & (kLanes - 1), sub = lane / kLanes;
+  const bool on = 8 * chunk < p.dim;
+  const uint4 wq = load_weight(p.q_weight, chunk, on), wk = load_weight(p.k_weight, chunk, on);
+  const int addr = partner_lane(p, lane, chunk);
+  float dwq[8], dwk[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.0f;
+  const uint32_t step = gridDim.x * kWavesPerBlock;
+  for (uint32_t unit = wave_index(blockIdx.x); unit < (uint32_t)p.units; unit += step) {
+    const uint32_t token32 = unit / (uint32_t)p.slabs;
+    const int64_t token = token32;
+    const int head0 = (int)(unit - token32 * p.slabs) * (kSet * kH) + sub;
+    uint4 raw[kH];
+    uint2 code[kH];
+    float scale[kH], rs[kH];
+#pragma unroll
+    for (int i = 0; i < kH; ++i) {
+      const int head = head0 + kSet * i;
+      raw[i] = make_uint4(0, 0, 0, 0);
+      code[i] = make_uint2(0, 0);
+      scale[i] = rs[i] = 0.0f;
+      if (on && head < p.heads) {
+        const int64_t row = token * p.heads + head, at = row * p.dim + 8 * chunk;
+        raw[i] = load_stream16(head < p.q_heads ? p.q + token * p.q_stride + (int64_t)head * p.dim + 8 * chunk
+                                                : p.k + token * p.k_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk);
+        code[i] = load_stream8(p.codes + at);
+        scale[i] = p.scales[at >> p.group_shift];
+        rs[i] = p.rstd[row];
+      }
+    }
+    const Turn turn = load_turn(p, token, chunk, -1.0f);
+#pragma unroll
+    for (int i = 0; i < kH; ++i) {
+      const int head = head0 + kSet * i;
+      const bool key = head >= p.q_heads, ok = on && head < p.heads;
+      float d[8], far[8], n[8], w[8];
+      if (!turn.live) {   // padding: nothing of it counts, whatever its buffers hold
+        raw[i] = make_uint4(0, 0, 0, 0);
+        code[i] = make_uint2(0, 0);
+        scale[i] = rs[i] = 0.0f;
+      }
+      unpack8(raw[i], d);
+      if (p.interleaved)
+        swap_pairs(d, far);
+      else
+        unpack8(from_lane(raw[i], addr), far);
+      e4m3_values8(code[i], n);
+      unpack8(pick(key, wq, wk), w);
+      float dot = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        d[e] = __builtin_fmaf(far[e], turn.sin[e], d[e] * turn.cos[e]);
+        n[e] = n[e] * scale[i] * rs[i];
+        const float g = d[e] * n[e];
+        dwq[e] += key ? 0.0f : g;
+        dwk[e] += key ? g : 0.0f;
+        d[e] *= w[e];
+        dot = __builtin_fmaf(d[e], n[e], dot);
+      }
+      const float mean = lanes_sum<kLanes>(dot) * p.inv_dim;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = rs[i] * __builtin_fmaf(-n[e], mean, d[e]);
+      if (ok)
+        store_stream16(key ? p.k_out + token * p.k_out_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk
+                           : p.q_out + token * p.q_out_stride + (int64_t)head * p.dim + 8 * chunk,
+                       pack8(d));
+    }
+  }
+  if (p.partials) {
+    // [wave and set of heads][2 D]: the block's rows, added column by column
+    constexpr int kRows = kWavesPerBlock * kSet;
+    __shared__ float sums[kRows][2 * 8 * kLanes + 4];
+    const int r = (threadIdx.x >> 6) * kSet + sub;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      sums[r][8 * chunk + e] = dwq[e];
+      sums[r][8 * kLanes + 8 * chunk + e] = dwk[e];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.dim; c += kBlockThreads) {
+      const int at = c < p.dim ? c : 8 * kLanes + c - p.dim;
+      float v = sums[0][at];
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) v += sums[i][at];
+      p.partials[(int64_t)blockIdx.x * 2 * p.dim + c] = v;
+    }
+  }
+}
+
+constexpr int64_t kMaxHeads = 1 << 16;
+constexpr int64_t kMaxDim = 256;
+
+// Rows of partial sums of the backward pass, a constant for the reasons of
+// the norm's.
+constexpr int64_t kQkParts = 1024;
+
+int lanes_for(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
+
+// Sets of heads a wave takes: 4, or 1 where slabs of 4 sets would give fewer
+// waves than the chip holds at four per SIMD.
+struct QkSplit {
+  int sets;
+  int32_t slabs;
+  int64_t units;   // at most kMaxUnits
+};
+
+constexpr int64_t kMaxUnits = 0x7FFFFFFF - kWavesPerBlock * 65536;   // unit + step stays below 2^32
+
+QkSplit split_heads(int64_t tokens, int64_t heads, int64_t dim) {
+  const int64_t set = 64 / lanes_for(dim);
+  int sets = 4;
+  int64_t slabs = (heads + set * sets - 1) / (set * sets);
+  if (tokens * slabs < 4096) {
+    sets = 1;
+    slabs = (heads + set - 1) / set;
+  }
+  return {sets, (int32_t)slabs, tokens * slabs};
+}
+
+bool units_ok(int64_t tokens, int64_t heads, int64_t dim) {
+  return tokens <= kMaxUnits && split_heads(tokens, heads, dim).units <= kMaxUnits;
+}
+
+int64_t qk_parts(int64_t units) {
+  const int64_t blocks = (units + kWavesPerBlock - 1) / kWavesPerBlock;
+  return blocks < kQkParts ? blocks : kQkParts;
+}
+
+const void* qk_kernel_for(int lanes, int sets, bool backward) {
+#define COAT_QK(L, H)                                                                 \
+  if (lanes == L && sets == H)                                                        \
+    return backward ? reinterpret_cast<const void*>(&qk_norm_rope_bwd_kernel<L, H>)   \
+                    : reinterpret_cast<const void*>(&qk_norm_rope_kernel<L, H>);
+  COAT_QK(8, 1)
+  COAT_QK(8, 4)
+  COAT_QK(16, 1)
+  COAT_QK(16, 4)
+  COAT_QK(32, 1)
+  COAT_QK(32, 4)
+#undef COAT_QK
+  return nullptr;
+}
+
+bool bad_stride(int64_t stride, int64_t heads, int64_t dim, int64_t tokens) {
+  return stride % 8 != 0 || (tokens > 1 && stride < heads * dim) || stride > (INT64_MAX / 4) / (tokens > 0 ? tokens : 1);
+}
+
+coat_status_t check_qk(const coat_qk_shape_t& s) {
+  if (s.tokens < 0 || s.q_heads < 0 || s.k_heads < 0 || s.q_heads > kMaxHeads || s.k_heads > kMaxHeads ||
+      s.table_rows < 0)
+    return COAT_ERR_INVALID_VALUE;
+  if (!valid_group_size(s.group_size)) return COAT_ERR_GROUP_SIZE;
+  if (s.head_dim < 16 || s.head_dim > kMaxDim || s.head_dim % 16 != 0 || s.head_dim % s.group_size != 0)
+    return COAT_ERR_INVALID_VALUE;
+  if (s.rot_dim < 16 || s.rot_dim > s.head_dim || s.rot_dim % 16 != 0) return COAT_ERR_INVALID_VALUE;
+  if (s.table_rows > INT64_MAX / 4 / s.head_dim) return COAT_ERR_INVALID_VALUE;
+  if (!units_ok(s.tokens, s.q_heads + s.k_heads, s.head_dim)) return COAT_ERR_INVALID_VALUE;
+  return COAT_OK;
+}
+
+void fill(QkParams& p, const coat_qk_shape_t& s, const QkSplit& split) {
+  memset(&p, 0, sizeof(p));
+  p.tokens = s.tokens;
+  p.table_rows = s.table_rows;
+  p.units = (int32_t)split.units;
+  p.slabs = split.slabs;
+  p.q_heads = s.q_heads;
+  p.heads = s.q_heads + s.k_heads;
+  p.dim = s.head_dim;
+  p.rot = s.rot_dim;
+  p.interleaved = s.interleaved != 0;
+  p.group_shift = __builtin_ctz((unsigned)s.group_size);
+  p.inv_dim = (float)(1.0 / (double)s.head_dim);
+}
+
+}  // namespace
+
+extern "C" {
+
+coat_status_t coat_fp8_qk_norm_rope(const coat_qk_norm_rope_args_t* a, hipStream_t stream) {
+  if (!a) return COAT_ERR_NULL_POINTER;
+  const coat_qk_shape_t& s = a->shape;
+  const coat_status_t st = check_qk(s);
+  if (st != COAT_OK) return st;
+  if (!isfinite(a->eps) || a->eps <= 0.0f) return COAT_ERR_INVALID_VALUE;
+  if (bad_stride(a->q_stride, s.q_heads, s.head_dim, s.tokens) ||
+      bad_stride(a->k_stride, s.k_heads, s.head_dim, s.tokens) ||
+      bad_stride(a->q_out_stride, s.q_heads, s.head_dim, s.tokens) ||
+      bad_stride(a->k_out_stride, s.k_heads, s.head_dim, s.tokens))
+    return COAT_ERR_INVALID_VALUE;
+  if (s.tokens == 0 || s.q_heads + s.k_heads == 0) return COAT_OK;
+  if ((s.q_heads && (!a->q || !a->q_out)) || (s.k_heads && (!a->k || !a->k_out)) || !a->q_weight || !a->k_weight ||
+      !a->positions || (s.table_rows && (!a->cos || !a->sin)) || !a->codes != !a->scales)
+    return COAT_ERR_NULL_POINTER;
+  if (!aligned(a->q, 16) || !aligned(a->k, 16) || !aligned(a->q_out, 16) || !aligned(a->k_out, 16) ||
+      !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16) || !aligned(a->cos, 16) || !aligned(a->sin, 16) ||
+      !aligned(a->positions, 8) || !aligned(a->codes, 16) || !aligned(a->scales, 4) || !aligned(a->rstd, 4))
+    return COAT_ERR_MISALIGNED;
+  const QkSplit split = split_heads(s.tokens, s.q_heads + s.k_heads, s.head_dim);
+  const int64_t blocks = (split.units + kWavesPerBlock - 1) / kWavesPerBlock;
+  QkParams p;
+  fill(p, s, split);
+  p.q = a->q;
+  p.k = a->k;
+  p.q_stride = a->q_stride;
+  p.k_stride = a->k_stride;
+  p.q_out = a->q_out;
+  p.k_out = a->k_out;
+  p.q_out_stride = a->q_out_stride;
+  p.k_out_stride = a->k_out_stride;
+  p.q_weight = a->q_weight;
+  p.k_weight = a->k_weight;
+  p.cos = a->cos;
+  p.sin = a->sin;
+  p.positions = a->positions;
+  p.codes = a->codes;
+  p.scales = a->scales;
+  p.rstd = a->rstd;
+  p.eps = a->eps;
+  void* args[] = {&p};
+  const hipError_t e = hipLaunchKernel(qk_kernel_for(lanes_for(s.head_dim), split.sets, false), dim3((unsigned)blocks),
+                                       dim3(kBlockThreads), args, 0, stream);
+  return e == hipSuccess ? COAT_OK : hip_fail(e);
+}
+
+int64_t coat_fp8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads, int64_t head_dim) {
+  if (tokens < 0 || heads < 0 || heads > 2 * kMaxHeads || head_dim < 16 || head_dim > kMaxDim || head_dim % 16 != 0 ||
+      !units_ok(tokens, heads, head_dim))
+    return -1;
+  return qk_parts(split_heads(tokens, heads, head_dim).units) * 2 * head_dim * (int64_t)sizeof(float);
+}
+
+coat_status_t coat_fp8_qk_norm_rope_bwd(const coat_qk_norm_rope_bwd_args_t* a, hipStream_t stream) {
+  if (!a) return COAT_ERR_NULL_POINTER;
+  const coat_qk_shape_t& s = a->shape;
+  const coat_status_t st = check_qk(s);
+  if (st != COAT_OK) return st;
+  if (bad_stride(a->dq_out_stride, s.q_heads, s.head_dim, s.tokens) ||
+      bad_stride(a->dk_out_stride, s.k_heads, s.head_dim, s.tokens) ||
+      bad_stride(a->dq_stride, s.q_heads, s.head_dim, s.tokens) ||
+      bad_stride(a->dk_stride, s.k_heads, s.head_dim, s.tokens))
+    return COAT_ERR_INVALID_VALUE;
+  if (!a->dq_weight != !a->dk_weight) return COAT_ERR_NULL_POINTER;
+  const bool dw = a->dq_weight != nullptr, work = s.tokens > 0 && s.q_heads + s.k_heads > 0;
+  if (!work && (!dw || a->accumulate)) return COAT_OK;
+  if (work && ((s.q_heads && (!a->dq_out || !a->dq)) || (s.k_heads && (!a->dk_out || !a->dk)) || !a->codes ||
+               !a->scales || !a->rstd || !a->q_weight || !a->k_weight || !a->positions ||
+               (s.table_rows && (!a->cos || !a->sin)) || (dw && !a->workspace)))
+    return COAT_ERR_NULL_POINTER;
+  if (!aligned(a->dq_out, 16) || !aligned(a->dk_out, 16) || !aligned(a->codes, 16) || !aligned(a->scales, 4) ||
+      !aligned(a->rstd, 4) || !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16) || !aligned(a->cos, 16) ||
+      !aligned(a->sin, 16) || !aligned(a->positions, 8) || !aligned(a->dq, 16) || !aligned(a->dk, 16) ||
+      !aligned(a->dq_weight, 4) || !aligned(a->dk_weight, 4) || !aligned(a->workspace, 16))
+    return COAT_ERR_MISALIGNED;
+  if (work && dw &&
+      a->workspace_bytes < coat_fp8_qk_norm_rope_bwd_workspace(s.tokens, s.q_heads + s.k_heads, s.head_dim))
+    return COAT_ERR_INVALID_VALUE;
+  const QkSplit split = split_heads(s.tokens, s.q_heads + s.k_heads, s.head_dim);
+  const int64_t blocks = work ? qk_parts(split.units) : 0;
+  hipError_t e = hipSuccess;
+  if (work) {
+    QkParams p;
+    fill(p, s, split);
+    p.q = a->dq_out;
+    p.k = a->dk_out;
+    p.q_stride = a->dq_out_stride;
+    p.k_stride = a->dk_out_stride;
+    p.q_out = a->dq;
+    p.k_out = a->dk;
+    p.q_out_stride = a->dq_stride;
+    p.k_out_stride = a->dk_stride;
+    p.q_weight = a->q_weight;
+    p.k_weight = a->k_weight;
+    p.cos = a->cos;
+    p.sin = a->sin;
+    p.positions = a->positions;
+    p.codes = const_cast<uint8_t*>(a->codes);
+    p.scales = const_cast<float*>(a->scales);
+    p.rstd = const_cast<float*>(a->rstd);
+    p.partials = dw ? (float*)a->workspace : nullptr;
+    void* args[] = {&p};
+    e = hipLaunchKernel(qk_kernel_for(lanes_for(s.head_dim), split.sets, true), dim3((unsigned)blocks),
+                        dim3(kBlockThreads), args, 0, stream);
+  }
+  if (e == hipSuccess && dw)
+    e = launch_sum_partials((const float*)a->workspace, (int)blocks, 2 * s.head_dim, a->dq_weight, s.head_dim,
+                            a->dk_weight, a->accumulate != 0, stream);
+  return e == hipSuccess ? COAT_OK : hip_fail(e);
+}
+
+}  // extern "C"

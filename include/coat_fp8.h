@@ -224,6 +224,225 @@ coat_status_t coat_fp8_gemm_bf16(const uint8_t* a, const uint8_t* b,
                                  int64_t N, int64_t K, uint16_t* c_bf16,
                                  hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Activation checkpoints: the operators between the linear layers, which keep
+ * what their backward pass needs as E4M3 codes and read it there again ([P1]
+ * section 三, 混合粒度激活量化: per 1xG group for non-linear layers, one scale
+ * per tensor in front of linear layers).
+ *
+ * A checkpoint of a rows x cols matrix is what coat_fp8_quantize_act and
+ * coat_fp8_gemm_group_quant write: codes rows x cols, scales
+ * rows x (cols / group_size) with S = max|x| / 448, and stands for code * S.
+ * Codes "under one scale" s stand for code * s; a value v is stored as the
+ * E4M3 rounding of v * fl(1/s), saturating at +-448.  BF16 outputs and
+ * gradients are rounded once, to nearest even, from FP32.
+ *
+ * The rules at the top hold, with these additions:
+ *   - Optional arrays may be NULL.  Rows are contiguous except where a stride
+ *     is an argument.
+ *   - *_amax, if given, is raised to the largest magnitude (before the scale)
+ *     of the FP32 values that were rounded to codes; it must hold a
+ *     non-negative value before (0 to start a new maximum).  A NaN is not
+ *     counted (its code is NaN).
+ *   - Gradients of weights are FP32 and sums over rows in a fixed order.
+ *     accumulate != 0 adds them to what the array holds, else they overwrite
+ *     it.  A weight gradient pointer may be NULL (a frozen weight).
+ *   - workspace: device memory of at least the bytes that the *_workspace
+ *     function gives for the same sizes, 16-byte aligned, its content neither
+ *     read before it is written nor of use afterwards.  Calls, or replays of
+ *     captured graphs, that share one must not overlap.
+ *   - A NaN or infinity reaches no output outside its row (qk: its head,
+ *     swiglu: its value) except the weight gradients; the scale of its group
+ *     in a checkpoint is not finite.
+ */
+
+/*
+ * RMS norm of a residual stream with a checkpoint of its input:
+ *   h = bf16(x + residual), or x without a residual,
+ *   rstd = (mean(h^2) + eps)^-1/2,  y = h * rstd * weight.
+ * cols is a multiple of group_size, at most 32768; squares are summed in FP32.
+ * Errors: NULL_POINTER (args, x, weight; neither y nor y_codes; residual
+ * without residual_out or codes without scales, or the reverse),
+ * INVALID_VALUE (sizes; eps not finite or <= 0; with y_codes, y_scale not
+ * positive and finite or its reciprocal infinite; y_amax without y_codes),
+ * GROUP_SIZE, MISALIGNED (16 bytes; scales, rstd and y_amax 4), HIP.
+ */
+typedef struct coat_rms_norm_args {
+  const uint16_t* x;         /* rows x cols BF16                             */
+  const uint16_t* residual;  /* rows x cols BF16, or NULL                    */
+  const uint16_t* weight;    /* cols BF16                                    */
+  uint16_t* residual_out;    /* h (written), with residual                   */
+  uint16_t* y;               /* BF16 y (written), or NULL                    */
+  uint8_t* y_codes;          /* y under one scale (written), or NULL         */
+  float* y_amax;             /* optional, see above                          */
+  uint8_t* codes;            /* checkpoint of h (written), or NULL           */
+  float* scales;
+  float* rstd;               /* rows FP32 (written), or NULL                 */
+  int64_t rows, cols;
+  float eps, y_scale;
+  int32_t group_size;
+} coat_rms_norm_args_t;
+
+coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* args,
+                                hipStream_t stream);
+
+/*
+ * Its gradient, with n = code * S * rstd and dn = dy * weight:
+ *   dx = rstd * (dn - n * mean(dn * n)) (+ d_residual),
+ *   dw = sum over rows of dy * n.
+ * d_residual is the gradient that reaches residual_out from elsewhere; dx is
+ * then the gradient of both x and residual.
+ * Errors: as above (codes, scales and rstd are required; workspace with dw;
+ * INVALID_VALUE for a workspace that is too small).
+ */
+typedef struct coat_rms_norm_bwd_args {
+  const uint16_t* dy;          /* rows x cols BF16                           */
+  const uint8_t* codes;        /* the checkpoint                             */
+  const float* scales;
+  const float* rstd;
+  const uint16_t* weight;
+  const uint16_t* d_residual;  /* rows x cols BF16, or NULL                  */
+  uint16_t* dx;                /* rows x cols BF16 (written)                 */
+  float* dw;                   /* cols FP32, or NULL                         */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t rows, cols;
+  int32_t group_size, accumulate;
+} coat_rms_norm_bwd_args_t;
+
+coat_status_t coat_fp8_rms_norm_bwd(const coat_rms_norm_bwd_args_t* args,
+                                    hipStream_t stream);
+
+/* Bytes of workspace for that call, or -1 for sizes it refuses. */
+int64_t coat_fp8_rms_norm_bwd_workspace(int64_t rows, int64_t cols);
+
+/*
+ * Gated activation h = gate * sigmoid(gate) * up.  A row of 2 * cols values
+ * holds the gates, then the ups, as the packed projection leaves it.
+ * Without gate_up the input is the checkpoint codes, scales (read), for
+ * instance the output of coat_fp8_gemm_group_quant; with gate_up it is BF16,
+ * and codes, scales, if given, are written as its checkpoint.
+ * Exactly one of h and h_codes is given.  A sigmoid below 2^-126 is 0.
+ * Errors: NULL_POINTER (args; no output; no input; codes without scales or
+ * the reverse), INVALID_VALUE (sizes, cols not a multiple of group_size or
+ * over 2^30, both outputs, h_scale as y_scale above, h_amax without h_codes),
+ * GROUP_SIZE, MISALIGNED (16 bytes; scales and h_amax 4), HIP.
+ */
+typedef struct coat_swiglu_args {
+  const uint16_t* gate_up;  /* rows x 2 cols BF16, or NULL                   */
+  uint8_t* codes;           /* rows x 2 cols: the input, or the checkpoint   */
+  float* scales;
+  uint16_t* h;              /* rows x cols BF16 (written), or NULL           */
+  uint8_t* h_codes;         /* h under one scale (written), or NULL          */
+  float* h_amax;            /* optional, see above                           */
+  int64_t rows, cols;
+  float h_scale;
+  int32_t group_size;
+} coat_swiglu_args_t;
+
+coat_status_t coat_fp8_swiglu(const coat_swiglu_args_t* args,
+                              hipStream_t stream);
+
+/*
+ * Its gradient, with gate and up the checkpoint's values and s = sigmoid(gate):
+ *   d_gate = dh * up * s * (1 + gate * (1 - s)),  d_up = dh * gate * s.
+ * dh rows x cols BF16; d_gate_up rows x 2 cols BF16 (written), gates first.
+ * Errors: as above.
+ */
+coat_status_t coat_fp8_swiglu_bwd(const uint16_t* dh, const uint8_t* codes,
+                                  const float* scales, int64_t rows,
+                                  int64_t cols, int32_t group_size,
+                                  uint16_t* d_gate_up, hipStream_t stream);
+
+/* Sizes that the two calls below share. */
+typedef struct coat_qk_shape {
+  int64_t tokens, table_rows;  /* table_rows: rows of cos and sin            */
+  int32_t q_heads, k_heads;    /* each 0 to 65536                            */
+  int32_t head_dim;            /* multiple of 16 and group_size, 16 to 256   */
+  int32_t rot_dim;             /* rotated values: multiple of 16, <= head_dim */
+  int32_t interleaved;         /* pairs (2j, 2j+1), else (j, j + rot_dim/2)  */
+  int32_t group_size;
+} coat_qk_shape_t;
+
+/*
+ * RMS norm of every query and key head and the position rotation:
+ *   rstd = (mean over the head of x^2 + eps)^-1/2,  y = x * rstd * weight,
+ * then pair j (a, b) of the first rot_dim values of y becomes
+ *   (a cos_j - b sin_j, b cos_j + a sin_j),  cos and sin: row positions[token]
+ * of the tables (table_rows x rot_dim/2 FP32).  The heads of a token are
+ * contiguous (head h at h * head_dim); a stride counts the values from one
+ * token to the next, so queries and keys may be parts of one packed
+ * projection.  q_out may be q and k_out k, with equal strides.
+ * The checkpoint and rstd hold the query heads of a token, then its key
+ * heads: codes tokens x (q_heads + k_heads) x head_dim, scales
+ * tokens x heads x head_dim / group_size, rstd tokens x heads.
+ * A token whose position lies outside [0, table_rows) is padding: its
+ * outputs, codes, scales and rstd are written as zero.
+ * Errors: NULL_POINTER, INVALID_VALUE (sizes as above, a stride below a
+ * token's values or not a multiple of 8, eps as above), GROUP_SIZE,
+ * MISALIGNED (16 bytes; positions 8, scales and rstd 4), HIP.
+ */
+typedef struct coat_qk_norm_rope_args {
+  coat_qk_shape_t shape;
+  const uint16_t* q;        /* BF16 heads                                    */
+  const uint16_t* k;
+  int64_t q_stride, k_stride;
+  const uint16_t* q_weight; /* head_dim BF16                                 */
+  const uint16_t* k_weight;
+  const float* cos;
+  const float* sin;
+  const int64_t* positions; /* tokens                                        */
+  uint16_t* q_out;          /* BF16 heads (written)                          */
+  uint16_t* k_out;
+  int64_t q_out_stride, k_out_stride;
+  uint8_t* codes;           /* checkpoint (written), or NULL                 */
+  float* scales;
+  float* rstd;              /* (written), or NULL                            */
+  float eps;
+} coat_qk_norm_rope_args_t;
+
+coat_status_t coat_fp8_qk_norm_rope(const coat_qk_norm_rope_args_t* args,
+                                    hipStream_t stream);
+
+/*
+ * Its gradient from the checkpoint: dy is d*_out rotated by minus the angle,
+ * then as coat_fp8_rms_norm_bwd head by head; dq_weight and dk_weight sum
+ * over tokens and heads.  Padding tokens get zero gradients and add nothing,
+ * whatever their buffers hold.  dq may be dq_out and dk dk_out, with equal
+ * strides.  Errors: as above (codes, scales and rstd are required; dq_weight
+ * and dk_weight both or neither; workspace as above).
+ */
+typedef struct coat_qk_norm_rope_bwd_args {
+  coat_qk_shape_t shape;
+  const uint16_t* dq_out;   /* BF16 heads                                    */
+  const uint16_t* dk_out;
+  int64_t dq_out_stride, dk_out_stride;
+  const uint8_t* codes;     /* the checkpoint                                */
+  const float* scales;
+  const float* rstd;
+  const uint16_t* q_weight;
+  const uint16_t* k_weight;
+  const float* cos;
+  const float* sin;
+  const int64_t* positions;
+  uint16_t* dq;             /* BF16 heads (written)                          */
+  uint16_t* dk;
+  int64_t dq_stride, dk_stride;
+  float* dq_weight;         /* head_dim FP32, or NULL                        */
+  float* dk_weight;
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t accumulate;
+} coat_qk_norm_rope_bwd_args_t;
+
+coat_status_t coat_fp8_qk_norm_rope_bwd(const coat_qk_norm_rope_bwd_args_t* args,
+                                        hipStream_t stream);
+
+/* Bytes of workspace for that call (heads: queries and keys), or -1. */
+int64_t coat_fp8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads,
+                                            int64_t head_dim);
+
 /* Static, NUL-terminated description of a status code. */
 const char* coat_status_string(coat_status_t status);
 
