@@ -12,7 +12,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("coat_fp8.hip", "coat_act.hip", "coat_gemm.hip",
-                                                    "coat_norm.hip", "coat_swiglu.hip", "coat_qk.hip")]
+                                                    "coat_norm.hip", "coat_swiglu.hip", "coat_qk.hip",
+                                                    "coat_wgrad.hip")]
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libcoat_fp8.so")
 BENCH_SOURCES = [os.path.join(HERE, "csrc", f) for f in ("coat_mix_ceiling.hip", "coat_stream_ceiling.hip")]

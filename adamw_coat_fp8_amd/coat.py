@@ -38,6 +38,7 @@ EXPORTED_SYMBOLS = (
     "coat_fp8_rms_norm", "coat_fp8_rms_norm_bwd", "coat_fp8_rms_norm_bwd_workspace",
     "coat_fp8_swiglu", "coat_fp8_swiglu_bwd", "coat_fp8_qk_norm_rope",
     "coat_fp8_qk_norm_rope_bwd", "coat_fp8_qk_norm_rope_bwd_workspace",
+    "coat_fp8_weight_grad", "coat_fp8_weight_grad_workspace",
 )
 
 
@@ -107,6 +108,11 @@ class QkNormRopeBwdArgs(ctypes.Structure):
         "workspace, i64: workspace_bytes, i32: accumulate")
 
 
+class WeightGradArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: dy x_codes x_scales dw_bf16 dw_f32 workspace, i64: workspace_bytes M N K, "
+                       "f32: x_scale, i32: group_size accumulate")
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -133,7 +139,7 @@ def _load(path: str = LIB_PATH):
     lib.coat_fp8_gemm_bf16.argtypes = [vp, vp, f32, f32, i64, i64, i64, vp, vp]
     for name, args in (("rms_norm", RMSNormArgs), ("rms_norm_bwd", RMSNormBwdArgs),
                        ("swiglu", SwigluArgs), ("qk_norm_rope", QkNormRopeArgs),
-                       ("qk_norm_rope_bwd", QkNormRopeBwdArgs)):
+                       ("qk_norm_rope_bwd", QkNormRopeBwdArgs), ("weight_grad", WeightGradArgs)):
         fn = getattr(lib, f"coat_fp8_{name}")
         fn.restype = ctypes.c_int
         fn.argtypes = [ctypes.POINTER(args), vp]
@@ -143,6 +149,8 @@ def _load(path: str = LIB_PATH):
     lib.coat_fp8_rms_norm_bwd_workspace.argtypes = [i64, i64]
     lib.coat_fp8_qk_norm_rope_bwd_workspace.restype = i64
     lib.coat_fp8_qk_norm_rope_bwd_workspace.argtypes = [i64, i64, i64]
+    lib.coat_fp8_weight_grad_workspace.restype = i64
+    lib.coat_fp8_weight_grad_workspace.argtypes = [i64, i64, i64]
     lib.coat_status_string.restype = ctypes.c_char_p
     lib.coat_status_string.argtypes = [ctypes.c_int]
     lib.coat_last_hip_error.restype = ctypes.c_char_p
@@ -645,3 +653,36 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, codes: torch.Te
                           _ptr(positions), _ptr(dq), _ptr(dk), dq_stride, dk_stride, _ptr(dq_weight),
                           _ptr(dk_weight), ws, ws_bytes, int(accumulate))
     _check(lib.coat_fp8_qk_norm_rope_bwd(ctypes.byref(a), _stream(stream)))
+
+
+def weight_grad_workspace(rows: int, n: int, k: int) -> int:
+    """Bytes of workspace weight_grad needs (0: none)."""
+    return _workspace_bytes(lib.coat_fp8_weight_grad_workspace(rows, n, k))
+
+
+def weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales, dw: torch.Tensor, *,
+                accumulate: bool = False, workspace: Optional[torch.Tensor] = None,
+                group_size: int = 128, stream=None):
+    """dw = dy^T X for a linear layer whose input X (rows x K) was kept as E4M3
+    codes: with group scales (a float32 tensor, rows x K/group_size) or under
+    one scale (a number).  dy is rows x N BF16, dw N x K BF16 or float32; a
+    float32 dw can be accumulated into.  Needs weight_grad_workspace bytes."""
+    rows, n = _shape2(dy, "dy")
+    x_rows, k = _shape2(codes, "codes")
+    if x_rows != rows:
+        raise ValueError("dy and codes disagree on the rows")
+    grouped = isinstance(scales, torch.Tensor)
+    _need(dy, "dy", BF16_DTYPES, 0)
+    _need(codes, "codes", CODE_DTYPES, 0)
+    if grouped:
+        _need(scales, "scales", F32_DTYPES, rows * _groups(k, group_size))
+    elif not isinstance(scales, (int, float)):
+        raise ValueError("scales must be a float32 tensor or a number")
+    _need(dw, "dw", BF16_DTYPES + F32_DTYPES, n * k)
+    ws, ws_bytes = _workspace(workspace, True, weight_grad_workspace(rows, n, k))
+    _on_device(dy=dy, codes=codes, scales=scales if grouped else None, dw=dw, workspace=workspace)
+    f32 = dw.dtype == torch.float32
+    a = WeightGradArgs(_ptr(dy), _ptr(codes), _ptr(scales) if grouped else None, None if f32 else _ptr(dw),
+                       _ptr(dw) if f32 else None, ws, ws_bytes, rows, n, k, 1.0 if grouped else scales,
+                       group_size, int(accumulate))
+    _check(lib.coat_fp8_weight_grad(ctypes.byref(a), _stream(stream)))

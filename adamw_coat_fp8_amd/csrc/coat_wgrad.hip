@@ -1,0 +1,480 @@
+// coat_wgrad.hip -- gfx950 weight gradient of a linear layer whose input was
+// kept in E4M3, and its C ABI.
+//
+// Sources (see include/coat_fp8.h for the full citations):
+//   [P1] COAT paper review (xllm-io.github.io), section 三: linear layers keep
+//        their input in E4M3 (混合粒度激活量化) and the backward pass computes
+//        the weight gradient from it.
+
+#include <hip/hip_runtime.h>
+
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "coat_elem.h"
+
+using namespace coat;
+
+namespace {
+
+// dW[n][k] = sum over rows m of dy[m][n] x[m][k],  x[m][k] = code[m][k] S
+//
+// A product whose contracted axis is the slow one of both operands: the MFMA
+// wants eight consecutive m of one column in a lane.  Both panels go from
+// global memory straight into the LDS as they lie (dy in BF16, x as codes),
+// and the LDS's transposing reads (16-bit for dy, 8-bit for the codes) hand
+// each lane its column.  The codes become BF16 in registers, on the way into
+// the MFMA: under one scale their values are exact in BF16 and the scale
+// multiplies the FP32 result; with group scales, which change along m, the
+// product code * S is rounded to BF16 (2^-9 of a value that E4M3 had already
+// rounded by up to 2^-4).  Sums are FP32 in the matrix cores.
+//
+// A block computes a kBN x kBK tile of dW; kWN x kWK waves own kJ x kI tiles
+// of 32 x 32.  64 rows a step, three LDS stages: the loads of step t + 2 go
+// out behind the barrier of step t, so each has two steps to arrive, and one
+// barrier a step is enough.
+
+constexpr int kStep = 64;   // rows per pipeline step
+
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+enum Out { kBF16 = 0, kF32 = 1, kF32Add = 2, kPartial = 3 };
+
+struct WgradParams {
+  const uint16_t* dy;
+  const uint8_t* codes;
+  const float* scales;   // rows x K/G, or NULL: `scale` for all
+  void* dw;              // N x K, or the partial sums (splits x N x K)
+  int64_t M, N, K;
+  int64_t groups;        // K / G
+  int32_t n_tiles, k_tiles;
+  int32_t steps;         // steps of all rows, ceil(M / 64)
+  int32_t splits;
+  int32_t out;
+  float scale;
+};
+
+template <int kWN, int kWK, int kJ, int kI>
+struct Tile {
+  static constexpr int kWaves = kWN * kWK, kThreads = 64 * kWaves;
+  static constexpr int kBN = 32 * kWN * kJ, kBK = 32 * kWK * kI;
+  static constexpr int kA = kStep * kBN * 2, kB = kStep * kBK;   // bytes of a stage's panels
+  static constexpr int kLA = kA / 1024 / kWaves, kLB = kB / 1024 / kWaves;
+};
+
+// A dy row holds kBN values; its 64-byte chunks are XORed with m % 4, so that
+// a transposing read's 4 rows x 64 bytes (32 lanes) meet all 64 banks once.
+// (Rows are a multiple of 256 bytes.)
+__device__ __forceinline__ int dy_chunk(int m, int c64) { return c64 ^ (m & 3); }
+
+// A code row holds kBK bytes, 256 or 128; an 8-bit read's 8 rows x 32 bytes
+// meet all banks once when the 32-byte chunks are XORed with m % 8, or for
+// 128-byte rows, two to a sweep of the banks, with (m / 2) % 4.
+template <int kBK>
+__device__ __forceinline__ int code_chunk(int m, int c32) {
+  return kBK == 256 ? c32 ^ (m & 7) : c32 ^ ((m >> 1) & 3);
+}
+
+template <class T, int G>
+struct Stage {
+  static constexpr int kGroups = G ? T::kBK / G : 0;                             // of a tile's row
+  static constexpr int kLS = G ? (kGroups + T::kWaves - 1) / T::kWaves : 0;      // scale loads of a wave
+  static constexpr int kSlots = kLS * T::kWaves;
+};
+
+// LDS arrays of the three stages.  They are distinct objects: the compiler can
+// tell the loads into one stage from the reads of another and need not wait
+// for loads in flight.
+template <int kBytes, int kWhich>
+__device__ __forceinline__ uint8_t* lds_array() {
+  __shared__ __attribute__((aligned(1024))) uint8_t bytes[kBytes];
+  return bytes;
+}
+
+// Issues the loads of a step into stage kSt.
+template <class T, int G, int kSt>
+__device__ __forceinline__ void load_step(const WgradParams& p, int step, int wave, int lane, int64_t k0,
+                                          const int (&a_row)[T::kLA], const uint32_t (&a_col)[T::kLA],
+                                          const int (&b_row)[T::kLB], const uint32_t (&b_col)[T::kLB]) {
+  using S = Stage<T, G>;
+  const int64_t m0 = (int64_t)step * kStep;
+  const int last = (int)(p.M - m0 < kStep ? p.M - m0 : kStep) - 1;
+  const uint32_t a_stride = 2u * (uint32_t)p.N, b_stride = (uint32_t)p.K;
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(p.dy + m0 * p.N), (short)0, (int)0xFFFFFFFF, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rb =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + m0 * p.K), (short)0, (int)0xFFFFFFFF, 0x00020000);
+  uint8_t* a = lds_array<T::kA, kSt>();
+  uint8_t* b = lds_array<T::kB, 3 + kSt>();
+#pragma unroll
+  for (int i = 0; i < T::kLA; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, a + 1024 * (T::kLA * wave + i), 16,
+                                             (int)((uint32_t)min(a_row[i], last) * a_stride + a_col[i]), 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < T::kLB; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, b + 1024 * (T::kLB * wave + i), 16,
+                                             (int)((uint32_t)min(b_row[i], last) * b_stride + b_col[i]), 0, 0, 0);
+  if constexpr (G != 0) {
+    // slot g holds the scales of group g for the step's 64 rows (slots past
+    // the tile's groups repeat them: every wave issues as many loads)
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales + m0 * p.groups), (short)0, (int)0xFFFFFFFF, 0x00020000);
+    uint8_t* sc = lds_array<256 * S::kSlots, 6 + kSt>();
+#pragma unroll
+    for (int i = 0; i < S::kLS; ++i) {
+      const int slot = S::kLS * wave + i;
+      const int64_t g = k0 / G + slot % S::kGroups;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, sc + 256 * slot, 4,
+          (int)(4u * ((uint32_t)min(lane, last) * (uint32_t)p.groups + (uint32_t)(g < p.groups ? g : p.groups - 1))), 0,
+          0, 0);
+    }
+  }
+}
+
+// G = 0: one scale.
+template <class T, int kWK, int kJ, int kI, int G>
+__global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p) {
+  using S = Stage<T, G>;
+  constexpr int kBN = T::kBN, kBK = T::kBK;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave / kWK, wk = wave % kWK;
+  // Tile order: an XCD takes a contiguous run; inside it eight k tiles are
+  // walked for each n tile, so the 32 tiles an XCD works on at once share
+  // about 4 dy panels and 8 code panels (half as wide) in its L2.
+  const int64_t tiles = (int64_t)p.n_tiles * p.k_tiles;
+  const int64_t order = xcd_contiguous(blockIdx.x, gridDim.x);
+  const int64_t part = order / tiles, local = order - part * tiles;
+  const int64_t band = local / (8 * (int64_t)p.n_tiles), first_k = 8 * band;
+  const int64_t wide = p.k_tiles - first_k < 8 ? p.k_tiles - first_k : 8;
+  const int64_t in_band = local - band * 8 * p.n_tiles;
+  const int64_t n0 = in_band / wide * kBN, k0 = (first_k + in_band % wide) * kBK;
+  const int step0 = (int)((int64_t)p.steps * part / p.splits), step1 = (int)((int64_t)p.steps * (part + 1) / p.splits);
+
+  // Loads.  A wave-wide 16-byte load fills 1 KB of a panel, lane L at byte
+  // 16 L; the swizzles act on the global side.  Rows past M re-load row M - 1
+  // (their dy is cleared below), columns past N or K the last whole chunk
+  // (they reach only results that are not stored): no address is out of range.
+  const int64_t N = p.N, K = p.K, M = p.M;
+  int a_row[T::kLA], b_row[T::kLB];
+  uint32_t a_col[T::kLA], b_col[T::kLB];
+#pragma unroll
+  for (int i = 0; i < T::kLA; ++i) {
+    const int byte = 1024 * (T::kLA * wave + i) + 16 * lane, m = byte / (2 * kBN), c16 = byte % (2 * kBN) / 16;
+    a_row[i] = m;
+    const int64_t n = n0 + 8 * (4 * dy_chunk(m, c16 >> 2) + (c16 & 3));
+    a_col[i] = 2u * (uint32_t)(n < N ? n : N - 8);
+  }
+#pragma unroll
+  for (int i = 0; i < T::kLB; ++i) {
+    const int byte = 1024 * (T::kLB * wave + i) + 16 * lane, m = byte / kBK, c16 = byte % kBK / 16;
+    b_row[i] = m;
+    const int64_t k = k0 + 16 * (2 * code_chunk<kBK>(m, c16 >> 1) + (c16 & 1));
+    b_col[i] = (uint32_t)(k < K ? k : K - 16);
+  }
+  auto load = [&](int step, auto st) __attribute__((always_inline)) {
+    load_step<T, G, decltype(st)::value>(p, step, wave, lane, k0, a_row, a_col, b_row, b_col);
+  };
+  constexpr int kL = T::kLA + T::kLB + S::kLS;
+  // s_waitcnt immediates for vmcnt(kL) or vmcnt(0), and lgkmcnt(0): the
+  // wave's reads of the stage that is loaded next are done (vmcnt in bits 3:0
+  // and 15:14, expcnt in 6:4, lgkmcnt in 11:8)
+  static_assert(kL < 64, "vmcnt holds at most 63");
+  constexpr int kOneStepInFlight = (kL & 15) | ((kL >> 4) << 14) | (7 << 4);
+  constexpr int kNoneInFlight = 7 << 4;
+
+  v16f acc[kI][kJ];
+#pragma unroll
+  for (int i = 0; i < kI; ++i)
+#pragma unroll
+    for (int j = 0; j < kJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  // Fragment reads.  16 lanes of a transposing read share a block: for 16-bit
+  // values 4 rows x 16 columns (lane t points at row t / 4, values 4 (t % 4)),
+  // for codes 8 rows x 16 columns (row t / 2, bytes 8 (t % 2)); lane t
+  // receives column t.  Lanes 0-31 cover 32 columns of rows 0-7 of a 16-row
+  // substep, lanes 32-63 rows 8-15.
+  const int t16 = lane & 15, col16 = (lane >> 4) & 1, half = lane >> 5;
+  auto read_dy = [&](const uint8_t* panel, int s, int j) __attribute__((always_inline)) {
+    v4s lo, hi;
+    const int c = 32 * (wn * kJ + j) + 16 * col16 + 4 * (t16 & 3);   // first of the 4 values
+    const int m = 16 * s + 8 * half + (t16 >> 2);
+    const int at = m * 2 * kBN + 64 * dy_chunk(m, c >> 5) + 2 * (c & 31);
+    lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(panel + at));
+    hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(panel + at + 4 * 2 * kBN));
+    return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto read_x = [&](const uint8_t* panel, const float* scales, int s, int i) __attribute__((always_inline)) {
+    const int c = 32 * (wk * kI + i) + 16 * col16 + 8 * (t16 & 1);
+    const int m = 16 * s + 8 * half + (t16 >> 1);
+    const int at = m * kBK + 32 * code_chunk<kBK>(m, c >> 5) + (c & 31);
+    const v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)(panel + at));
+    uint32_t o[4];
+    if constexpr (G == 0) {
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], 1.0f, false));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], 1.0f, true));
+      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], 1.0f, false));
+      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], 1.0f, true));
+    } else {
+      const int col = 32 * (wk * kI + i) + (lane & 31);
+      const float* sc = scales + 64 * (col / G) + 16 * s + 8 * half;
+      const float4 lo = *reinterpret_cast<const float4*>(sc), hi = *reinterpret_cast<const float4*>(sc + 4);
+      float v[8];
+      e4m3_values8(make_uint2((uint32_t)w[0], (uint32_t)w[1]), v);
+      o[0] = bf16_pack2(v[0] * lo.x, v[1] * lo.y);
+      o[1] = bf16_pack2(v[2] * lo.z, v[3] * lo.w);
+      o[2] = bf16_pack2(v[4] * hi.x, v[5] * hi.y);
+      o[3] = bf16_pack2(v[6] * hi.z, v[7] * hi.w);
+    }
+    return __builtin_bit_cast(v8bf, make_uint4(o[0], o[1], o[2], o[3]));
+  };
+
+  auto compute = [&](int step, auto st) __attribute__((always_inline)) {
+    uint8_t* a = lds_array<T::kA, decltype(st)::value>();
+    const uint8_t* b = lds_array<T::kB, 3 + decltype(st)::value>();
+    const float* sc = nullptr;
+    if constexpr (G != 0) sc = reinterpret_cast<const float*>(lds_array<256 * S::kSlots, 6 + decltype(st)::value>());
+    if (M - (int64_t)step * kStep < kStep) {
+      // last rows: clear dy past row M - 1
+      const int valid = (int)(M - (int64_t)step * kStep);
+      for (int o = valid * 2 * kBN + 16 * (int)threadIdx.x; o < T::kA; o += 16 * T::kThreads)
+        *reinterpret_cast<uint4*>(a + o) = make_uint4(0, 0, 0, 0);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int s = 0; s < kStep / 16; ++s) {
+      v8bf x[kI], d[kJ];
+#pragma unroll
+      for (int i = 0; i < kI; ++i) x[i] = read_x(b, sc, s, i);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) d[j] = read_dy(a, s, j);
+#pragma unroll
+      for (int i = 0; i < kI; ++i)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], d[j], acc[i][j], 0, 0, 0);
+    }
+  };
+  // One step: this stage's loads have arrived in every wave (barrier), which
+  // also means that every wave is done with the stage of the step before;
+  // that one takes the loads of step + 2.
+  auto run = [&](int step, auto st, auto st2) __attribute__((always_inline)) {
+    if (step + 1 < step1)
+      __builtin_amdgcn_s_waitcnt(kOneStepInFlight);
+    else
+      __builtin_amdgcn_s_waitcnt(kNoneInFlight);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    if (step + 2 < step1) load(step + 2, st2);
+    compute(step, st);
+  };
+  using C0 = std::integral_constant<int, 0>;
+  using C1 = std::integral_constant<int, 1>;
+  using C2 = std::integral_constant<int, 2>;
+  if (step0 < step1) load(step0, C0{});
+  if (step0 + 1 < step1) load(step0 + 1, C1{});
+  for (int step = step0; step < step1; step += 3) {
+    run(step, C0{}, C2{});
+    if (step + 1 < step1) run(step + 1, C1{}, C0{});
+    if (step + 2 < step1) run(step + 2, C2{}, C1{});
+  }
+
+  // Register 4 q + e of acc[i][j] is dW[n][k] with
+  //   n = n0 + 32 (wn kJ + j) + lane % 32,  k = k0 + 32 (wk kI + i) + 8 q + 4 half + e.
+  const float scale = p.out == kPartial ? 1.0f : p.scale;
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    const int64_t n = n0 + 32 * (wn * kJ + j) + (lane & 31);
+    if (n >= N) continue;
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t k = k0 + 32 * (wk * kI + i) + 8 * q + 4 * half;
+        if (k >= K) continue;
+        const float v0 = acc[i][j][4 * q] * scale, v1 = acc[i][j][4 * q + 1] * scale;
+        const float v2 = acc[i][j][4 * q + 2] * scale, v3 = acc[i][j][4 * q + 3] * scale;
+        const int64_t at = n * K + k;
+        if (p.out == kBF16) {
+          *reinterpret_cast<uint2*>((uint16_t*)p.dw + at) = make_uint2(bf16_pack2(v0, v1), bf16_pack2(v2, v3));
+        } else {
+          float4* dst = reinterpret_cast<float4*>((float*)p.dw + (p.out == kPartial ? part * N * K : 0) + at);
+          if (p.out == kF32Add) {
+            const float4 old = *dst;
+            *dst = make_float4(old.x + v0, old.y + v1, old.z + v2, old.w + v3);
+          } else {
+            *dst = make_float4(v0, v1, v2, v3);
+          }
+        }
+      }
+  }
+}
+
+// Adds the partial sums of the splits in order, scales and stores.
+__global__ __launch_bounds__(256) void wgrad_join_kernel(const float* partials, int splits, int64_t size, void* dw,
+                                                         int out, float scale) {
+  const int64_t at = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (at >= size) return;
+  float4 v = *reinterpret_cast<const float4*>(partials + at);
+  for (int s = 1; s < splits; ++s) {
+    const float4 o = *reinterpret_cast<const float4*>(partials + s * size + at);
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+  if (out == kBF16) {
+    *reinterpret_cast<uint2*>((uint16_t*)dw + at) = make_uint2(bf16_pack2(v.x, v.y), bf16_pack2(v.z, v.w));
+  } else {
+    float4* dst = reinterpret_cast<float4*>((float*)dw + at);
+    if (out == kF32Add) {
+      const float4 old = *dst;
+      v.x += old.x, v.y += old.y, v.z += old.z, v.w += old.w;
+    }
+    *dst = v;
+  }
+}
+
+// No rows: the empty sum.
+__global__ __launch_bounds__(256) void wgrad_zero_kernel(void* dw, int64_t bytes) {
+  const int64_t at = 16 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (at < bytes) *reinterpret_cast<uint4*>((uint8_t*)dw + at) = make_uint4(0, 0, 0, 0);
+}
+
+using Large = Tile<2, 4, 4, 2>;   // 256 x 256, eight waves of 128 x 64
+using Small = Tile<2, 2, 2, 2>;   // 128 x 128, four waves of 64 x 64
+
+template <int G>
+const void* large_fn() { return reinterpret_cast<const void*>(&wgrad_kernel<Large, 4, 4, 2, G>); }
+template <int G>
+const void* small_fn() { return reinterpret_cast<const void*>(&wgrad_kernel<Small, 2, 2, 2, G>); }
+
+const void* wgrad_kernel_for(bool large, int32_t g) {
+  switch (g) {
+    case 0: return large ? large_fn<0>() : small_fn<0>();
+    case 16: return large ? large_fn<16>() : small_fn<16>();
+    case 32: return large ? large_fn<32>() : small_fn<32>();
+    case 64: return large ? large_fn<64>() : small_fn<64>();
+    default: return large ? large_fn<128>() : small_fn<128>();
+  }
+}
+
+constexpr int64_t kMaxDim = 1 << 24;     // 64 rows of dy stay below 2^32 bytes
+constexpr int64_t kUnits = 256;          // compute units of the device the split is made for
+
+struct Plan {
+  bool large;
+  int32_t n_tiles, k_tiles, splits;
+};
+
+// Large tiles where they fill the compute units once, else small ones (two
+// blocks to a unit).  Where even those leave units empty and there are rows
+// for it, the rows are split, 256 rows to a part at least, and the parts
+// joined from the workspace.  A function of the sizes alone, so that the
+// workspace and the order of the sums are.
+Plan plan(int64_t M, int64_t N, int64_t K) {
+  Plan p;
+  auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
+  p.large = up(N, Large::kBN) * up(K, Large::kBK) >= kUnits;
+  p.n_tiles = (int32_t)up(N, p.large ? Large::kBN : Small::kBN);
+  p.k_tiles = (int32_t)up(K, p.large ? Large::kBK : Small::kBK);
+  const int64_t tiles = (int64_t)p.n_tiles * p.k_tiles;
+  int64_t splits = 1;
+  if (!p.large && tiles < kUnits) {
+    splits = kUnits / tiles;
+    const int64_t most = M / 256;
+    splits = splits < most ? splits : most;
+    splits = splits < 1 ? 1 : splits;
+  }
+  p.splits = (int32_t)splits;
+  return p;
+}
+
+bool wgrad_sizes_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 0 && N >= 0 && K >= 0 && N % 16 == 0 && K % 16 == 0 && N <= kMaxDim && K <= kMaxDim &&
+         M <= (int64_t)kStep * 0x7FFFFFF0 && (N == 0 || K <= INT64_MAX / 8 / N) &&
+         (N + 127) / 128 * ((K + 127) / 128) <= 0x7FFFFFFF;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t coat_fp8_weight_grad_workspace(int64_t M, int64_t N, int64_t K) {
+  if (!wgrad_sizes_ok(M, N, K)) return -1;
+  if (M == 0 || N == 0 || K == 0) return 0;
+  const Plan p = plan(M, N, K);
+  return p.splits > 1 ? p.splits * N * K * (int64_t)sizeof(float) : 0;
+}
+
+coat_status_t coat_fp8_weight_grad(const coat_weight_grad_args_t* a, hipStream_t stream) {
+  if (!a) return COAT_ERR_NULL_POINTER;
+  const int64_t M = a->M, N = a->N, K = a->K;
+  if (!wgrad_sizes_ok(M, N, K)) return COAT_ERR_INVALID_VALUE;
+  if (a->x_scales && !valid_group_size(a->group_size)) return COAT_ERR_GROUP_SIZE;
+  if (a->x_scales && K % a->group_size != 0) return COAT_ERR_INVALID_VALUE;
+  if (!a->x_scales && !isfinite(a->x_scale)) return COAT_ERR_INVALID_VALUE;
+  if (a->dw_bf16 && (a->dw_f32 || a->accumulate)) return COAT_ERR_INVALID_VALUE;
+  if (N == 0 || K == 0) return COAT_OK;
+  if (!a->dw_bf16 && !a->dw_f32) return COAT_ERR_NULL_POINTER;
+  if (M > 0 && (!a->dy || !a->x_codes)) return COAT_ERR_NULL_POINTER;
+  if (!aligned(a->dy, 16) || !aligned(a->x_codes, 16) || !aligned(a->x_scales, 4) || !aligned(a->dw_bf16, 16) ||
+      !aligned(a->dw_f32, 16) || !aligned(a->workspace, 16))
+    return COAT_ERR_MISALIGNED;
+  void* dw = a->dw_bf16 ? (void*)a->dw_bf16 : (void*)a->dw_f32;
+  const int out = a->dw_bf16 ? kBF16 : a->accumulate ? kF32Add : kF32;
+  hipError_t e = hipSuccess;
+  if (M == 0) {
+    if (out == kF32Add) return COAT_OK;
+    int64_t bytes = N * K * (a->dw_bf16 ? 2 : 4);
+    if (bytes / 4096 > 0x7FFFFFF0) return COAT_ERR_INVALID_VALUE;
+    void* args[] = {&dw, &bytes};
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&wgrad_zero_kernel), dim3((unsigned)((bytes + 4095) / 4096)),
+                        dim3(256), args, 0, stream);
+    return e == hipSuccess ? COAT_OK : hip_fail(e);
+  }
+  const Plan pl = plan(M, N, K);
+  if (pl.splits > 1) {
+    if (!a->workspace) return COAT_ERR_NULL_POINTER;
+    if (a->workspace_bytes < coat_fp8_weight_grad_workspace(M, N, K)) return COAT_ERR_INVALID_VALUE;
+  }
+  WgradParams p;
+  memset(&p, 0, sizeof(p));
+  p.dy = a->dy;
+  p.codes = a->x_codes;
+  p.scales = a->x_scales;
+  p.dw = pl.splits > 1 ? a->workspace : dw;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.groups = a->x_scales ? K / a->group_size : 0;
+  p.n_tiles = pl.n_tiles;
+  p.k_tiles = pl.k_tiles;
+  p.steps = (int32_t)((M + kStep - 1) / kStep);
+  p.splits = pl.splits;
+  p.out = pl.splits > 1 ? (int)kPartial : out;
+  p.scale = a->x_scales ? 1.0f : a->x_scale;
+  void* args[] = {&p};
+  e = hipLaunchKernel(wgrad_kernel_for(pl.large, a->x_scales ? a->group_size : 0),
+                      dim3((unsigned)((int64_t)pl.n_tiles * pl.k_tiles * pl.splits)),
+                      dim3(pl.large ? Large::kThreads : Small::kThreads), args, 0, stream);
+  if (e == hipSuccess && pl.splits > 1) {
+    const float* partials = (const float*)a->workspace;
+    int splits = pl.splits, o = out;
+    int64_t size = N * K;
+    float scale = p.scale;
+    void* join[] = {&partials, &splits, &size, &dw, &o, &scale};
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&wgrad_join_kernel), dim3((unsigned)((size + 1023) / 1024)),
+                        dim3(256), join, 0, stream);
+  }
+  return e == hipSuccess ? COAT_OK : hip_fail(e);
+}
+
+}  // extern "C"

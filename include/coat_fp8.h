@@ -443,6 +443,40 @@ coat_status_t coat_fp8_qk_norm_rope_bwd(const coat_qk_norm_rope_bwd_args_t* args
 int64_t coat_fp8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads,
                                             int64_t head_dim);
 
+/*
+ * Weight gradient of a linear layer C = X W^T whose input X was kept in E4M3:
+ *   dW[n][k] = sum over rows m of dy[m][n] * X[m][k],
+ * X = code * S per group (x_scales) or code * x_scale (x_scales NULL),
+ * accumulated in FP32 on the matrix cores.  Under one scale the codes' values
+ * are exact in BF16 and x_scale multiplies the FP32 sum; code * S is rounded
+ * to BF16 (by at most 2^-8 of it) before it is multiplied.
+ * N and K multiples of 16, K of group_size with x_scales; both at most 2^24.
+ * Exactly one of dw_bf16 and dw_f32 is given; accumulate needs dw_f32.
+ * M == 0 gives a zero gradient.  The workspace may be NULL when the workspace
+ * function gives 0.
+ * Errors: NULL_POINTER, INVALID_VALUE (sizes, x_scale not finite, dw_bf16
+ * with dw_f32 or accumulate, a workspace that is too small), GROUP_SIZE,
+ * MISALIGNED (16 bytes; x_scales 4), HIP.
+ */
+typedef struct coat_weight_grad_args {
+  const uint16_t* dy;      /* M x N BF16                                     */
+  const uint8_t* x_codes;  /* M x K                                          */
+  const float* x_scales;   /* M x K/group_size, or NULL                      */
+  uint16_t* dw_bf16;       /* N x K BF16 (written), or NULL                  */
+  float* dw_f32;           /* N x K FP32 (written or added to), or NULL      */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t M, N, K;
+  float x_scale;
+  int32_t group_size, accumulate;
+} coat_weight_grad_args_t;
+
+coat_status_t coat_fp8_weight_grad(const coat_weight_grad_args_t* args,
+                                   hipStream_t stream);
+
+/* Bytes of workspace for that call, or -1 for sizes it refuses. */
+int64_t coat_fp8_weight_grad_workspace(int64_t M, int64_t N, int64_t K);
+
 /* Static, NUL-terminated description of a status code. */
 const char* coat_status_string(coat_status_t status);
 

@@ -37,7 +37,8 @@ def test_structs_have_the_c_layout(coat):
     structs = {"coat_rms_norm_args_t": coat.RMSNormArgs, "coat_rms_norm_bwd_args_t": coat.RMSNormBwdArgs,
                "coat_swiglu_args_t": coat.SwigluArgs, "coat_qk_shape_t": coat.QkShape,
                "coat_qk_norm_rope_args_t": coat.QkNormRopeArgs,
-               "coat_qk_norm_rope_bwd_args_t": coat.QkNormRopeBwdArgs}
+               "coat_qk_norm_rope_bwd_args_t": coat.QkNormRopeBwdArgs,
+               "coat_weight_grad_args_t": coat.WeightGradArgs}
     lines, want = [], []
     for c, py in structs.items():
         lines.append(f'printf("%zu\\n", sizeof({c}));')
@@ -157,8 +158,24 @@ def test_qk_norm_rope_bwd(coat, change, status):
     assert call(coat, "qk_norm_rope_bwd", coat.QkNormRopeBwdArgs, QK_BWD, shape=SHAPE, **change) == status
 
 
+WGRAD = dict(dy=A, x_codes=A, x_scales=A, dw_bf16=A, M=4096, N=256, K=256, group_size=128, x_scale=float("nan"),
+             workspace=A, workspace_bytes=1 << 40)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(M=-1), INVAL), (dict(N=8), INVAL), (dict(K=24), INVAL), (dict(N=1 << 25), INVAL), (dict(K=-16), INVAL),
+    (dict(K=144), INVAL), (dict(group_size=256), GSIZE), (dict(x_scales=None), INVAL), (dict(dw_f32=A), INVAL),
+    (dict(accumulate=1), INVAL), (dict(workspace_bytes=64), INVAL), (dict(workspace=None), NULLP),
+    (dict(dw_bf16=None), NULLP), (dict(dy=None), NULLP), (dict(x_codes=None), NULLP), (dict(M=1 << 50), INVAL),
+    (dict(N=0), OK), (dict(K=0), OK)] +
+    [({n: A + 2}, MISAL) for n in ("dy", "x_codes", "x_scales", "dw_bf16", "workspace")] +
+    [(dict(dw_bf16=None, dw_f32=A + 8), MISAL), (dict(M=0, accumulate=1, dw_bf16=None, dw_f32=A), OK)])
+def test_weight_grad(coat, change, status):
+    assert call(coat, "weight_grad", coat.WeightGradArgs, WGRAD, **change) == status
+
+
 def test_null_arguments(coat):
-    for name in ("rms_norm", "rms_norm_bwd", "swiglu", "qk_norm_rope", "qk_norm_rope_bwd"):
+    for name in ("rms_norm", "rms_norm_bwd", "swiglu", "qk_norm_rope", "qk_norm_rope_bwd", "weight_grad"):
         assert getattr(coat.lib, f"coat_fp8_{name}")(None, None) == NULLP
 
 
@@ -173,6 +190,17 @@ def test_workspaces(coat):
     for bad in ((-1, 4, 128), (1, -1, 128), (1, 4, 0), (1, 4, 100), (1, 4, 512), (1 << 50, 4, 128)):
         with pytest.raises(coat.CoatError):
             coat.qk_norm_rope_bwd_workspace(*bad)
+
+
+def test_weight_grad_workspace(coat):
+    assert coat.weight_grad_workspace(0, 128, 128) == 0
+    assert coat.weight_grad_workspace(8192, 4096, 4096) == 0            # the tiles fill the chip
+    need = coat.weight_grad_workspace(1 << 20, 256, 256)                # few tiles, many rows
+    assert need % (256 * 256 * 4) == 0 and need >= 2 * 256 * 256 * 4
+    assert coat.weight_grad_workspace(1 << 22, 256, 256) == need
+    for bad in ((-1, 16, 16), (1, 8, 16), (1, 16, 20), (1, 1 << 25, 16)):
+        with pytest.raises(coat.CoatError):
+            coat.weight_grad_workspace(*bad)
 
 
 # ------------------------------------------------------------ the binding
@@ -251,6 +279,18 @@ def test_binding_qk(coat):
     refuses("workspace is required", go, dq_weight=f32(128), dk_weight=f32(128))
     refuses("dk has shape", go, dk=z(4, 1, 128))
     refuses("rstd holds", go, rstd=f32(4, 5))
+
+
+def test_binding_weight_grad(coat):
+    go = lambda **k: coat.weight_grad(**{**dict(dy=z(4, 128), codes=u8(4, 256), scales=0.5, dw=f32(128, 256)), **k})  # noqa: E731
+    refuses("device", go)
+    refuses("disagree", go, codes=u8(3, 256))
+    refuses("scales holds", go, scales=f32(4, 1))
+    refuses("number", go, scales=None)
+    refuses("dw holds", go, dw=f32(128, 255))
+    refuses("dw has dtype", go, dw=u8(128, 256))
+    refuses("workspace is required", go, dy=z(4096, 128), codes=u8(4096, 256))
+    refuses("workspace holds", go, dy=z(4096, 128), codes=u8(4096, 256), workspace=f32(10))
 
 
 def test_every_argument_struct_is_documented(coat):
