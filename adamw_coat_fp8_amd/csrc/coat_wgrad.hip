@@ -33,9 +33,13 @@ namespace {
 // rounded by up to 2^-4).  Sums are FP32 in the matrix cores.
 //
 // A block computes a kBN x kBK tile of dW; kWN x kWK waves own kJ x kI tiles
-// of 32 x 32.  64 rows a step, three LDS stages: the loads of step t + 2 go
-// out behind the barrier of step t, so each has two steps to arrive, and one
-// barrier a step is enough.
+// of 32 x 32.  64 rows a step, three LDS stages.  A step is four substeps of
+// 16 rows; while the MFMAs of one run, the fragments of the next are read and
+// its codes expanded.  Before the last substep every wave waits for its reads
+// of the step's stage and for its loads into the next one, and the block
+// meets at the step's one barrier: the last substep then reads ahead from the
+// next stage, and the loads of step t + 3 go into the one just read, so each
+// load has two steps and more to arrive.
 
 constexpr int kStep = 64;   // rows per pipeline step
 
@@ -89,14 +93,23 @@ struct Stage {
   static constexpr int kSlots = kLS * T::kWaves;
 };
 
-// LDS arrays of the three stages.  They are distinct objects: the compiler can
-// tell the loads into one stage from the reads of another and need not wait
-// for loads in flight.
+// LDS arrays of the three stages: the dy panel, and the code panel with the
+// scales behind it.  They are distinct objects: the compiler can tell the
+// loads into one stage from the reads of another and does not wait for loads
+// in flight.  (It follows a read's address back over a few additions only, so
+// the lane's offsets below are single opaque values, and it keeps apart seven
+// such objects at most.)
 template <int kBytes, int kWhich>
 __device__ __forceinline__ uint8_t* lds_array() {
   __shared__ __attribute__((aligned(1024))) uint8_t bytes[kBytes];
   return bytes;
 }
+
+template <class T, int kSt>
+__device__ __forceinline__ uint8_t* dy_stage() { return lds_array<T::kA, kSt>(); }
+
+template <class T, int G, int kSt>
+__device__ __forceinline__ uint8_t* code_stage() { return lds_array<T::kB + 256 * Stage<T, G>::kSlots, 3 + kSt>(); }
 
 // Issues the loads of a step into stage kSt.
 template <class T, int G, int kSt>
@@ -111,8 +124,8 @@ __device__ __forceinline__ void load_step(const WgradParams& p, int step, int wa
       __builtin_amdgcn_make_buffer_rsrc((void*)(p.dy + m0 * p.N), (short)0, (int)0xFFFFFFFF, 0x00020000);
   const __amdgpu_buffer_rsrc_t rb =
       __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + m0 * p.K), (short)0, (int)0xFFFFFFFF, 0x00020000);
-  uint8_t* a = lds_array<T::kA, kSt>();
-  uint8_t* b = lds_array<T::kB, 3 + kSt>();
+  uint8_t* a = dy_stage<T, kSt>();
+  uint8_t* b = code_stage<T, G, kSt>();
 #pragma unroll
   for (int i = 0; i < T::kLA; ++i)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, a + 1024 * (T::kLA * wave + i), 16,
@@ -126,13 +139,12 @@ __device__ __forceinline__ void load_step(const WgradParams& p, int step, int wa
     // the tile's groups repeat them: every wave issues as many loads)
     const __amdgpu_buffer_rsrc_t rs =
         __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales + m0 * p.groups), (short)0, (int)0xFFFFFFFF, 0x00020000);
-    uint8_t* sc = lds_array<256 * S::kSlots, 6 + kSt>();
 #pragma unroll
     for (int i = 0; i < S::kLS; ++i) {
       const int slot = S::kLS * wave + i;
       const int64_t g = k0 / G + slot % S::kGroups;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, sc + 256 * slot, 4,
+          rs, b + T::kB + 256 * slot, 4,
           (int)(4u * ((uint32_t)min(lane, last) * (uint32_t)p.groups + (uint32_t)(g < p.groups ? g : p.groups - 1))), 0,
           0, 0);
     }
@@ -183,10 +195,11 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
     load_step<T, G, decltype(st)::value>(p, step, wave, lane, k0, a_row, a_col, b_row, b_col);
   };
   constexpr int kL = T::kLA + T::kLB + S::kLS;
-  // s_waitcnt immediates for vmcnt(kL) or vmcnt(0), and lgkmcnt(0): the
-  // wave's reads of the stage that is loaded next are done (vmcnt in bits 3:0
-  // and 15:14, expcnt in 6:4, lgkmcnt in 11:8)
-  static_assert(kL < 64, "vmcnt holds at most 63");
+  // s_waitcnt immediates that leave the loads of two, one or no steps in
+  // flight, and lgkmcnt(0): the wave's reads of the stage that is loaded next
+  // are done (vmcnt in bits 3:0 and 15:14, expcnt in 6:4, lgkmcnt in 11:8)
+  static_assert(2 * kL < 64, "vmcnt holds at most 63");
+  constexpr int kTwoStepsInFlight = (2 * kL & 15) | ((2 * kL >> 4) << 14) | (7 << 4);
   constexpr int kOneStepInFlight = (kL & 15) | ((kL >> 4) << 14) | (7 << 4);
   constexpr int kNoneInFlight = 7 << 4;
 
@@ -204,118 +217,183 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
   // receives column t.  Lanes 0-31 cover 32 columns of rows 0-7 of a 16-row
   // substep, lanes 32-63 rows 8-15.
   const int t16 = lane & 15, col16 = (lane >> 4) & 1, half = lane >> 5;
-  auto read_dy = [&](const uint8_t* panel, int s, int j) __attribute__((always_inline)) {
-    v4s lo, hi;
-    const int c = 32 * (wn * kJ + j) + 16 * col16 + 4 * (t16 & 3);   // first of the 4 values
-    const int m = 16 * s + 8 * half + (t16 >> 2);
-    const int at = m * 2 * kBN + 64 * dy_chunk(m, c >> 5) + 2 * (c & 31);
-    lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(panel + at));
-    hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(panel + at + 4 * 2 * kBN));
-    return __builtin_bit_cast(v8bf, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  v4s dlo[2][kJ], dhi[2][kJ];   // dy fragments of two substeps
+  v2i xw[kI];                   // codes of the substep being read
+  float4 slo[kI], shi[kI];      // and their scales
+  v8bf x[2][kI];
+  int dy_off[kJ], x_off[kI], s_off[kI];
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    const int c = 32 * (wn * kJ + j) + 16 * col16 + 4 * (t16 & 3), m = 8 * half + (t16 >> 2);
+    dy_off[j] = m * 2 * kBN + 64 * dy_chunk(m, c >> 5) + 2 * (c & 31);
+    asm volatile("" : "+v"(dy_off[j]));
+  }
+#pragma unroll
+  for (int i = 0; i < kI; ++i) {
+    const int c = 32 * (wk * kI + i) + 16 * col16 + 8 * (t16 & 1), m = 8 * half + (t16 >> 1);
+    x_off[i] = m * kBK + 32 * code_chunk<kBK>(m, c >> 5) + (c & 31);
+    asm volatile("" : "+v"(x_off[i]));
+    s_off[i] = G ? T::kB + 4 * (64 * ((32 * (wk * kI + i) + (lane & 31)) / (G ? G : 1)) + 8 * half) : 0;
+    if constexpr (G != 0) asm volatile("" : "+v"(s_off[i]));
+  }
+  // (the swizzles repeat every 4 and 8 rows: a substep is 16 further, the
+  // second half of a dy fragment 4)
+  auto read_dy = [&](const uint8_t* panel, int f, int s, int j, int high) __attribute__((always_inline)) {
+    (high ? dhi : dlo)[f][j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) v4s*)(panel + (dy_off[j] + (16 * s + 4 * high) * 2 * kBN)));
   };
-  auto read_x = [&](const uint8_t* panel, const float* scales, int s, int i) __attribute__((always_inline)) {
-    const int c = 32 * (wk * kI + i) + 16 * col16 + 8 * (t16 & 1);
-    const int m = 16 * s + 8 * half + (t16 >> 1);
-    const int at = m * kBK + 32 * code_chunk<kBK>(m, c >> 5) + (c & 31);
-    const v2i w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) v2i*)(panel + at));
+  auto read_x = [&](const uint8_t* panel, int s, int i) __attribute__((always_inline)) {
+    xw[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+        (__attribute__((address_space(3))) v2i*)(panel + (x_off[i] + 16 * s * kBK)));
+    if constexpr (G != 0) {
+      slo[i] = *reinterpret_cast<const float4*>(panel + (s_off[i] + 64 * s));
+      shi[i] = *reinterpret_cast<const float4*>(panel + (s_off[i] + 64 * s + 16));
+    }
+  };
+  auto expand = [&](int f, int i) __attribute__((always_inline)) {
     uint32_t o[4];
     if constexpr (G == 0) {
-      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], 1.0f, false));
-      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], 1.0f, true));
-      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], 1.0f, false));
-      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[1], 1.0f, true));
+      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][0], 1.0f, false));
+      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][0], 1.0f, true));
+      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][1], 1.0f, false));
+      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][1], 1.0f, true));
     } else {
-      const int col = 32 * (wk * kI + i) + (lane & 31);
-      const float* sc = scales + 64 * (col / G) + 16 * s + 8 * half;
-      const float4 lo = *reinterpret_cast<const float4*>(sc), hi = *reinterpret_cast<const float4*>(sc + 4);
       float v[8];
-      e4m3_values8(make_uint2((uint32_t)w[0], (uint32_t)w[1]), v);
-      o[0] = bf16_pack2(v[0] * lo.x, v[1] * lo.y);
-      o[1] = bf16_pack2(v[2] * lo.z, v[3] * lo.w);
-      o[2] = bf16_pack2(v[4] * hi.x, v[5] * hi.y);
-      o[3] = bf16_pack2(v[6] * hi.z, v[7] * hi.w);
+      e4m3_values8(make_uint2((uint32_t)xw[i][0], (uint32_t)xw[i][1]), v);
+      o[0] = bf16_pack2(v[0] * slo[i].x, v[1] * slo[i].y);
+      o[1] = bf16_pack2(v[2] * slo[i].z, v[3] * slo[i].w);
+      o[2] = bf16_pack2(v[4] * shi[i].x, v[5] * shi[i].y);
+      o[3] = bf16_pack2(v[6] * shi[i].z, v[7] * shi[i].w);
     }
-    return __builtin_bit_cast(v8bf, make_uint4(o[0], o[1], o[2], o[3]));
+    x[f][i] = __builtin_bit_cast(v8bf, make_uint4(o[0], o[1], o[2], o[3]));
   };
-
-  auto compute = [&](int step, auto st) __attribute__((always_inline)) {
-    uint8_t* a = lds_array<T::kA, decltype(st)::value>();
-    const uint8_t* b = lds_array<T::kB, 3 + decltype(st)::value>();
-    const float* sc = nullptr;
-    if constexpr (G != 0) sc = reinterpret_cast<const float*>(lds_array<256 * S::kSlots, 6 + decltype(st)::value>());
+  auto mma = [&](int f, int n) __attribute__((always_inline)) {
+    const int i = n / kJ, j = n % kJ;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        x[f][i], __builtin_bit_cast(v8bf, __builtin_shufflevector(dlo[f][j], dhi[f][j], 0, 1, 2, 3, 4, 5, 6, 7)),
+        acc[i][j], 0, 0, 0);
+  };
+  // The MFMAs of fragment set f, with substep s of a stage read into the other
+  // set between them: codes first, expanded behind the last MFMAs.
+  constexpr int kMF = kI * kJ, kR = 2 * kJ;
+  auto substep = [&](int f, const uint8_t* a, const uint8_t* b, int s) __attribute__((always_inline)) {
+#pragma unroll
+    for (int n = 0; n < kMF; ++n) {
+      mma(f, n);
+      if (n == 0) {
+#pragma unroll
+        for (int i = 0; i < kI; ++i) read_x(b, s, i);
+      }
+#pragma unroll
+      for (int r = n * kR / kMF; r < (n + 1) * kR / kMF; ++r) read_dy(a, 1 - f, s, r / 2, r % 2);
+      if (n >= kMF - kI) expand(1 - f, n - (kMF - kI));
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // Clears dy past row M - 1 in the stage of a step, behind its barrier.
+  auto clear_tail = [&](int step, uint8_t* a) __attribute__((always_inline)) {
     if (M - (int64_t)step * kStep < kStep) {
-      // last rows: clear dy past row M - 1
       const int valid = (int)(M - (int64_t)step * kStep);
       for (int o = valid * 2 * kBN + 16 * (int)threadIdx.x; o < T::kA; o += 16 * T::kThreads)
         *reinterpret_cast<uint4*>(a + o) = make_uint4(0, 0, 0, 0);
       __syncthreads();
     }
-#pragma unroll
-    for (int s = 0; s < kStep / 16; ++s) {
-      v8bf x[kI], d[kJ];
-#pragma unroll
-      for (int i = 0; i < kI; ++i) x[i] = read_x(b, sc, s, i);
-#pragma unroll
-      for (int j = 0; j < kJ; ++j) d[j] = read_dy(a, s, j);
-#pragma unroll
-      for (int i = 0; i < kI; ++i)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x[i], d[j], acc[i][j], 0, 0, 0);
-    }
   };
-  // One step: this stage's loads have arrived in every wave (barrier), which
-  // also means that every wave is done with the stage of the step before;
-  // that one takes the loads of step + 2.
-  auto run = [&](int step, auto st, auto st2) __attribute__((always_inline)) {
-    if (step + 1 < step1)
+  auto meet = [&](int in_flight) __attribute__((always_inline)) {
+    if (in_flight >= 2)
+      __builtin_amdgcn_s_waitcnt(kTwoStepsInFlight);
+    else if (in_flight == 1)
       __builtin_amdgcn_s_waitcnt(kOneStepInFlight);
     else
       __builtin_amdgcn_s_waitcnt(kNoneInFlight);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
-    if (step + 2 < step1) load(step + 2, st2);
-    compute(step, st);
+  };
+  // kMore: steps up to step + 3 follow, so nothing depends on the step (the
+  // compiler then sees that the next stage's loads have been waited for)
+  auto run = [&](int step, auto st, auto next, auto more) __attribute__((always_inline)) {
+    constexpr bool kMore = decltype(more)::value;
+    constexpr int kSt = decltype(st)::value, kNext = decltype(next)::value;
+    const uint8_t* a = dy_stage<T, kSt>();
+    const uint8_t* b = code_stage<T, G, kSt>();
+    substep(0, a, b, 1);
+    substep(1, a, b, 2);
+    substep(0, a, b, 3);
+    uint8_t* an = dy_stage<T, kNext>();
+    const uint8_t* bn = code_stage<T, G, kNext>();
+    if constexpr (kMore) {
+      meet(1);
+      load(step + 3, st);
+    } else {
+      // (behind the last step this reads a stage that nothing uses)
+      meet(step + 2 < step1 ? 1 : 0);
+      if (step + 1 < step1) clear_tail(step + 1, an);
+      if (step + 3 < step1) load(step + 3, st);
+    }
+    substep(1, an, bn, 0);
   };
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
   using C2 = std::integral_constant<int, 2>;
-  if (step0 < step1) load(step0, C0{});
-  if (step0 + 1 < step1) load(step0 + 1, C1{});
-  for (int step = step0; step < step1; step += 3) {
-    run(step, C0{}, C2{});
-    if (step + 1 < step1) run(step + 1, C1{}, C0{});
-    if (step + 2 < step1) run(step + 2, C2{}, C1{});
+  if (step0 < step1) {
+    load(step0, C0{});
+    if (step0 + 1 < step1) load(step0 + 1, C1{});
+    if (step0 + 2 < step1) load(step0 + 2, C2{});
+    meet(step1 - step0 - 1);
+    uint8_t* a = dy_stage<T, 0>();
+    clear_tail(step0, a);
+#pragma unroll
+    for (int i = 0; i < kI; ++i) read_x(code_stage<T, G, 0>(), 0, i);
+#pragma unroll
+    for (int r = 0; r < kR; ++r) read_dy(a, 0, 0, r / 2, r % 2);
+#pragma unroll
+    for (int i = 0; i < kI; ++i) expand(0, i);
+  }
+  int step = step0;
+  for (; step + 5 < step1; step += 3) {
+    run(step, C0{}, C1{}, std::true_type{});
+    run(step + 1, C1{}, C2{}, std::true_type{});
+    run(step + 2, C2{}, C0{}, std::true_type{});
+  }
+  for (; step < step1; step += 3) {
+    run(step, C0{}, C1{}, std::false_type{});
+    if (step + 1 < step1) run(step + 1, C1{}, C2{}, std::false_type{});
+    if (step + 2 < step1) run(step + 2, C2{}, C0{}, std::false_type{});
   }
 
   // Register 4 q + e of acc[i][j] is dW[n][k] with
   //   n = n0 + 32 (wn kJ + j) + lane % 32,  k = k0 + 32 (wk kI + i) + 8 q + 4 half + e.
-  const float scale = p.out == kPartial ? 1.0f : p.scale;
+  auto each = [&](auto store) __attribute__((always_inline)) {
+    const float scale = p.out == kPartial ? 1.0f : p.scale;
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) {
-    const int64_t n = n0 + 32 * (wn * kJ + j) + (lane & 31);
-    if (n >= N) continue;
+    for (int j = 0; j < kJ; ++j) {
+      const int64_t n = n0 + 32 * (wn * kJ + j) + (lane & 31);
+      if (n >= N) continue;
 #pragma unroll
-    for (int i = 0; i < kI; ++i)
+      for (int i = 0; i < kI; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t k = k0 + 32 * (wk * kI + i) + 8 * q + 4 * half;
-        if (k >= K) continue;
-        const float v0 = acc[i][j][4 * q] * scale, v1 = acc[i][j][4 * q + 1] * scale;
-        const float v2 = acc[i][j][4 * q + 2] * scale, v3 = acc[i][j][4 * q + 3] * scale;
-        const int64_t at = n * K + k;
-        if (p.out == kBF16) {
-          *reinterpret_cast<uint2*>((uint16_t*)p.dw + at) = make_uint2(bf16_pack2(v0, v1), bf16_pack2(v2, v3));
-        } else {
-          float4* dst = reinterpret_cast<float4*>((float*)p.dw + (p.out == kPartial ? part * N * K : 0) + at);
-          if (p.out == kF32Add) {
-            const float4 old = *dst;
-            *dst = make_float4(old.x + v0, old.y + v1, old.z + v2, old.w + v3);
-          } else {
-            *dst = make_float4(v0, v1, v2, v3);
-          }
+        for (int q = 0; q < 4; ++q) {
+          const int64_t k = k0 + 32 * (wk * kI + i) + 8 * q + 4 * half;
+          if (k < K)
+            store(n * K + k, make_float4(acc[i][j][4 * q] * scale, acc[i][j][4 * q + 1] * scale,
+                                         acc[i][j][4 * q + 2] * scale, acc[i][j][4 * q + 3] * scale));
         }
-      }
+    }
+  };
+  if (p.out == kBF16) {
+    uint16_t* dw = (uint16_t*)p.dw;
+    each([&](int64_t at, float4 v) __attribute__((always_inline)) {
+      *reinterpret_cast<uint2*>(dw + at) = make_uint2(bf16_pack2(v.x, v.y), bf16_pack2(v.z, v.w));
+    });
+  } else if (p.out == kF32Add) {
+    float* dw = (float*)p.dw;
+    each([&](int64_t at, float4 v) __attribute__((always_inline)) {
+      const float4 old = *reinterpret_cast<const float4*>(dw + at);
+      *reinterpret_cast<float4*>(dw + at) = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+    });
+  } else {
+    float* dw = (float*)p.dw + (p.out == kPartial ? part * N * K : 0);
+    each([&](int64_t at, float4 v) __attribute__((always_inline)) { *reinterpret_cast<float4*>(dw + at) = v; });
   }
 }
 
