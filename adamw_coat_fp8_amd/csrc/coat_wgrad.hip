@@ -111,43 +111,35 @@ __device__ __forceinline__ uint8_t* dy_stage() { return lds_array<T::kA, kSt>();
 template <class T, int G, int kSt>
 __device__ __forceinline__ uint8_t* code_stage() { return lds_array<T::kB + 256 * Stage<T, G>::kSlots, 3 + kSt>(); }
 
-// Issues the loads of a step into stage kSt.
-template <class T, int G, int kSt>
-__device__ __forceinline__ void load_step(const WgradParams& p, int step, int wave, int lane, int64_t k0,
-                                          const int (&a_row)[T::kLA], const uint32_t (&a_col)[T::kLA],
-                                          const int (&b_row)[T::kLB], const uint32_t (&b_col)[T::kLB]) {
-  using S = Stage<T, G>;
+// Load q of a wave's loads of a step, into stage kSt: dy, codes, scales.  `off`
+// are the lane's byte offsets from the step's first row.  kRagged: the step
+// may end past row M - 1; those rows re-load it.
+template <class T, int G, int kSt, bool kRagged>
+__device__ __forceinline__ void load_one(const WgradParams& p, int step, int wave, int lane, int q,
+                                         const uint32_t (&off)[T::kLA + T::kLB + Stage<T, G>::kLS]) {
   const int64_t m0 = (int64_t)step * kStep;
   const int last = (int)(p.M - m0 < kStep ? p.M - m0 : kStep) - 1;
-  const uint32_t a_stride = 2u * (uint32_t)p.N, b_stride = (uint32_t)p.K;
-  const __amdgpu_buffer_rsrc_t ra =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(p.dy + m0 * p.N), (short)0, (int)0xFFFFFFFF, 0x00020000);
-  const __amdgpu_buffer_rsrc_t rb =
-      __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + m0 * p.K), (short)0, (int)0xFFFFFFFF, 0x00020000);
-  uint8_t* a = dy_stage<T, kSt>();
-  uint8_t* b = code_stage<T, G, kSt>();
-#pragma unroll
-  for (int i = 0; i < T::kLA; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, a + 1024 * (T::kLA * wave + i), 16,
-                                             (int)((uint32_t)min(a_row[i], last) * a_stride + a_col[i]), 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < T::kLB; ++i)
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, b + 1024 * (T::kLB * wave + i), 16,
-                                             (int)((uint32_t)min(b_row[i], last) * b_stride + b_col[i]), 0, 0, 0);
-  if constexpr (G != 0) {
-    // slot g holds the scales of group g for the step's 64 rows (slots past
-    // the tile's groups repeat them: every wave issues as many loads)
-    const __amdgpu_buffer_rsrc_t rs =
+  auto back = [&](int row, uint32_t stride) __attribute__((always_inline)) {
+    return kRagged && row > last ? (uint32_t)(row - last) * stride : 0u;
+  };
+  if (q < T::kLA) {
+    const int row = (1024 * (T::kLA * wave + q) + 16 * lane) / (2 * T::kBN);
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(p.dy + m0 * p.N), (short)0, (int)0xFFFFFFFF, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dy_stage<T, kSt>() + 1024 * (T::kLA * wave + q), 16,
+                                             (int)(off[q] - back(row, 2u * (uint32_t)p.N)), 0, 0, 0);
+  } else if (q < T::kLA + T::kLB) {
+    const int i = q - T::kLA, row = (1024 * (T::kLB * wave + i) + 16 * lane) / T::kBK;
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + m0 * p.K), (short)0, (int)0xFFFFFFFF, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, code_stage<T, G, kSt>() + 1024 * (T::kLB * wave + i), 16,
+                                             (int)(off[q] - back(row, (uint32_t)p.K)), 0, 0, 0);
+  } else {
+    const int i = q - T::kLA - T::kLB;
+    const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales + m0 * p.groups), (short)0, (int)0xFFFFFFFF, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < S::kLS; ++i) {
-      const int slot = S::kLS * wave + i;
-      const int64_t g = k0 / G + slot % S::kGroups;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          rs, b + T::kB + 256 * slot, 4,
-          (int)(4u * ((uint32_t)min(lane, last) * (uint32_t)p.groups + (uint32_t)(g < p.groups ? g : p.groups - 1))), 0,
-          0, 0);
-    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, code_stage<T, G, kSt>() + T::kB + 256 * (Stage<T, G>::kLS * wave + i), 4,
+                                             (int)(off[q] - back(lane, 4u * (uint32_t)p.groups)), 0, 0, 0);
   }
 }
 
@@ -173,28 +165,37 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
   // Loads.  A wave-wide 16-byte load fills 1 KB of a panel, lane L at byte
   // 16 L; the swizzles act on the global side.  Rows past M re-load row M - 1
   // (their dy is cleared below), columns past N or K the last whole chunk
-  // (they reach only results that are not stored): no address is out of range.
+  // (they reach only results that are not stored): no address is out of
+  // range.  Slot g of the scales holds those of group g for the step's 64
+  // rows; slots past the tile's groups repeat them, so that every wave issues
+  // as many loads.
   const int64_t N = p.N, K = p.K, M = p.M;
-  int a_row[T::kLA], b_row[T::kLB];
-  uint32_t a_col[T::kLA], b_col[T::kLB];
+  constexpr int kL = T::kLA + T::kLB + S::kLS;
+  uint32_t off[kL];
 #pragma unroll
   for (int i = 0; i < T::kLA; ++i) {
     const int byte = 1024 * (T::kLA * wave + i) + 16 * lane, m = byte / (2 * kBN), c16 = byte % (2 * kBN) / 16;
-    a_row[i] = m;
     const int64_t n = n0 + 8 * (4 * dy_chunk(m, c16 >> 2) + (c16 & 3));
-    a_col[i] = 2u * (uint32_t)(n < N ? n : N - 8);
+    off[i] = 2u * ((uint32_t)m * (uint32_t)N + (uint32_t)(n < N ? n : N - 8));
   }
 #pragma unroll
   for (int i = 0; i < T::kLB; ++i) {
     const int byte = 1024 * (T::kLB * wave + i) + 16 * lane, m = byte / kBK, c16 = byte % kBK / 16;
-    b_row[i] = m;
     const int64_t k = k0 + 16 * (2 * code_chunk<kBK>(m, c16 >> 1) + (c16 & 1));
-    b_col[i] = (uint32_t)(k < K ? k : K - 16);
+    off[T::kLA + i] = (uint32_t)m * (uint32_t)K + (uint32_t)(k < K ? k : K - 16);
+  }
+  if constexpr (G != 0) {
+#pragma unroll
+    for (int i = 0; i < S::kLS; ++i) {
+      const int64_t g = k0 / G + (S::kLS * wave + i) % S::kGroups;
+      off[T::kLA + T::kLB + i] =
+          4u * ((uint32_t)lane * (uint32_t)p.groups + (uint32_t)(g < p.groups ? g : p.groups - 1));
+    }
   }
   auto load = [&](int step, auto st) __attribute__((always_inline)) {
-    load_step<T, G, decltype(st)::value>(p, step, wave, lane, k0, a_row, a_col, b_row, b_col);
+#pragma unroll
+    for (int q = 0; q < kL; ++q) load_one<T, G, decltype(st)::value, true>(p, step, wave, lane, q, off);
   };
-  constexpr int kL = T::kLA + T::kLB + S::kLS;
   // s_waitcnt immediates that leave the loads of two, one or no steps in
   // flight, and lgkmcnt(0): the wave's reads of the stage that is loaded next
   // are done (vmcnt in bits 3:0 and 15:14, expcnt in 6:4, lgkmcnt in 11:8)
@@ -220,7 +221,7 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
   v4s dlo[2][kJ], dhi[2][kJ];   // dy fragments of two substeps
   v2i xw[kI];                   // codes of the substep being read
   float4 slo[kI], shi[kI];      // and their scales
-  v8bf x[2][kI];
+  u32x4v x[2][kI];
   int dy_off[kJ], x_off[kI], s_off[kI];
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
@@ -245,38 +246,34 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
   auto read_x = [&](const uint8_t* panel, int s, int i) __attribute__((always_inline)) {
     xw[i] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
         (__attribute__((address_space(3))) v2i*)(panel + (x_off[i] + 16 * s * kBK)));
-    if constexpr (G != 0) {
+    if (G != 0 && (i == 0 || G < 32 * kI)) {   // (a wave's columns may share their group)
       slo[i] = *reinterpret_cast<const float4*>(panel + (s_off[i] + 64 * s));
       shi[i] = *reinterpret_cast<const float4*>(panel + (s_off[i] + 64 * s + 16));
     }
   };
-  auto expand = [&](int f, int i) __attribute__((always_inline)) {
-    uint32_t o[4];
+  // Dword q of fragment i: two values.
+  auto expand = [&](int f, int i, int q) __attribute__((always_inline)) {
     if constexpr (G == 0) {
-      o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][0], 1.0f, false));
-      o[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][0], 1.0f, true));
-      o[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][1], 1.0f, false));
-      o[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][1], 1.0f, true));
+      x[f][i][q] = __builtin_bit_cast(uint32_t, q & 1 ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][q / 2], 1.0f, true)
+                                                      : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(xw[i][q / 2], 1.0f, false));
     } else {
-      float v[8];
-      e4m3_values8(make_uint2((uint32_t)xw[i][0], (uint32_t)xw[i][1]), v);
-      o[0] = bf16_pack2(v[0] * slo[i].x, v[1] * slo[i].y);
-      o[1] = bf16_pack2(v[2] * slo[i].z, v[3] * slo[i].w);
-      o[2] = bf16_pack2(v[4] * shi[i].x, v[5] * shi[i].y);
-      o[3] = bf16_pack2(v[6] * shi[i].z, v[7] * shi[i].w);
+      const int g = G >= 32 * kI ? 0 : i;
+      const auto v = q & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(xw[i][q / 2], true) : __builtin_amdgcn_cvt_pk_f32_fp8(xw[i][q / 2], false);
+      const float4 sc = q < 2 ? slo[g] : shi[g];
+      x[f][i][q] = q & 1 ? bf16_pack2(v[0] * sc.z, v[1] * sc.w) : bf16_pack2(v[0] * sc.x, v[1] * sc.y);
     }
-    x[f][i] = __builtin_bit_cast(v8bf, make_uint4(o[0], o[1], o[2], o[3]));
   };
   auto mma = [&](int f, int n) __attribute__((always_inline)) {
     const int i = n / kJ, j = n % kJ;
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        x[f][i], __builtin_bit_cast(v8bf, __builtin_shufflevector(dlo[f][j], dhi[f][j], 0, 1, 2, 3, 4, 5, 6, 7)),
+        __builtin_bit_cast(v8bf, x[f][i]), __builtin_bit_cast(v8bf, __builtin_shufflevector(dlo[f][j], dhi[f][j], 0, 1, 2, 3, 4, 5, 6, 7)),
         acc[i][j], 0, 0, 0);
   };
   // The MFMAs of fragment set f, with substep s of a stage read into the other
-  // set between them: codes first, expanded behind the last MFMAs.
-  constexpr int kMF = kI * kJ, kR = 2 * kJ;
-  auto substep = [&](int f, const uint8_t* a, const uint8_t* b, int s) __attribute__((always_inline)) {
+  // set between them: the codes first, expanded dword by dword behind the
+  // later MFMAs.
+  constexpr int kMF = kI * kJ, kR = 2 * kJ, kE = 4 * kI, kFirst = kMF > 4 ? 3 : 1;
+  auto substep = [&](int f, const uint8_t* a, const uint8_t* b, int s, auto also) __attribute__((always_inline)) {
 #pragma unroll
     for (int n = 0; n < kMF; ++n) {
       mma(f, n);
@@ -286,10 +283,16 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
       }
 #pragma unroll
       for (int r = n * kR / kMF; r < (n + 1) * kR / kMF; ++r) read_dy(a, 1 - f, s, r / 2, r % 2);
-      if (n >= kMF - kI) expand(1 - f, n - (kMF - kI));
+      if (n >= kFirst) {
+#pragma unroll
+        for (int e = (n - kFirst) * kE / (kMF - kFirst); e < (n - kFirst + 1) * kE / (kMF - kFirst); ++e)
+          expand(1 - f, e / 4, e % 4);
+      }
+      also(n);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
+  auto nothing = [](int) __attribute__((always_inline)) {};
   // Clears dy past row M - 1 in the stage of a step, behind its barrier.
   auto clear_tail = [&](int step, uint8_t* a) __attribute__((always_inline)) {
     if (M - (int64_t)step * kStep < kStep) {
@@ -309,28 +312,32 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
   };
-  // kMore: steps up to step + 3 follow, so nothing depends on the step (the
-  // compiler then sees that the next stage's loads have been waited for)
+  // kMore: step + 3 is not the last step, so nothing depends on the step (the
+  // compiler then sees that the next stage's loads have been waited for), and
+  // step + 3's loads go out between the MFMAs.
   auto run = [&](int step, auto st, auto next, auto more) __attribute__((always_inline)) {
     constexpr bool kMore = decltype(more)::value;
     constexpr int kSt = decltype(st)::value, kNext = decltype(next)::value;
     const uint8_t* a = dy_stage<T, kSt>();
     const uint8_t* b = code_stage<T, G, kSt>();
-    substep(0, a, b, 1);
-    substep(1, a, b, 2);
-    substep(0, a, b, 3);
+    substep(0, a, b, 1, nothing);
+    substep(1, a, b, 2, nothing);
+    substep(0, a, b, 3, nothing);
     uint8_t* an = dy_stage<T, kNext>();
     const uint8_t* bn = code_stage<T, G, kNext>();
     if constexpr (kMore) {
       meet(1);
-      load(step + 3, st);
+      substep(1, an, bn, 0, [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q = n * kL / kMF; q < (n + 1) * kL / kMF; ++q) load_one<T, G, kSt, false>(p, step + 3, wave, lane, q, off);
+      });
     } else {
       // (behind the last step this reads a stage that nothing uses)
       meet(step + 2 < step1 ? 1 : 0);
       if (step + 1 < step1) clear_tail(step + 1, an);
       if (step + 3 < step1) load(step + 3, st);
+      substep(1, an, bn, 0, nothing);
     }
-    substep(1, an, bn, 0);
   };
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
@@ -347,10 +354,10 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
 #pragma unroll
     for (int r = 0; r < kR; ++r) read_dy(a, 0, 0, r / 2, r % 2);
 #pragma unroll
-    for (int i = 0; i < kI; ++i) expand(0, i);
+    for (int e = 0; e < kE; ++e) expand(0, e / 4, e % 4);
   }
   int step = step0;
-  for (; step + 5 < step1; step += 3) {
+  for (; step + 6 < step1; step += 3) {
     run(step, C0{}, C1{}, std::true_type{});
     run(step + 1, C1{}, C2{}, std::true_type{});
     run(step + 2, C2{}, C0{}, std::true_type{});
