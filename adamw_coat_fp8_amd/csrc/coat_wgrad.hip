@@ -112,34 +112,38 @@ template <class T, int G, int kSt>
 __device__ __forceinline__ uint8_t* code_stage() { return lds_array<T::kB + 256 * Stage<T, G>::kSlots, 3 + kSt>(); }
 
 // Load q of a wave's loads of a step, into stage kSt: dy, codes, scales.  `off`
-// are the lane's byte offsets from the step's first row.  kRagged: the step
-// may end past row M - 1; those rows re-load it.
-template <class T, int G, int kSt, bool kRagged>
-__device__ __forceinline__ void load_one(const WgradParams& p, int step, int wave, int lane, int q,
+// are the lane's byte offsets from the step's first row.  kLast: the step may
+// end past row M - 1, and those rows re-load it; or lie at or past step1, and
+// then every lane loads the first bytes of the last step, which nothing reads:
+// the number of loads in flight does not depend on the step.
+template <class T, int G, int kSt, bool kLast>
+__device__ __forceinline__ void load_one(const WgradParams& p, int step, int step1, int wave, int lane, int q,
                                          const uint32_t (&off)[T::kLA + T::kLB + Stage<T, G>::kLS]) {
-  const int64_t m0 = (int64_t)step * kStep;
+  const int64_t m0 = (int64_t)(kLast && step >= step1 ? step1 - 1 : step) * kStep;
   const int last = (int)(p.M - m0 < kStep ? p.M - m0 : kStep) - 1;
-  auto back = [&](int row, uint32_t stride) __attribute__((always_inline)) {
-    return kRagged && row > last ? (uint32_t)(row - last) * stride : 0u;
+  auto at = [&](int row, uint32_t stride) __attribute__((always_inline)) {
+    if constexpr (!kLast) return (int)off[q];
+    const uint32_t back = row > last ? (uint32_t)(row - last) * stride : 0u;
+    return (int)(off[q] - back) & ((step - step1) >> 31);   // 0 where step >= step1
   };
   if (q < T::kLA) {
     const int row = (1024 * (T::kLA * wave + q) + 16 * lane) / (2 * T::kBN);
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc((void*)(p.dy + m0 * p.N), (short)0, (int)0xFFFFFFFF, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dy_stage<T, kSt>() + 1024 * (T::kLA * wave + q), 16,
-                                             (int)(off[q] - back(row, 2u * (uint32_t)p.N)), 0, 0, 0);
+                                             at(row, 2u * (uint32_t)p.N), 0, 0, 0);
   } else if (q < T::kLA + T::kLB) {
     const int i = q - T::kLA, row = (1024 * (T::kLB * wave + i) + 16 * lane) / T::kBK;
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc((void*)(p.codes + m0 * p.K), (short)0, (int)0xFFFFFFFF, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, code_stage<T, G, kSt>() + 1024 * (T::kLB * wave + i), 16,
-                                             (int)(off[q] - back(row, (uint32_t)p.K)), 0, 0, 0);
+                                             at(row, (uint32_t)p.K), 0, 0, 0);
   } else {
     const int i = q - T::kLA - T::kLB;
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc((void*)(p.scales + m0 * p.groups), (short)0, (int)0xFFFFFFFF, 0x00020000);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, code_stage<T, G, kSt>() + T::kB + 256 * (Stage<T, G>::kLS * wave + i), 4,
-                                             (int)(off[q] - back(lane, 4u * (uint32_t)p.groups)), 0, 0, 0);
+                                             at(lane, 4u * (uint32_t)p.groups), 0, 0, 0);
   }
 }
 
@@ -192,17 +196,12 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
           4u * ((uint32_t)lane * (uint32_t)p.groups + (uint32_t)(g < p.groups ? g : p.groups - 1));
     }
   }
-  auto load = [&](int step, auto st) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < kL; ++q) load_one<T, G, decltype(st)::value, true>(p, step, wave, lane, q, off);
-  };
-  // s_waitcnt immediates that leave the loads of two, one or no steps in
-  // flight, and lgkmcnt(0): the wave's reads of the stage that is loaded next
-  // are done (vmcnt in bits 3:0 and 15:14, expcnt in 6:4, lgkmcnt in 11:8)
+  // s_waitcnt immediates that leave the loads of two or one steps in flight,
+  // and lgkmcnt(0): the wave's reads of the stage that is loaded next are done
+  // (vmcnt in bits 3:0 and 15:14, expcnt in 6:4, lgkmcnt in 11:8)
   static_assert(2 * kL < 64, "vmcnt holds at most 63");
   constexpr int kTwoStepsInFlight = (2 * kL & 15) | ((2 * kL >> 4) << 14) | (7 << 4);
   constexpr int kOneStepInFlight = (kL & 15) | ((kL >> 4) << 14) | (7 << 4);
-  constexpr int kNoneInFlight = 7 << 4;
 
   v16f acc[kI][kJ];
 #pragma unroll
@@ -302,21 +301,14 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
       __syncthreads();
     }
   };
-  auto meet = [&](int in_flight) __attribute__((always_inline)) {
-    if (in_flight >= 2)
-      __builtin_amdgcn_s_waitcnt(kTwoStepsInFlight);
-    else if (in_flight == 1)
-      __builtin_amdgcn_s_waitcnt(kOneStepInFlight);
-    else
-      __builtin_amdgcn_s_waitcnt(kNoneInFlight);
+  auto meet = [&](auto wait) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(decltype(wait)::value);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
   };
-  // kMore: step + 3 is not the last step, so nothing depends on the step (the
-  // compiler then sees that the next stage's loads have been waited for), and
-  // step + 3's loads go out between the MFMAs.
-  auto run = [&](int step, auto st, auto next, auto more) __attribute__((always_inline)) {
-    constexpr bool kMore = decltype(more)::value;
+  // last: the step's successors may be the last step or none
+  auto run = [&](int step, auto st, auto next, auto last) __attribute__((always_inline)) {
+    constexpr bool kLast = decltype(last)::value;
     constexpr int kSt = decltype(st)::value, kNext = decltype(next)::value;
     const uint8_t* a = dy_stage<T, kSt>();
     const uint8_t* b = code_stage<T, G, kSt>();
@@ -324,49 +316,46 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
     substep(1, a, b, 2, nothing);
     substep(0, a, b, 3, nothing);
     uint8_t* an = dy_stage<T, kNext>();
-    const uint8_t* bn = code_stage<T, G, kNext>();
-    if constexpr (kMore) {
-      meet(1);
-      substep(1, an, bn, 0, [&](int n) __attribute__((always_inline)) {
-#pragma unroll
-        for (int q = n * kL / kMF; q < (n + 1) * kL / kMF; ++q) load_one<T, G, kSt, false>(p, step + 3, wave, lane, q, off);
-      });
-    } else {
-      // (behind the last step this reads a stage that nothing uses)
-      meet(step + 2 < step1 ? 1 : 0);
+    meet(std::integral_constant<int, kOneStepInFlight>{});
+    if constexpr (kLast) {
       if (step + 1 < step1) clear_tail(step + 1, an);
-      if (step + 3 < step1) load(step + 3, st);
-      substep(1, an, bn, 0, nothing);
     }
+    // (behind the last step this reads a stage that nothing uses)
+    substep(1, an, code_stage<T, G, kNext>(), 0, [&](int n) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = n * kL / kMF; q < (n + 1) * kL / kMF; ++q)
+        load_one<T, G, kSt, kLast>(p, step + 3, step1, wave, lane, q, off);
+    });
   };
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
   using C2 = std::integral_constant<int, 2>;
-  if (step0 < step1) {
-    load(step0, C0{});
-    if (step0 + 1 < step1) load(step0 + 1, C1{});
-    if (step0 + 2 < step1) load(step0 + 2, C2{});
-    meet(step1 - step0 - 1);
-    uint8_t* a = dy_stage<T, 0>();
-    clear_tail(step0, a);
 #pragma unroll
-    for (int i = 0; i < kI; ++i) read_x(code_stage<T, G, 0>(), 0, i);
+  for (int q = 0; q < kL; ++q) load_one<T, G, 0, true>(p, step0, step1, wave, lane, q, off);
 #pragma unroll
-    for (int r = 0; r < kR; ++r) read_dy(a, 0, 0, r / 2, r % 2);
+  for (int q = 0; q < kL; ++q) load_one<T, G, 1, true>(p, step0 + 1, step1, wave, lane, q, off);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) expand(0, e / 4, e % 4);
-  }
+  for (int q = 0; q < kL; ++q) load_one<T, G, 2, true>(p, step0 + 2, step1, wave, lane, q, off);
+  meet(std::integral_constant<int, kTwoStepsInFlight>{});
+  clear_tail(step0, dy_stage<T, 0>());
+#pragma unroll
+  for (int i = 0; i < kI; ++i) read_x(code_stage<T, G, 0>(), 0, i);
+#pragma unroll
+  for (int r = 0; r < kR; ++r) read_dy(dy_stage<T, 0>(), 0, 0, r / 2, r % 2);
+#pragma unroll
+  for (int e = 0; e < kE; ++e) expand(0, e / 4, e % 4);
   int step = step0;
   for (; step + 6 < step1; step += 3) {
-    run(step, C0{}, C1{}, std::true_type{});
-    run(step + 1, C1{}, C2{}, std::true_type{});
-    run(step + 2, C2{}, C0{}, std::true_type{});
+    run(step, C0{}, C1{}, std::false_type{});
+    run(step + 1, C1{}, C2{}, std::false_type{});
+    run(step + 2, C2{}, C0{}, std::false_type{});
   }
   for (; step < step1; step += 3) {
-    run(step, C0{}, C1{}, std::false_type{});
-    if (step + 1 < step1) run(step + 1, C1{}, C2{}, std::false_type{});
-    if (step + 2 < step1) run(step + 2, C2{}, C0{}, std::false_type{});
+    run(step, C0{}, C1{}, std::true_type{});
+    if (step + 1 < step1) run(step + 1, C1{}, C2{}, std::true_type{});
+    if (step + 2 < step1) run(step + 2, C2{}, C0{}, std::true_type{});
   }
+  __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);   // no load into the LDS outlives the block
 
   // Register 4 q + e of acc[i][j] is dW[n][k] with
   //   n = n0 + 32 (wn kJ + j) + lane % 32,  k = k0 + 32 (wk kI + i) + 8 q + 4 half + e.
