@@ -147,6 +147,12 @@ __device__ __forceinline__ void load_one(const WgradParams& p, int step, int ste
   }
 }
 
+// xcd_contiguous for 32-bit indexes.
+__device__ __forceinline__ uint32_t xcd_contiguous32(uint32_t b, uint32_t nb) {
+  const uint32_t q = nb / 8, r = nb % 8, xcd = b % 8, local = b / 8;
+  return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
+}
+
 // G = 0: one scale.
 template <class T, int kWK, int kJ, int kI, int G>
 __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p) {
@@ -157,14 +163,16 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
   // Tile order: an XCD takes a contiguous run; inside it eight k tiles are
   // walked for each n tile, so the 32 tiles an XCD works on at once share
   // about 4 dy panels and 8 code panels (half as wide) in its L2.
-  const int64_t tiles = (int64_t)p.n_tiles * p.k_tiles;
-  const int64_t order = xcd_contiguous(blockIdx.x, gridDim.x);
-  const int64_t part = order / tiles, local = order - part * tiles;
-  const int64_t band = local / (8 * (int64_t)p.n_tiles), first_k = 8 * band;
-  const int64_t wide = p.k_tiles - first_k < 8 ? p.k_tiles - first_k : 8;
-  const int64_t in_band = local - band * 8 * p.n_tiles;
-  const int64_t n0 = in_band / wide * kBN, k0 = (first_k + in_band % wide) * kBK;
-  const int step0 = (int)((int64_t)p.steps * part / p.splits), step1 = (int)((int64_t)p.steps * (part + 1) / p.splits);
+  // (32-bit numbers: a block's share of them is scalar work of a few cycles)
+  const uint32_t n_tiles = (uint32_t)p.n_tiles, k_tiles = (uint32_t)p.k_tiles, tiles = n_tiles * k_tiles;
+  const uint32_t order = (uint32_t)xcd_contiguous32(blockIdx.x, gridDim.x);
+  const uint32_t part = order / tiles, local = order - part * tiles;
+  const uint32_t band = local / (8 * n_tiles), first_k = 8 * band;
+  const uint32_t wide = k_tiles - first_k < 8 ? k_tiles - first_k : 8;
+  const uint32_t in_band = local - band * 8 * n_tiles, row = in_band / wide;
+  const int64_t n0 = (int64_t)row * kBN, k0 = (int64_t)(first_k + in_band - row * wide) * kBK;
+  const int step0 = p.splits == 1 ? 0 : (int)((int64_t)p.steps * part / p.splits);
+  const int step1 = p.splits == 1 ? p.steps : (int)((int64_t)p.steps * (part + 1) / p.splits);
 
   // Loads.  A wave-wide 16-byte load fills 1 KB of a panel, lane L at byte
   // 16 L; the swizzles act on the global side.  Rows past M re-load row M - 1
@@ -191,7 +199,7 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
   if constexpr (G != 0) {
 #pragma unroll
     for (int i = 0; i < S::kLS; ++i) {
-      const int64_t g = k0 / G + (S::kLS * wave + i) % S::kGroups;
+      const int64_t g = (uint32_t)k0 / G + (S::kLS * wave + i) % S::kGroups;
       off[T::kLA + T::kLB + i] =
           4u * ((uint32_t)lane * (uint32_t)p.groups + (uint32_t)(g < p.groups ? g : p.groups - 1));
     }
@@ -350,11 +358,16 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
     run(step + 1, C1{}, C2{}, std::false_type{});
     run(step + 2, C2{}, C0{}, std::false_type{});
   }
-  for (; step < step1; step += 3) {
-    run(step, C0{}, C1{}, std::true_type{});
-    if (step + 1 < step1) run(step + 1, C1{}, C2{}, std::true_type{});
-    if (step + 2 < step1) run(step + 2, C2{}, C0{}, std::true_type{});
-  }
+  // the last one to six steps, without a loop (where paths of different
+  // lengths meet, the compiler waits for every load)
+  auto last_steps = [&](auto self, int s, auto st, auto left) __attribute__((always_inline)) -> void {
+    constexpr int kSt = decltype(st)::value, kLeft = decltype(left)::value;
+    using Next = std::integral_constant<int, (kSt + 1) % 3>;
+    if (s >= step1) return;
+    run(s, st, Next{}, std::true_type{});
+    if constexpr (kLeft > 1) self(self, s + 1, Next{}, std::integral_constant<int, kLeft - 1>{});
+  };
+  last_steps(last_steps, step, C0{}, std::integral_constant<int, 6>{});
   __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);   // no load into the LDS outlives the block
 
   // Register 4 q + e of acc[i][j] is dW[n][k] with
@@ -418,8 +431,8 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* partials, 
 
 // No rows: the empty sum.
 __global__ __launch_bounds__(256) void wgrad_zero_kernel(void* dw, int64_t bytes) {
-  const int64_t at = 16 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-  if (at < bytes) *reinterpret_cast<uint4*>((uint8_t*)dw + at) = make_uint4(0, 0, 0, 0);
+  for (int64_t at = 16 * ((int64_t)blockIdx.x * 256 + threadIdx.x); at < bytes; at += 4096 * (int64_t)gridDim.x)
+    *reinterpret_cast<uint4*>((uint8_t*)dw + at) = make_uint4(0, 0, 0, 0);
 }
 
 using Large = Tile<2, 4, 4, 2>;   // 256 x 256, eight waves of 128 x 64
@@ -441,6 +454,7 @@ const void* wgrad_kernel_for(bool large, int32_t g) {
 }
 
 constexpr int64_t kMaxDim = 1 << 24;     // 64 rows of dy stay below 2^32 bytes
+constexpr int64_t kMaxTiles = 1 << 23;   // of 128 x 128: a launch's threads stay below 2^32
 constexpr int64_t kUnits = 256;          // compute units of the device the split is made for
 
 struct Plan {
@@ -474,7 +488,7 @@ Plan plan(int64_t M, int64_t N, int64_t K) {
 bool wgrad_sizes_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 0 && N >= 0 && K >= 0 && N % 16 == 0 && K % 16 == 0 && N <= kMaxDim && K <= kMaxDim &&
          M <= (int64_t)kStep * 0x7FFFFFF0 && (N == 0 || K <= INT64_MAX / 8 / N) &&
-         (N + 127) / 128 * ((K + 127) / 128) <= 0x7FFFFFFF;
+         (N + 127) / 128 * ((K + 127) / 128) <= kMaxTiles;
 }
 
 }  // namespace
@@ -508,10 +522,10 @@ coat_status_t coat_fp8_weight_grad(const coat_weight_grad_args_t* a, hipStream_t
   if (M == 0) {
     if (out == kF32Add) return COAT_OK;
     int64_t bytes = N * K * (a->dw_bf16 ? 2 : 4);
-    if (bytes / 4096 > 0x7FFFFFF0) return COAT_ERR_INVALID_VALUE;
+    const int64_t blocks = (bytes + 4095) / 4096;
     void* args[] = {&dw, &bytes};
-    e = hipLaunchKernel(reinterpret_cast<const void*>(&wgrad_zero_kernel), dim3((unsigned)((bytes + 4095) / 4096)),
-                        dim3(256), args, 0, stream);
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&wgrad_zero_kernel),
+                        dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), args, 0, stream);
     return e == hipSuccess ? COAT_OK : hip_fail(e);
   }
   const Plan pl = plan(M, N, K);

@@ -167,7 +167,7 @@ WGRAD = dict(dy=A, x_codes=A, x_scales=A, dw_bf16=A, M=4096, N=256, K=256, group
     (dict(K=144), INVAL), (dict(group_size=256), GSIZE), (dict(x_scales=None), INVAL), (dict(dw_f32=A), INVAL),
     (dict(accumulate=1), INVAL), (dict(workspace_bytes=64), INVAL), (dict(workspace=None), NULLP),
     (dict(dw_bf16=None), NULLP), (dict(dy=None), NULLP), (dict(x_codes=None), NULLP), (dict(M=1 << 50), INVAL),
-    (dict(N=0), OK), (dict(K=0), OK)] +
+    (dict(N=1 << 24, K=1 << 24), INVAL), (dict(N=0), OK), (dict(K=0), OK)] +
     [({n: A + 2}, MISAL) for n in ("dy", "x_codes", "x_scales", "dw_bf16", "workspace")] +
     [(dict(dw_bf16=None, dw_f32=A + 8), MISAL), (dict(M=0, accumulate=1, dw_bf16=None, dw_f32=A), OK)])
 def test_weight_grad(coat, change, status):
