@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -73,6 +74,17 @@ def _fields(spec: str):
     types = {"ptr": _vp, "f32": _f32, "i32": _i32, "i64": _i64}
     return [(name, types[kind.strip()]) for part in spec.split(",")
             for kind, names in [part.split(":")] for name in names.split()]
+
+
+def _packer(structure):
+    """A function that packs a structure's values, in the order of its fields,
+    into bytes of the same layout (in a quarter of the time that building the
+    ctypes structure takes, which a small kernel would wait for)."""
+    codes = {_vp: "P", _f32: "f", _i32: "i", _i64: "q"}
+    flat = []
+    for _, t in structure._fields_:
+        flat += [u for _, u in t._fields_] if issubclass(t, ctypes.Structure) else [t]
+    return struct.Struct("@" + "".join(codes[t] for t in flat)).pack
 
 
 class RMSNormArgs(ctypes.Structure):
@@ -137,12 +149,10 @@ def _load(path: str = LIB_PATH):
     lib.coat_fp8_gemm_group_quant.argtypes = [vp, vp, f32, f32, i64, i64, i64, i32, vp, vp, vp, vp]
     lib.coat_fp8_gemm_bf16.restype = ctypes.c_int
     lib.coat_fp8_gemm_bf16.argtypes = [vp, vp, f32, f32, i64, i64, i64, vp, vp]
-    for name, args in (("rms_norm", RMSNormArgs), ("rms_norm_bwd", RMSNormBwdArgs),
-                       ("swiglu", SwigluArgs), ("qk_norm_rope", QkNormRopeArgs),
-                       ("qk_norm_rope_bwd", QkNormRopeBwdArgs), ("weight_grad", WeightGradArgs)):
+    for name in ("rms_norm", "rms_norm_bwd", "swiglu", "qk_norm_rope", "qk_norm_rope_bwd", "weight_grad"):
         fn = getattr(lib, f"coat_fp8_{name}")
         fn.restype = ctypes.c_int
-        fn.argtypes = [ctypes.POINTER(args), vp]
+        fn.argtypes = [vp, vp]   # a structure by reference, or its packed bytes
     lib.coat_fp8_swiglu_bwd.restype = ctypes.c_int
     lib.coat_fp8_swiglu_bwd.argtypes = [vp, vp, vp, i64, i64, i32, vp, vp]
     lib.coat_fp8_rms_norm_bwd_workspace.restype = i64
@@ -421,15 +431,60 @@ def gemm_bf16(a: torch.Tensor, b: torch.Tensor, a_scale: float, b_scale: float,
 
 # ------------------------------------------------- activation checkpoints
 
+_pack_rms_norm, _pack_rms_norm_bwd = _packer(RMSNormArgs), _packer(RMSNormBwdArgs)
+_pack_swiglu, _pack_weight_grad = _packer(SwigluArgs), _packer(WeightGradArgs)
+_pack_qk, _pack_qk_bwd = _packer(QkNormRopeArgs), _packer(QkNormRopeBwdArgs)
+CODES, BF16, F32 = CODE_DTYPES, BF16_DTYPES, F32_DTYPES
+
+
+def _addresses(buffers, heads=()):
+    """Addresses (0 for None) of `buffers`, (tensor, name, dtypes, least number
+    of values) each, then of `heads` (checked by _heads but for the device),
+    (tensor, name) each, after the checks of _need and _on_device; and the
+    raw handle of torch's current stream.  One pass over what is right; what
+    is not is gone through again for its message."""
+    out = []
+    dev = None
+    try:
+        for t, _, dtypes, n in buffers:
+            if t is None:
+                out.append(0)
+                continue
+            d = t.get_device()
+            if d != dev:
+                if dev is not None or d < 0 or d != torch._C._cuda_getDevice():
+                    return _refuse(buffers, heads)
+                dev = d
+            if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < n:
+                return _refuse(buffers, heads)
+            out.append(t.data_ptr())
+        for t, _ in heads:
+            if t.get_device() != dev:
+                return _refuse(buffers, heads)
+            out.append(t.data_ptr())
+    except AttributeError:   # not a tensor
+        return _refuse(buffers, heads)
+    return out, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _refuse(buffers, heads):
+    for t, name, dtypes, n in buffers:
+        if t is not None:
+            _need(t, name, dtypes, n)
+    _on_device(**{b[1]: b[0] for b in buffers}, **dict((name, t) for t, name in heads))
+    raise ValueError("no buffer on the current device")
+
+
+def _launch(fn, packed: bytes, stream, current):
+    status = fn(packed, current if stream is None else _stream(stream))
+    if status != COAT_OK:
+        _check(status)
+
+
 def _shape2(t, name: str):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D tensor")
     return t.shape
-
-
-def _opt(t, name: str, dtypes, min_numel: int):
-    if t is not None:
-        _need(t, name, dtypes, min_numel)
 
 
 def _groups(cols: int, group_size: int) -> int:
@@ -448,22 +503,12 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, *, y: Optional[t
     the rows' reciprocal root mean squares, for rms_norm_bwd."""
     rows, cols = _shape2(x, "x")
     n = rows * cols
-    _need(x, "x", BF16_DTYPES, 0)
-    _need(weight, "weight", BF16_DTYPES, cols)
-    _opt(residual, "residual", BF16_DTYPES, n)
-    _opt(residual_out, "residual_out", BF16_DTYPES, n)
-    _opt(y, "y", BF16_DTYPES, n)
-    _opt(y_codes, "y_codes", CODE_DTYPES, n)
-    _opt(y_amax, "y_amax", F32_DTYPES, 1)
-    _opt(codes, "codes", CODE_DTYPES, n)
-    _opt(scales, "scales", F32_DTYPES, rows * _groups(cols, group_size))
-    _opt(rstd, "rstd", F32_DTYPES, rows)
-    _on_device(x=x, weight=weight, residual=residual, residual_out=residual_out, y=y, y_codes=y_codes,
-               y_amax=y_amax, codes=codes, scales=scales, rstd=rstd)
-    a = RMSNormArgs(_ptr(x), _ptr(residual), _ptr(weight), _ptr(residual_out), _ptr(y), _ptr(y_codes),
-                    _ptr(y_amax), _ptr(codes), _ptr(scales), _ptr(rstd), rows, cols, eps, y_scale,
-                    group_size)
-    _check(lib.coat_fp8_rms_norm(ctypes.byref(a), _stream(stream)))
+    p, current = _addresses((
+        (x, "x", BF16, 0), (residual, "residual", BF16, n), (weight, "weight", BF16, cols),
+        (residual_out, "residual_out", BF16, n), (y, "y", BF16, n), (y_codes, "y_codes", CODES, n),
+        (y_amax, "y_amax", F32, 1), (codes, "codes", CODES, n),
+        (scales, "scales", F32, rows * _groups(cols, group_size)), (rstd, "rstd", F32, rows)))
+    _launch(lib.coat_fp8_rms_norm, _pack_rms_norm(*p, rows, cols, eps, y_scale, group_size), stream, current)
 
 
 def rms_norm_bwd_workspace(rows: int, cols: int) -> int:
@@ -477,19 +522,26 @@ def _workspace_bytes(n: int) -> int:
     return n
 
 
-def _workspace(workspace, need: bool, nbytes: int):
-    """Address and size of the workspace: a byte count of `nbytes` is required
-    where `need`."""
+def _workspace(workspace, nbytes: int) -> int:
+    """The workspace's size in bytes; at least nbytes."""
     if workspace is None:
-        if need and nbytes > 0:
+        if nbytes > 0:
             raise ValueError(f"workspace is required ({nbytes} bytes)")
-        return None, 0
+        return 0
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous torch.Tensor")
-    have = workspace.numel() * workspace.element_size()
-    if need and have < nbytes:
+    have = workspace.nbytes
+    if have < nbytes:
         raise ValueError(f"workspace holds {have} bytes, needs at least {nbytes}")
-    return workspace.data_ptr(), have
+    return have
+
+
+class _AnyDtype:
+    def __contains__(self, dtype):
+        return True
+
+
+ANY = _AnyDtype()   # the workspace's dtype does not matter
 
 
 def rms_norm_bwd(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, rstd: torch.Tensor,
@@ -501,21 +553,14 @@ def rms_norm_bwd(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, rs
     rms_norm_bwd_workspace(rows, cols) bytes of workspace)."""
     rows, cols = _shape2(dy, "dy")
     n = rows * cols
-    _need(dy, "dy", BF16_DTYPES, 0)
-    _need(codes, "codes", CODE_DTYPES, n)
-    _need(scales, "scales", F32_DTYPES, rows * _groups(cols, group_size))
-    _need(rstd, "rstd", F32_DTYPES, rows)
-    _need(weight, "weight", BF16_DTYPES, cols)
-    _need(dx, "dx", BF16_DTYPES, n)
-    _opt(dw, "dw", F32_DTYPES, cols)
-    _opt(d_residual, "d_residual", BF16_DTYPES, n)
-    need = dw is not None
-    ws, ws_bytes = _workspace(workspace, need, rms_norm_bwd_workspace(rows, cols) if need else 0)
-    _on_device(dy=dy, codes=codes, scales=scales, rstd=rstd, weight=weight, dx=dx, dw=dw,
-               d_residual=d_residual, workspace=workspace)
-    a = RMSNormBwdArgs(_ptr(dy), _ptr(codes), _ptr(scales), _ptr(rstd), _ptr(weight), _ptr(d_residual),
-                       _ptr(dx), _ptr(dw), ws, ws_bytes, rows, cols, group_size, int(accumulate))
-    _check(lib.coat_fp8_rms_norm_bwd(ctypes.byref(a), _stream(stream)))
+    ws_bytes = _workspace(workspace, rms_norm_bwd_workspace(rows, cols) if dw is not None else 0)
+    p, current = _addresses((
+        (dy, "dy", BF16, 0), (codes, "codes", CODES, n),
+        (scales, "scales", F32, rows * _groups(cols, group_size)), (rstd, "rstd", F32, rows),
+        (weight, "weight", BF16, cols), (d_residual, "d_residual", BF16, n), (dx, "dx", BF16, n),
+        (dw, "dw", F32, cols), (workspace, "workspace", ANY, 0)))
+    _launch(lib.coat_fp8_rms_norm_bwd,
+            _pack_rms_norm_bwd(*p, ws_bytes, rows, cols, group_size, accumulate), stream, current)
 
 
 def swiglu(codes: Optional[torch.Tensor], scales: Optional[torch.Tensor], *,
@@ -527,20 +572,15 @@ def swiglu(codes: Optional[torch.Tensor], scales: Optional[torch.Tensor], *,
     h_amax is raised to the largest |h|).  The input is the checkpoint codes,
     scales; or gate_up (BF16), whose checkpoint is then written to codes and
     scales if they are given."""
-    rows, wide = _shape2(codes if gate_up is None else gate_up, "codes" if gate_up is None else "gate_up")
+    rows, wide = _shape2(codes, "codes") if gate_up is None else _shape2(gate_up, "gate_up")
     if wide % 2:
         raise ValueError("a row holds the gates and as many ups: its length is even")
     cols = wide // 2
-    _opt(gate_up, "gate_up", BF16_DTYPES, 0)
-    _opt(codes, "codes", CODE_DTYPES, rows * wide)
-    _opt(scales, "scales", F32_DTYPES, 2 * rows * _groups(cols, group_size))
-    _opt(h, "h", BF16_DTYPES, rows * cols)
-    _opt(h_codes, "h_codes", CODE_DTYPES, rows * cols)
-    _opt(h_amax, "h_amax", F32_DTYPES, 1)
-    _on_device(gate_up=gate_up, codes=codes, scales=scales, h=h, h_codes=h_codes, h_amax=h_amax)
-    a = SwigluArgs(_ptr(gate_up), _ptr(codes), _ptr(scales), _ptr(h), _ptr(h_codes), _ptr(h_amax), rows,
-                   cols, h_scale, group_size)
-    _check(lib.coat_fp8_swiglu(ctypes.byref(a), _stream(stream)))
+    p, current = _addresses((
+        (gate_up, "gate_up", BF16, 0), (codes, "codes", CODES, rows * wide),
+        (scales, "scales", F32, 2 * rows * _groups(cols, group_size)), (h, "h", BF16, rows * cols),
+        (h_codes, "h_codes", CODES, rows * cols), (h_amax, "h_amax", F32, 1)))
+    _launch(lib.coat_fp8_swiglu, _pack_swiglu(*p, rows, cols, h_scale, group_size), stream, current)
 
 
 def swiglu_bwd(dh: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, d_gate_up: torch.Tensor,
@@ -548,13 +588,12 @@ def swiglu_bwd(dh: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, d_ga
     """Gradient of swiglu from its checkpoint: d_gate_up (BF16), the gates'
     gradients first in each row."""
     rows, cols = _shape2(dh, "dh")
-    _need(dh, "dh", BF16_DTYPES, 0)
-    _need(codes, "codes", CODE_DTYPES, 2 * rows * cols)
-    _need(scales, "scales", F32_DTYPES, 2 * rows * _groups(cols, group_size))
-    _need(d_gate_up, "d_gate_up", BF16_DTYPES, 2 * rows * cols)
-    _on_device(dh=dh, codes=codes, scales=scales, d_gate_up=d_gate_up)
-    _check(lib.coat_fp8_swiglu_bwd(_ptr(dh), _ptr(codes), _ptr(scales), rows, cols, group_size,
-                                   _ptr(d_gate_up), _stream(stream)))
+    (a, b, c, d), current = _addresses((
+        (dh, "dh", BF16, 0), (codes, "codes", CODES, 2 * rows * cols),
+        (scales, "scales", F32, 2 * rows * _groups(cols, group_size)),
+        (d_gate_up, "d_gate_up", BF16, 2 * rows * cols)))
+    _check(lib.coat_fp8_swiglu_bwd(a, b, c, rows, cols, group_size, d,
+                                   current if stream is None else _stream(stream)))
 
 
 def _heads(t: torch.Tensor, name: str, like=None):
@@ -564,30 +603,33 @@ def _heads(t: torch.Tensor, name: str, like=None):
         raise ValueError(f"{name} must be a 3-D (tokens, heads, head_dim) tensor")
     if t.dtype not in BF16_DTYPES:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {BF16_DTYPES}")
-    tokens, heads, dim = t.shape
-    if like is not None and tuple(t.shape) != tuple(like.shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
-    stride = t.stride(0) if tokens > 1 else heads * dim
-    if t.numel() and ((dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim)
-                      or stride < heads * dim):
+    shape = t.shape
+    tokens, heads, dim = shape
+    if like is not None and shape != like:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected {tuple(like)}")
+    s0, s1, s2 = t.stride()
+    if tokens <= 1:
+        s0 = heads * dim
+    if tokens and heads and dim and ((dim > 1 and s2 != 1) or (heads > 1 and s1 != dim) or s0 < heads * dim):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return tokens, heads, dim, stride
+    return tokens, heads, dim, s0
 
 
-def _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, group_size, names):
-    tokens, q_heads, dim, _ = _heads(q, names[0])
-    k_tokens, k_heads, k_dim, _ = _heads(k, names[1])
+def _qk_sizes(q, k, q_other, k_other, cos, sin, names):
+    """Sizes and strides that both passes take from their heads and tables."""
+    tokens, q_heads, dim, q_stride = _heads(q, names[0])
+    k_tokens, k_heads, k_dim, k_stride = _heads(k, names[1])
     if k_tokens != tokens or k_dim != dim:
         raise ValueError(f"{names[0]} and {names[1]} disagree on tokens or head_dim")
+    q_other_stride = _heads(q_other, names[2], q.shape)[3]
+    k_other_stride = _heads(k_other, names[3], k.shape)[3]
     table_rows, half = _shape2(cos, "cos")
-    if tuple(_shape2(sin, "sin")) != (table_rows, half):
+    if _shape2(sin, "sin") != cos.shape:
         raise ValueError("cos and sin differ in shape")
-    _need(cos, "cos", F32_DTYPES, 0)
-    _need(sin, "sin", F32_DTYPES, 0)
-    _need(q_weight, "q_weight", BF16_DTYPES, dim)
-    _need(k_weight, "k_weight", BF16_DTYPES, dim)
-    _need(positions, "positions", (torch.int64,), tokens)
-    return QkShape(tokens, table_rows, q_heads, k_heads, dim, 2 * half, int(interleaved), group_size)
+    return tokens, q_heads, k_heads, dim, table_rows, 2 * half, q_stride, k_stride, q_other_stride, k_other_stride
+
+
+I64_DTYPES = (torch.int64,)
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
@@ -601,19 +643,17 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
     q and k.  codes, scales and rstd, if given, receive the checkpoint (the
     query heads of a token, then its key heads).  Tokens whose position is
     outside the tables are padding and get zeros."""
-    s = _qk_shape(q, k, q_weight, k_weight, cos, sin, positions, interleaved, group_size, ("q", "k"))
-    q_stride, k_stride = _heads(q, "q")[3], _heads(k, "k")[3]
-    q_out_stride, k_out_stride = _heads(q_out, "q_out", q)[3], _heads(k_out, "k_out", k)[3]
-    rows = s.tokens * (s.q_heads + s.k_heads)
-    _opt(codes, "codes", CODE_DTYPES, rows * s.head_dim)
-    _opt(scales, "scales", F32_DTYPES, rows * _groups(s.head_dim, group_size))
-    _opt(rstd, "rstd", F32_DTYPES, rows)
-    _on_device(q=q, k=k, q_weight=q_weight, k_weight=k_weight, cos=cos, sin=sin, positions=positions,
-               q_out=q_out, k_out=k_out, codes=codes, scales=scales, rstd=rstd)
-    a = QkNormRopeArgs(s, _ptr(q), _ptr(k), q_stride, k_stride, _ptr(q_weight), _ptr(k_weight), _ptr(cos),
-                       _ptr(sin), _ptr(positions), _ptr(q_out), _ptr(k_out), q_out_stride, k_out_stride,
-                       _ptr(codes), _ptr(scales), _ptr(rstd), eps)
-    _check(lib.coat_fp8_qk_norm_rope(ctypes.byref(a), _stream(stream)))
+    tokens, q_heads, k_heads, dim, table, rot, qs, ks, qos, kos = _qk_sizes(
+        q, k, q_out, k_out, cos, sin, ("q", "k", "q_out", "k_out"))
+    rows = tokens * (q_heads + k_heads)
+    (wq, wk, c, s, pos, pc, ps, pr, pq, pk, pqo, pko), current = _addresses((
+        (q_weight, "q_weight", BF16, dim), (k_weight, "k_weight", BF16, dim), (cos, "cos", F32, 0),
+        (sin, "sin", F32, 0), (positions, "positions", I64_DTYPES, tokens), (codes, "codes", CODES, rows * dim),
+        (scales, "scales", F32, rows * _groups(dim, group_size)), (rstd, "rstd", F32, rows)),
+        ((q, "q"), (k, "k"), (q_out, "q_out"), (k_out, "k_out")))
+    _launch(lib.coat_fp8_qk_norm_rope,
+            _pack_qk(tokens, table, q_heads, k_heads, dim, rot, interleaved, group_size, pq, pk, qs, ks, wq, wk, c, s,
+                     pos, pqo, pko, qos, kos, pc, ps, pr, eps), stream, current)
 
 
 def qk_norm_rope_bwd_workspace(tokens: int, heads: int, head_dim: int) -> int:
@@ -632,27 +672,20 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, codes: torch.Te
     """Gradient of qk_norm_rope from its checkpoint: dq and dk (BF16; they may
     be dq_out and dk_out) and, if given, dq_weight and dk_weight (FP32,
     written or accumulated; need qk_norm_rope_bwd_workspace bytes)."""
-    s = _qk_shape(dq_out, dk_out, q_weight, k_weight, cos, sin, positions, interleaved, group_size,
-                  ("dq_out", "dk_out"))
-    dq_out_stride, dk_out_stride = _heads(dq_out, "dq_out")[3], _heads(dk_out, "dk_out")[3]
-    dq_stride, dk_stride = _heads(dq, "dq", dq_out)[3], _heads(dk, "dk", dk_out)[3]
-    heads = s.q_heads + s.k_heads
-    _need(codes, "codes", CODE_DTYPES, s.tokens * heads * s.head_dim)
-    _need(scales, "scales", F32_DTYPES, s.tokens * heads * _groups(s.head_dim, group_size))
-    _need(rstd, "rstd", F32_DTYPES, s.tokens * heads)
-    _opt(dq_weight, "dq_weight", F32_DTYPES, s.head_dim)
-    _opt(dk_weight, "dk_weight", F32_DTYPES, s.head_dim)
-    need = dq_weight is not None
-    ws, ws_bytes = _workspace(workspace, need, qk_norm_rope_bwd_workspace(s.tokens, heads, s.head_dim)
-                              if need else 0)
-    _on_device(dq_out=dq_out, dk_out=dk_out, codes=codes, scales=scales, rstd=rstd, q_weight=q_weight,
-               k_weight=k_weight, cos=cos, sin=sin, positions=positions, dq=dq, dk=dk,
-               dq_weight=dq_weight, dk_weight=dk_weight, workspace=workspace)
-    a = QkNormRopeBwdArgs(s, _ptr(dq_out), _ptr(dk_out), dq_out_stride, dk_out_stride, _ptr(codes),
-                          _ptr(scales), _ptr(rstd), _ptr(q_weight), _ptr(k_weight), _ptr(cos), _ptr(sin),
-                          _ptr(positions), _ptr(dq), _ptr(dk), dq_stride, dk_stride, _ptr(dq_weight),
-                          _ptr(dk_weight), ws, ws_bytes, int(accumulate))
-    _check(lib.coat_fp8_qk_norm_rope_bwd(ctypes.byref(a), _stream(stream)))
+    tokens, q_heads, k_heads, dim, table, rot, qos, kos, qs, ks = _qk_sizes(
+        dq_out, dk_out, dq, dk, cos, sin, ("dq_out", "dk_out", "dq", "dk"))
+    rows = tokens * (q_heads + k_heads)
+    ws_bytes = _workspace(workspace, qk_norm_rope_bwd_workspace(tokens, q_heads + k_heads, dim)
+                          if dq_weight is not None else 0)
+    (pc, ps, pr, wq, wk, c, s, pos, dwq, dwk, ws, pqo, pko, pq, pk), current = _addresses((
+        (codes, "codes", CODES, rows * dim), (scales, "scales", F32, rows * _groups(dim, group_size)),
+        (rstd, "rstd", F32, rows), (q_weight, "q_weight", BF16, dim), (k_weight, "k_weight", BF16, dim),
+        (cos, "cos", F32, 0), (sin, "sin", F32, 0), (positions, "positions", I64_DTYPES, tokens),
+        (dq_weight, "dq_weight", F32, dim), (dk_weight, "dk_weight", F32, dim), (workspace, "workspace", ANY, 0)),
+        ((dq_out, "dq_out"), (dk_out, "dk_out"), (dq, "dq"), (dk, "dk")))
+    _launch(lib.coat_fp8_qk_norm_rope_bwd,
+            _pack_qk_bwd(tokens, table, q_heads, k_heads, dim, rot, interleaved, group_size, pqo, pko, qos, kos, pc, ps,
+                         pr, wq, wk, c, s, pos, pq, pk, qs, ks, dwq, dwk, ws, ws_bytes, accumulate), stream, current)
 
 
 def weight_grad_workspace(rows: int, n: int, k: int) -> int:
@@ -671,18 +704,22 @@ def weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales, dw: torch.Tensor,
     x_rows, k = _shape2(codes, "codes")
     if x_rows != rows:
         raise ValueError("dy and codes disagree on the rows")
-    grouped = isinstance(scales, torch.Tensor)
-    _need(dy, "dy", BF16_DTYPES, 0)
-    _need(codes, "codes", CODE_DTYPES, 0)
-    if grouped:
-        _need(scales, "scales", F32_DTYPES, rows * _groups(k, group_size))
-    elif not isinstance(scales, (int, float)):
+    grouped, x_scale = None, 1.0
+    if isinstance(scales, torch.Tensor):
+        grouped = scales
+    elif isinstance(scales, (int, float)):
+        x_scale = scales
+    else:
         raise ValueError("scales must be a float32 tensor or a number")
-    _need(dw, "dw", BF16_DTYPES + F32_DTYPES, n * k)
-    ws, ws_bytes = _workspace(workspace, True, weight_grad_workspace(rows, n, k))
-    _on_device(dy=dy, codes=codes, scales=scales if grouped else None, dw=dw, workspace=workspace)
+    ws_bytes = _workspace(workspace, weight_grad_workspace(rows, n, k))
+    (py, px, ps, pw, ws), current = _addresses((
+        (dy, "dy", BF16, 0), (codes, "codes", CODES, 0),
+        (grouped, "scales", F32, rows * _groups(k, group_size)), (dw, "dw", DW_DTYPES, n * k),
+        (workspace, "workspace", ANY, 0)))
     f32 = dw.dtype == torch.float32
-    a = WeightGradArgs(_ptr(dy), _ptr(codes), _ptr(scales) if grouped else None, None if f32 else _ptr(dw),
-                       _ptr(dw) if f32 else None, ws, ws_bytes, rows, n, k, 1.0 if grouped else scales,
-                       group_size, int(accumulate))
-    _check(lib.coat_fp8_weight_grad(ctypes.byref(a), _stream(stream)))
+    _launch(lib.coat_fp8_weight_grad,
+            _pack_weight_grad(py, px, ps, 0 if f32 else pw, pw if f32 else 0, ws, ws_bytes, rows, n, k, x_scale,
+                              group_size, accumulate), stream, current)
+
+
+DW_DTYPES = BF16_DTYPES + F32_DTYPES
