@@ -25,8 +25,10 @@ namespace {
 //   h = bf16(x + residual),  rstd = (mean(h^2) + eps)^-1/2,  y = h rstd w
 //
 // One block takes one row at a time and keeps it in registers: chunk i of
-// thread t is the eight columns from 8 (t + kThreads i), so every byte is
-// read and written once.  The weight's chunks stay in registers over the
+// thread t is the eight columns from 8 (t + blockDim i), so every byte is
+// read and written once (past 16384 columns the row no longer fits, and is
+// read again from the L2).  A block has as many waves as kC chunks a thread
+// need for the row (kMost: the most threads of an instance).  The weight's chunks stay in registers over the
 // rows of a block, and the next row is loaded before the current one is
 // reduced.  The sum of squares is FP32: eight values of a lane in order,
 // then lanes, then waves (LDS, two slots in turn, one barrier a row).  A
@@ -51,49 +53,81 @@ struct NormParams {
   float eps, inv_y_scale, inv_cols;
 };
 
+// Element `col` of a row that starts at the uniform address `row`: a scalar
+// base and a 32-bit offset, which takes one register a lane and not two for
+// each array.
+template <class V>
+__device__ __forceinline__ V* at(V* row, int col) {
+  return reinterpret_cast<V*>(reinterpret_cast<uintptr_t>(row) + (uint32_t)col * (uint32_t)sizeof(V));
+}
+
+// Chunks of a row that is read once, or twice (then the second time is from
+// the L2).
+template <bool kOnce>
+__device__ __forceinline__ uint4 load_row16(const void* p) {
+  return kOnce ? load_stream16(p) : *reinterpret_cast<const uint4*>(p);
+}
+
+template <bool kOnce>
+__device__ __forceinline__ uint2 load_row8(const void* p) {
+  return kOnce ? load_stream8(p) : *reinterpret_cast<const uint2*>(p);
+}
+
 // The block's sum of v (every thread gets it).  `slot` alternates between
 // calls: a wave can be at most one barrier ahead of another.
-template <int kThreads>
+template <int kMost>
 __device__ __forceinline__ float block_sum(float v, int slot) {
   v = lanes_sum<64>(v);
-  if constexpr (kThreads > 64) {
-    constexpr int kWaves = kThreads / 64;
+  if constexpr (kMost > 64) {
+    constexpr int kWaves = kMost / 64;
     __shared__ float part[2][kWaves];
+    const int waves = blockDim.x >> 6;
     if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = v;
     __syncthreads();
     v = part[slot][0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += part[slot][w];
+    for (int w = 1; w < kWaves; ++w) v += w < waves ? part[slot][w] : 0.0f;
   }
   return v;
 }
 
-template <int kThreads, int kC>
-__global__ __launch_bounds__(kThreads) void rms_norm_kernel(const NormParams p) {
-  const int t = threadIdx.x;
+template <int kMost, int kC>
+__global__ __launch_bounds__(kMost) void rms_norm_kernel(const NormParams p) {
+  const int t = threadIdx.x, threads = blockDim.x;
   const int cols = p.cols, lanes = 1 << (p.group_shift - 3);
   bool ok[kC];
   int col[kC];
   uint4 w[kC], next[kC], nres[kC];
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
-    col[i] = 8 * (t + kThreads * i);
+    col[i] = 8 * (t + threads * i);
     ok[i] = col[i] < cols;
     w[i] = next[i] = nres[i] = make_uint4(0, 0, 0, 0);
   }
-  auto load = [&](int64_t row) __attribute__((always_inline)) {
+  constexpr bool kKeep = kC <= 2;   // else each phase loads a chunk when it comes to it
+  auto load = [&](int64_t row, int i) __attribute__((always_inline)) {
+    if (!ok[i]) return;
+    next[i] = load_row16<kKeep>(at(p.x + row * cols, col[i]));
+    if (p.residual) nres[i] = load_row16<kKeep>(at(p.residual + row * cols, col[i]));
+  };
+  auto load_weight = [&](int i) __attribute__((always_inline)) {
+    if (ok[i]) w[i] = *reinterpret_cast<const uint4*>(at(p.weight, col[i]));
+  };
+  // the chunk as everything but the sum reads it: as it is stored
+  auto stored = [&](int i) __attribute__((always_inline)) {
+    if (!p.residual) return next[i];
+    float f[8], r[8];
+    unpack8(next[i], f);
+    unpack8(nres[i], r);
 #pragma unroll
-    for (int i = 0; i < kC; ++i)
-      if (ok[i]) {
-        next[i] = load_stream16(p.x + row * cols + col[i]);
-        if (p.residual) nres[i] = load_stream16(p.residual + row * cols + col[i]);
-      }
+    for (int e = 0; e < 8; ++e) f[e] += r[e];
+    return pack8(f);
   };
   int64_t row = blockIdx.x;
-  load(row);
+  if (kKeep) {
 #pragma unroll
-  for (int i = 0; i < kC; ++i)
-    if (ok[i]) w[i] = *reinterpret_cast<const uint4*>(p.weight + col[i]);
+    for (int i = 0; i < kC; ++i) load(row, i), load_weight(i);
+  }
 
   float top = 0.0f;
   int slot = 0;
@@ -103,41 +137,42 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const NormParams p) 
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       float f[8];
-      raw[i] = next[i];
-      if (p.residual) {
-        float r[8];
-        unpack8(raw[i], f);
-        unpack8(nres[i], r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] += r[e];
-        raw[i] = pack8(f);   // everything below reads the sum as it is stored
-      }
+      if (!kKeep) load(row, i);
+      raw[i] = stored(i);
       unpack8(raw[i], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
     }
-    if (row + gridDim.x < p.rows) load(row + gridDim.x);
-    const float rstd = 1.0f / sqrtf(__builtin_fmaf(block_sum<kThreads>(ss, slot), p.inv_cols, p.eps));
+    if (kKeep && row + gridDim.x < p.rows) {
+#pragma unroll
+      for (int i = 0; i < kC; ++i) load(row + gridDim.x, i);
+    }
+    const float rstd = 1.0f / sqrtf(__builtin_fmaf(block_sum<kMost>(ss, slot), p.inv_cols, p.eps));
     if (p.rstd && t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      const int64_t at = row * cols + col[i];
+      const int64_t start = row * cols;
+      if (!kKeep) {
+        load(row, i), load_weight(i);
+        raw[i] = stored(i);
+      }
       if (p.codes) {   // all lanes: groups exchange their maxima
         float scale;
         const uint2 c = checkpoint8(raw[i], lanes, scale);
         if (ok[i]) {
-          store_stream8(p.codes + at, c);
-          if (((t + kThreads * i) & (lanes - 1)) == 0) p.scales[at >> p.group_shift] = scale;
+          store_stream8(at(p.codes + start, col[i]), c);
+          if (((t + threads * i) & (lanes - 1)) == 0)
+            *at(p.scales + (start >> p.group_shift), col[i] >> p.group_shift) = scale;
         }
       }
       if (!ok[i]) continue;
-      if (p.sum) store_stream16(p.sum + at, raw[i]);
+      if (p.sum) store_stream16(at(p.sum + start, col[i]), raw[i]);
       float f[8], g[8];
       unpack8(raw[i], f);
       unpack8(w[i], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = f[e] * rstd * g[e];
-      if (p.y) store_stream16(p.y + at, pack8(f));
+      if (p.y) store_stream16(at(p.y + start, col[i]), pack8(f));
       if (p.y_codes) {
         const float m = max_mag(f);
         top = fmaxf(top, m);
@@ -145,7 +180,7 @@ __global__ __launch_bounds__(kThreads) void rms_norm_kernel(const NormParams p) 
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] *= p.inv_y_scale;
         e4m3_pack(f, m * p.inv_y_scale, c);
-        store_stream8(p.y_codes + at, make_uint2(c[0], c[1]));
+        store_stream8(at(p.y_codes + start, col[i]), make_uint2(c[0], c[1]));
       }
     }
   }
@@ -178,18 +213,18 @@ struct NormBwdParams {
   float inv_cols;
 };
 
-template <int kThreads, int kC>
-__global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const NormBwdParams p) {
-  const int t = threadIdx.x;
+template <int kMost, int kC>
+__global__ __launch_bounds__(kMost) void rms_norm_bwd_kernel(const NormBwdParams p) {
+  const int t = threadIdx.x, threads = blockDim.x;
   const int cols = p.cols;
   bool ok[kC];
   int col[kC];
   uint4 w[kC], dyn[kC], drn[kC];
   uint2 cn[kC];
-  float sn[kC], rn, dw[kC][8];
+  float sn[kC], rn = 0.0f, dw[kC][8];
 #pragma unroll
   for (int i = 0; i < kC; ++i) {
-    col[i] = 8 * (t + kThreads * i);
+    col[i] = 8 * (t + threads * i);
     ok[i] = col[i] < cols;
     w[i] = dyn[i] = drn[i] = make_uint4(0, 0, 0, 0);
     cn[i] = make_uint2(0, 0);
@@ -197,58 +232,90 @@ __global__ __launch_bounds__(kThreads) void rms_norm_bwd_kernel(const NormBwdPar
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
   }
-  auto load = [&](int64_t row) __attribute__((always_inline)) {
-    rn = p.rstd[row];
-#pragma unroll
-    for (int i = 0; i < kC; ++i)
-      if (ok[i]) {
-        const int64_t at = row * cols + col[i];
-        dyn[i] = load_stream16(p.dy + at);
-        cn[i] = load_stream8(p.codes + at);
-        sn[i] = p.scales[at >> p.group_shift];
-        if (p.d_residual) drn[i] = load_stream16(p.d_residual + at);
-      }
+  constexpr bool kKeep = kC <= 2;   // else each phase loads a chunk when it comes to it
+  auto load = [&](int64_t row, int i) __attribute__((always_inline)) {
+    if (!ok[i]) return;
+    const int64_t start = row * cols;
+    dyn[i] = load_row16<kKeep>(at(p.dy + start, col[i]));
+    cn[i] = load_row8<kKeep>(at(p.codes + start, col[i]));
+    sn[i] = *at(p.scales + (start >> p.group_shift), col[i] >> p.group_shift);
+  };
+  auto load_residual = [&](int64_t row, int i) __attribute__((always_inline)) {
+    if (ok[i] && p.d_residual) drn[i] = load_stream16(at(p.d_residual + row * cols, col[i]));
+  };
+  auto load_weight = [&](int i) __attribute__((always_inline)) {
+    if (ok[i]) w[i] = *reinterpret_cast<const uint4*>(at(p.weight, col[i]));
   };
   int64_t row = blockIdx.x;
-  load(row);
+  rn = p.rstd[row];
+  if (kKeep) {
 #pragma unroll
-  for (int i = 0; i < kC; ++i)
-    if (ok[i]) w[i] = *reinterpret_cast<const uint4*>(p.weight + col[i]);
+    for (int i = 0; i < kC; ++i) load(row, i), load_residual(row, i), load_weight(i);
+  }
 
   int slot = 0;
   for (; row < p.rows; row += gridDim.x, slot ^= 1) {
-    uint4 dr[kC];
-    float n[kC][8], dn[kC][8], dot = 0.0f;
+    // kept as they came: n and dn are formed twice, which costs less than the
+    // registers to hold them
+    uint4 dy[kC], dr[kC];
+    uint2 code[kC];
+    float scale[kC], dot = 0.0f;
     const float rstd = rn;
+    auto terms = [&](int i, float (&d)[8], float (&n)[8]) __attribute__((always_inline)) {
+      unpack8(dy[i], d);
+      e4m3_values8(code[i], n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) n[e] *= scale[i];
+    };
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
-      float g[8];
+      if (!kKeep) load(row, i), load_weight(i);
+      dy[i] = dyn[i];
       dr[i] = drn[i];
-      unpack8(dyn[i], dn[i]);
-      e4m3_values8(cn[i], n[i]);
+      code[i] = cn[i];
+      scale[i] = sn[i] * rstd;
+      float d[8], n[8], g[8];
+      terms(i, d, n);
       unpack8(w[i], g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        n[i][e] = n[i][e] * sn[i] * rstd;
-        dw[i][e] = __builtin_fmaf(dn[i][e], n[i][e], dw[i][e]);
-        dn[i][e] *= g[e];
-        dot = __builtin_fmaf(dn[i][e], n[i][e], dot);
+        const float dyn_e = d[e] * n[e];
+        dw[i][e] += dyn_e;
+        dot = __builtin_fmaf(dyn_e, g[e], dot);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (row + gridDim.x < p.rows) {
+      rn = p.rstd[row + gridDim.x];
+      if (kKeep) {
+#pragma unroll
+        for (int i = 0; i < kC; ++i) load(row + gridDim.x, i), load_residual(row + gridDim.x, i);
       }
     }
-    if (row + gridDim.x < p.rows) load(row + gridDim.x);
-    const float mean = block_sum<kThreads>(dot, slot) * p.inv_cols;
+    const float mean = block_sum<kMost>(dot, slot) * p.inv_cols;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
       if (!ok[i]) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) dn[i][e] = rstd * __builtin_fmaf(-n[i][e], mean, dn[i][e]);
-      if (p.d_residual) {
-        float r[8];
-        unpack8(dr[i], r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dn[i][e] += r[e];
+      if (kKeep) {
+        // (opaque, or the compiler keeps the expanded values after all)
+        asm volatile("" : "+v"(dy[i].x), "+v"(dy[i].y), "+v"(dy[i].z), "+v"(dy[i].w), "+v"(code[i].x), "+v"(code[i].y));
+        asm volatile("" : "+v"(w[i].x), "+v"(w[i].y), "+v"(w[i].z), "+v"(w[i].w));
+      } else {
+        load(row, i), load_residual(row, i), load_weight(i);
+        dy[i] = dyn[i], dr[i] = drn[i], code[i] = cn[i], scale[i] = sn[i] * rstd;
       }
-      store_stream16(p.dx + row * cols + col[i], pack8(dn[i]));
+      float d[8], n[8], g[8];
+      terms(i, d, n);
+      unpack8(w[i], g);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d[e] = rstd * __builtin_fmaf(-n[e], mean, d[e] * g[e]);
+      if (p.d_residual) {
+        unpack8(dr[i], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] += g[e];
+      }
+      store_stream16(at(p.dx + row * cols, col[i]), pack8(d));
     }
   }
   if (p.partials) {
@@ -274,8 +341,19 @@ __global__ __launch_bounds__(kSumCols* kSumSlices) void sum_partials_kernel(cons
   const int c = threadIdx.x % kSumCols, slice = threadIdx.x / kSumCols;
   const int64_t col = (int64_t)blockIdx.x * kSumCols + c;
   float v = 0.0f;
-  if (col < cols)
-    for (int r = slice; r < parts; r += kSumSlices) v += partials[r * cols + col];
+  if (col < cols) {
+    // eight rows' loads in flight at a time
+    for (int r = slice; r < parts; r += 8 * kSumSlices) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = r + i * kSumSlices;
+        x[i] = at < parts ? partials[at * cols + col] : 0.0f;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v += x[i];
+    }
+  }
   part[slice][c] = v;
   __syncthreads();
 #pragma unroll
@@ -289,42 +367,55 @@ __global__ __launch_bounds__(kSumCols* kSumSlices) void sum_partials_kernel(cons
   }
 }
 
-// Rows of partial sums of the backward pass: two blocks for each of 256
-// compute units.  A constant, so that the workspace and the order of the sums
-// do not depend on the device.
-constexpr int64_t kNormParts = 512;
+// Blocks for rows, at most `most`, that all take as many rows as the busiest.
+int64_t balanced(int64_t rows, int64_t most) {
+  if (rows <= most) return rows;
+  const int64_t each = (rows + most - 1) / most;
+  return (rows + each - 1) / each;
+}
 
-int64_t norm_parts(int64_t rows) { return rows < kNormParts ? rows : kNormParts; }
-
+// The instance for a row, and its threads: whole waves, as few as hold the
+// row.  One chunk a thread up to 8192 columns: fewer registers, so that two
+// blocks of independent rows share a CU (backward, 4097 x 5120: 34 us with two
+// chunks, 28 with one); only the forward pass of 2049 to 4096 columns is
+// better with two chunks and four waves (8192 x 4096 with residual and
+// checkpoint: 49.2 us against 50.8; without them 24.2 against 23.5).
 struct NormShape {
-  int threads, chunks;
+  int most, chunks, threads;
 };
 
-// Threads and chunks of a row: the row in registers, at least one wave.
-NormShape norm_shape(int64_t cols) {
-  if (cols <= 512) return {64, 1};
-  if (cols <= 1024) return {128, 1};
-  if (cols <= 2048) return {256, 1};
-  if (cols <= 4096) return {256, 2};
-  if (cols <= 8192) return {512, 2};
-  if (cols <= 16384) return {1024, 2};
-  return {1024, 4};
+NormShape norm_shape(int64_t cols, bool backward) {
+  NormShape s = cols <= 512     ? NormShape{64, 1, 0}
+                : cols <= 2048  ? NormShape{256, 1, 0}
+                : cols <= 4096 && !backward ? NormShape{256, 2, 0}
+                : cols <= 8192  ? NormShape{1024, 1, 0}
+                : cols <= 16384 ? NormShape{1024, 2, 0}
+                                : NormShape{1024, 4, 0};
+  s.threads = (int)((cols / 8 + 64 * s.chunks - 1) / (64 * s.chunks)) * 64;
+  return s;
 }
 
 const void* norm_kernel_for(NormShape s, bool backward) {
 #define COAT_NORM(T, C)                                                              \
-  if (s.threads == T && s.chunks == C)                                               \
+  if (s.most == T && s.chunks == C)                                                  \
     return backward ? reinterpret_cast<const void*>(&rms_norm_bwd_kernel<T, C>)      \
                     : reinterpret_cast<const void*>(&rms_norm_kernel<T, C>);
   COAT_NORM(64, 1)
-  COAT_NORM(128, 1)
   COAT_NORM(256, 1)
-  COAT_NORM(256, 2)
-  COAT_NORM(512, 2)
+  COAT_NORM(1024, 1)
   COAT_NORM(1024, 2)
   COAT_NORM(1024, 4)
 #undef COAT_NORM
+  if (!backward && s.most == 256 && s.chunks == 2) return reinterpret_cast<const void*>(&rms_norm_kernel<256, 2>);
   return nullptr;
+}
+
+// Rows of partial sums of the backward pass: a block for each of 256 compute
+// units, more where a block is less than eight waves.  No property of the
+// device, so that the workspace and the order of the sums are not either.
+int64_t norm_parts(int64_t rows, int64_t cols) {
+  const int threads = norm_shape(cols, true).threads;
+  return balanced(rows, 256 * (threads >= 512 ? 1 : threads >= 128 ? 512 / threads : 4));
 }
 
 coat_status_t check_norm_shape(int64_t rows, int64_t cols, int32_t group_size) {
@@ -388,9 +479,10 @@ coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* a, hipStream_t strea
   int cus = 0;
   hipError_t e = current_cu_count(&cus);
   if (e != hipSuccess) return hip_fail(e);
-  const NormShape s = norm_shape(a->cols);
-  const int64_t most = (int64_t)cus * (2048 / s.threads);   // the threads that fit a CU
-  const int64_t blocks = a->rows < most ? a->rows : most;
+  const NormShape s = norm_shape(a->cols, false);
+  // as many blocks as the registers let a CU hold, all with as many rows:
+  // 28 waves with one chunk a thread, 16 with more
+  const int64_t blocks = balanced(a->rows, (int64_t)cus * ((s.chunks == 1 ? 28 : 16) * 64 / s.threads));
   void* args[] = {&p};
   e = hipLaunchKernel(norm_kernel_for(s, false), dim3((unsigned)blocks), dim3(s.threads), args, 0, stream);
   return e == hipSuccess ? COAT_OK : hip_fail(e);
@@ -398,7 +490,7 @@ coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* a, hipStream_t strea
 
 int64_t coat_fp8_rms_norm_bwd_workspace(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || cols > kMaxCols) return -1;
-  return norm_parts(rows) * cols * (int64_t)sizeof(float);
+  return cols == 0 ? 0 : norm_parts(rows, cols) * cols * (int64_t)sizeof(float);
 }
 
 coat_status_t coat_fp8_rms_norm_bwd(const coat_rms_norm_bwd_args_t* a, hipStream_t stream) {
@@ -415,7 +507,7 @@ coat_status_t coat_fp8_rms_norm_bwd(const coat_rms_norm_bwd_args_t* a, hipStream
     return COAT_ERR_MISALIGNED;
   if (a->dw && a->rows > 0 && a->workspace_bytes < coat_fp8_rms_norm_bwd_workspace(a->rows, a->cols))
     return COAT_ERR_INVALID_VALUE;
-  const int64_t blocks = norm_parts(a->rows);
+  const int64_t blocks = norm_parts(a->rows, a->cols);
   hipError_t e = hipSuccess;
   if (a->rows > 0) {
     NormBwdParams p;
@@ -432,7 +524,7 @@ coat_status_t coat_fp8_rms_norm_bwd(const coat_rms_norm_bwd_args_t* a, hipStream
     p.cols = (int32_t)a->cols;
     p.group_shift = __builtin_ctz((unsigned)a->group_size);
     p.inv_cols = (float)(1.0 / (double)a->cols);
-    const NormShape s = norm_shape(a->cols);
+    const NormShape s = norm_shape(a->cols, true);
     void* args[] = {&p};
     e = hipLaunchKernel(norm_kernel_for(s, true), dim3((unsigned)blocks), dim3(s.threads), args, 0, stream);
   }

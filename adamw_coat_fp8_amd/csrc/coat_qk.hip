@@ -23,7 +23,7 @@ namespace {
 // wave works on 64 / kLanes neighbouring heads at once, queries first, then
 // keys.  A wave takes one token and kH such sets of heads: it loads them all
 // before it works on the first, and the token's cosines and sines and both
-// weights once.  kH is 4, or 1 where that would leave the chip empty.
+// weights once.
 //
 // Rotation.  Pair j of a head, (a, b), becomes (a cos_j - b sin_j,
 // b cos_j + a sin_j).  Interleaved: (a, b) = values (2j, 2j + 1), inside a
@@ -314,8 +314,9 @@ constexpr int64_t kQkParts = 1024;
 
 int lanes_for(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 
-// Sets of heads a wave takes: 4, or 1 where slabs of 4 sets would give fewer
-// waves than the chip holds at four per SIMD.
+// Sets of heads a wave takes (a slab): up to 4, the number that leaves the
+// fewest sets over; 1 where that would give fewer waves than the chip holds at
+// four per SIMD.
 struct QkSplit {
   int sets;
   int32_t slabs;
@@ -325,14 +326,17 @@ struct QkSplit {
 constexpr int64_t kMaxUnits = 0x7FFFFFFF - kWavesPerBlock * 65536;   // unit + step stays below 2^32
 
 QkSplit split_heads(int64_t tokens, int64_t heads, int64_t dim) {
-  const int64_t set = 64 / lanes_for(dim);
-  int sets = 4;
-  int64_t slabs = (heads + set * sets - 1) / (set * sets);
-  if (tokens * slabs < 4096) {
-    sets = 1;
-    slabs = (heads + set - 1) / set;
+  const int64_t sets = (heads + 64 / lanes_for(dim) - 1) / (64 / lanes_for(dim));
+  // a slab costs about half a set more than its sets (tables and weights)
+  int best = 1;
+  int64_t cost = INT64_MAX;
+  for (int h = 4; h >= 1; --h) {
+    const int64_t c = (sets + h - 1) / h * (2 * h + 1);
+    if (c < cost) cost = c, best = h;
   }
-  return {sets, (int32_t)slabs, tokens * slabs};
+  if (tokens * ((sets + best - 1) / best) < 4096) best = 1;
+  const int64_t slabs = (sets + best - 1) / best;
+  return {best, (int32_t)slabs, tokens * slabs};
 }
 
 bool units_ok(int64_t tokens, int64_t heads, int64_t dim) {
@@ -350,10 +354,16 @@ const void* qk_kernel_for(int lanes, int sets, bool backward) {
     return backward ? reinterpret_cast<const void*>(&qk_norm_rope_bwd_kernel<L, H>)   \
                     : reinterpret_cast<const void*>(&qk_norm_rope_kernel<L, H>);
   COAT_QK(8, 1)
+  COAT_QK(8, 2)
+  COAT_QK(8, 3)
   COAT_QK(8, 4)
   COAT_QK(16, 1)
+  COAT_QK(16, 2)
+  COAT_QK(16, 3)
   COAT_QK(16, 4)
   COAT_QK(32, 1)
+  COAT_QK(32, 2)
+  COAT_QK(32, 3)
   COAT_QK(32, 4)
 #undef COAT_QK
   return nullptr;
