@@ -39,13 +39,14 @@ __device__ __forceinline__ void store_stream16(void* p, uint4 v) {
 }
 
 // Largest BF16 magnitude (as its 15 bits) among the 8 values of a chunk:
-// sign-cleared BF16 patterns order like the magnitudes they encode.
+// sign-cleared BF16 patterns order like the magnitudes they encode, two to a
+// packed 16-bit maximum.
 __device__ __forceinline__ uint32_t bf16x8_max_mag(uint4 r) {
-  const uint32_t a = max(r.x & 0x7FFFu, (r.x >> 16) & 0x7FFFu);
-  const uint32_t b = max(r.y & 0x7FFFu, (r.y >> 16) & 0x7FFFu);
-  const uint32_t c = max(r.z & 0x7FFFu, (r.z >> 16) & 0x7FFFu);
-  const uint32_t d = max(r.w & 0x7FFFu, (r.w >> 16) & 0x7FFFu);
-  return max(max(a, b), max(c, d));
+  typedef uint16_t u16x2v __attribute__((ext_vector_type(2)));
+  auto mag = [](uint32_t w) __attribute__((always_inline)) { return __builtin_bit_cast(u16x2v, w & 0x7FFF7FFFu); };
+  const u16x2v m = __builtin_elementwise_max(__builtin_elementwise_max(mag(r.x), mag(r.y)),
+                                             __builtin_elementwise_max(mag(r.z), mag(r.w)));
+  return max((uint32_t)m[0], (uint32_t)m[1]);
 }
 
 // E4M3 codes of the group quotients of four BF16 values.
@@ -67,12 +68,31 @@ __device__ __forceinline__ uint32_t group_max_u32(uint32_t v, int lanes) {
   return v;
 }
 
+// amax / 448 rounded as the IEEE division rounds it, for BF16 amax: one
+// residual correction with the rounded reciprocal, which is exact for every
+// BF16 value from 2^-100 up (checked value by value in the tests); the
+// division below.
+__device__ __forceinline__ float scale_of(float amax) {
+  constexpr float kInv = 1.0f / 448.0f;
+  if (amax < 0x1p-100f) return amax / 448.0f;
+  const float q = amax * kInv;
+  const float v = __builtin_fmaf(__builtin_fmaf(-q, 448.0f, amax), kInv, q);
+  return v == v ? v : amax;   // infinity
+}
+
 // The checkpoint of one 8-value BF16 chunk whose group lies on `lanes`
-// neighbouring lanes: its codes, and the group's scale max / 448.
+// neighbouring lanes: its codes, and the group's scale max / 448.  The
+// reciprocal in the quotients is the hardware's, one ulp off at most: ties
+// stay exact under the correction in group_quot, and for BF16 values no other
+// quotient lies close enough to a midpoint for it to matter.
 __device__ __forceinline__ uint2 checkpoint8(uint4 raw, int lanes, float& scale) {
   const float amax = __uint_as_float(group_max_u32(bf16x8_max_mag(raw), lanes) << 16);
-  const GroupQuot d = group_quot_setup(amax);
-  scale = amax / 448.0f;
+  const float pre = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+  GroupQuot d;
+  d.c = 0.875f * pre;
+  d.b = amax * pre * 0x1p-9f;
+  d.r = __builtin_amdgcn_rcpf(d.b);
+  scale = scale_of(amax);
   if (amax == 0.0f) return make_uint2(0, 0);
   return make_uint2(act_pack4(raw.x, raw.y, d), act_pack4(raw.z, raw.w, d));
 }

@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kMost) void rms_norm_kernel(const NormParams p) {
 #pragma unroll
       for (int i = 0; i < kC; ++i) load(row + gridDim.x, i);
     }
-    const float rstd = 1.0f / sqrtf(__builtin_fmaf(block_sum<kMost>(ss, slot), p.inv_cols, p.eps));
+    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum<kMost>(ss, slot), p.inv_cols, p.eps));
     if (p.rstd && t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {
@@ -447,7 +447,7 @@ coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* a, hipStream_t strea
   if (!a) return COAT_ERR_NULL_POINTER;
   const coat_status_t st = check_norm_shape(a->rows, a->cols, a->group_size);
   if (st != COAT_OK) return st;
-  if (!isfinite(a->eps) || a->eps <= 0.0f) return COAT_ERR_INVALID_VALUE;
+  if (!isfinite(a->eps) || a->eps < 0x1p-126f) return COAT_ERR_INVALID_VALUE;
   if (a->y_codes && !(a->y_scale > 0.0f && isfinite(a->y_scale) && isfinite(1.0f / a->y_scale)))
     return COAT_ERR_INVALID_VALUE;
   if (a->y_amax && !a->y_codes) return COAT_ERR_INVALID_VALUE;

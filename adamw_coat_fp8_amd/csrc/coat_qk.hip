@@ -20,16 +20,19 @@ namespace {
 
 // A head of D values lies on kLanes lanes of a wave, eight values a lane
 // (kLanes the power of two >= D/8, at least 8; lanes past D/8 idle), so a
-// wave works on 64 / kLanes neighbouring heads at once, queries first, then
-// keys.  A wave takes one token and kH such sets of heads: it loads them all
-// before it works on the first, and the token's cosines and sines and both
-// weights once.
+// wave works on a set of 64 / kLanes neighbouring heads at once.  A wave takes
+// one token and kH sets of its query heads or of its key heads (a slab): it
+// loads them all before it works on the first, and the token's cosines and
+// sines and the weight once.
 //
 // Rotation.  Pair j of a head, (a, b), becomes (a cos_j - b sin_j,
 // b cos_j + a sin_j).  Interleaved: (a, b) = values (2j, 2j + 1), inside a
 // lane.  Otherwise values (j, j + rot/2): rot is a multiple of 16, so a whole
 // chunk's partner is the chunk rot/16 lanes away, which sends its BF16 words
-// over (ds_bpermute); the receiver norms them itself.
+// over (ds_bpermute).  The forward pass multiplies the weights into the
+// token's cosines and sines once, so a value costs x A + partner B and rstd:
+// 31 -> 17 vector instructions a value with that and the cheaper checkpoint
+// arithmetic, which had bound the kernel.
 // A token whose position is outside the table is padding: everything written
 // for it is zero.
 
@@ -51,8 +54,8 @@ struct QkParams {
   float* partials;          // backward: gridDim.x rows of 2 D, or NULL
   int64_t tokens, table_rows;
   int32_t units;            // (token, slab) pairs, < 2^31
-  int32_t slabs;            // slabs of heads of a token
-  int32_t q_heads, heads;
+  int32_t slabs, q_slabs;   // slabs of heads of a token, and those of queries
+  int32_t q_heads, k_heads;
   int32_t dim, rot;
   int32_t interleaved;
   int32_t group_shift;
@@ -133,12 +136,39 @@ __device__ __forceinline__ void swap_pairs(const float (&f)[8], float (&g)[8]) {
   for (int e = 0; e < 8; ++e) g[e] = f[e ^ 1];
 }
 
-__device__ __forceinline__ uint4 load_weight(const uint16_t* w, int chunk, bool on) {
-  return on ? *reinterpret_cast<const uint4*>(w + 8 * chunk) : make_uint4(0, 0, 0, 0);
+// What a wave works on: a token and heads first .. first + count - 1 (this
+// lane's head `sub` of a set further on) of its queries or keys.
+struct Slab {
+  int64_t token;
+  bool key;
+  int heads, first;      // of the queries or keys
+  int64_t row;           // index of the token's head 0 in the checkpoint
+  const uint16_t* in;    // the token's heads
+  uint16_t* out;
+  const uint16_t* weight;
+};
+
+template <int kSet, int kH>
+__device__ __forceinline__ Slab slab_of(const QkParams& p, uint32_t unit) {
+  Slab s;
+  const uint32_t token = unit / (uint32_t)p.slabs;
+  int slab = (int)(unit - token * (uint32_t)p.slabs);
+  s.token = token;
+  s.key = slab >= p.q_slabs;
+  if (s.key) slab -= p.q_slabs;
+  s.heads = s.key ? p.k_heads : p.q_heads;
+  s.first = slab * (kSet * kH);
+  s.row = s.token * (p.q_heads + p.k_heads) + (s.key ? p.q_heads : 0);
+  s.in = s.key ? p.k + s.token * p.k_stride : p.q + s.token * p.q_stride;
+  s.out = s.key ? p.k_out + s.token * p.k_out_stride : p.q_out + s.token * p.q_out_stride;
+  s.weight = s.key ? p.k_weight : p.q_weight;
+  return s;
 }
 
-__device__ __forceinline__ uint4 pick(bool key, uint4 q, uint4 k) {
-  return make_uint4(key ? k.x : q.x, key ? k.y : q.y, key ? k.z : q.z, key ? k.w : q.w);
+// Element `i` past a uniform address: a scalar base and a 32-bit offset.
+template <class V>
+__device__ __forceinline__ V* at(V* base, int i) {
+  return reinterpret_cast<V*>(reinterpret_cast<uintptr_t>(base) + (uint32_t)i * (uint32_t)sizeof(V));
 }
 
 template <int kLanes, int kH>
@@ -148,62 +178,61 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_kernel(const QkPar
   const bool on = 8 * chunk < p.dim;
   const uint32_t unit = wave_index(blockIdx.x);
   if (unit >= (uint32_t)p.units) return;
-  const uint32_t token32 = unit / (uint32_t)p.slabs;
-  const int64_t token = token32;
-  const int head0 = (int)(unit - token32 * p.slabs) * (kSet * kH) + sub;
+  const Slab s = slab_of<kSet, kH>(p, unit);
   uint4 raw[kH];
 #pragma unroll
   for (int i = 0; i < kH; ++i) {
-    const int head = head0 + kSet * i;
+    const int head = s.first + kSet * i + sub;
     raw[i] = make_uint4(0, 0, 0, 0);
-    if (on && head < p.heads)
-      raw[i] = load_stream16(head < p.q_heads ? p.q + token * p.q_stride + (int64_t)head * p.dim + 8 * chunk
-                                              : p.k + token * p.k_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk);
+    if (on && head < s.heads) raw[i] = load_stream16(at(s.in, head * p.dim + 8 * chunk));
   }
-  const Turn turn = load_turn(p, token, chunk, 1.0f);
-  const uint4 wq = load_weight(p.q_weight, chunk, on), wk = load_weight(p.k_weight, chunk, on);
+  const Turn turn = load_turn(p, s.token, chunk, 1.0f);
   const int addr = partner_lane(p, lane, chunk), lanes = 1 << (p.group_shift - 3);
-  const uint4 wq_far = from_lane(wq, addr), wk_far = from_lane(wk, addr);
+  float own[8], other[8];   // what a value and its partner are multiplied with, but for rstd
+  {
+    const uint4 w = on ? *reinterpret_cast<const uint4*>(at(s.weight, 8 * chunk)) : make_uint4(0, 0, 0, 0);
+    float f[8], g[8];
+    unpack8(w, f);
+    if (p.interleaved)
+      swap_pairs(f, g);
+    else
+      unpack8(from_lane(w, addr), g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      own[e] = f[e] * turn.cos[e];
+      other[e] = g[e] * turn.sin[e];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kH; ++i) {
-    const int head = head0 + kSet * i;
-    const bool key = head >= p.q_heads, ok = on && head < p.heads;
+    const int head = s.first + kSet * i + sub;
+    const bool ok = on && head < s.heads;
     if (!turn.live) raw[i] = make_uint4(0, 0, 0, 0);
-    float x[8], w[8], far[8], wf[8];
+    float x[8], far[8];
     unpack8(raw[i], x);
     float ss = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
-    float rstd = 1.0f / sqrtf(__builtin_fmaf(lanes_sum<kLanes>(ss), p.inv_dim, p.eps));
+    float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(lanes_sum<kLanes>(ss), p.inv_dim, p.eps));
     if (!turn.live) rstd = 0.0f;
-    const int64_t row = token * p.heads + head;
     if (p.codes) {
       float scale;
       const uint2 c = checkpoint8(raw[i], lanes, scale);
       if (ok) {
-        const int64_t at = row * p.dim + 8 * chunk;
-        store_stream8(p.codes + at, c);
-        if ((chunk & (lanes - 1)) == 0) p.scales[at >> p.group_shift] = scale;
+        const int from = head * p.dim + 8 * chunk;
+        store_stream8(at(p.codes + s.row * p.dim, from), c);
+        if ((chunk & (lanes - 1)) == 0)
+          *at(p.scales + ((s.row * p.dim) >> p.group_shift), from >> p.group_shift) = scale;
       }
     }
-    if (p.rstd && ok && chunk == 0) p.rstd[row] = rstd;
-    unpack8(pick(key, wq, wk), w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= rstd * w[e];
-    if (p.interleaved) {
+    if (p.rstd && ok && chunk == 0) *at(p.rstd + s.row, head) = rstd;
+    if (p.interleaved)
       swap_pairs(x, far);
-    } else {
+    else
       unpack8(from_lane(raw[i], addr), far);
-      unpack8(pick(key, wq_far, wk_far), wf);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) far[e] *= rstd * wf[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(far[e], turn.sin[e], x[e] * turn.cos[e]);
-    if (ok)
-      store_stream16(key ? p.k_out + token * p.k_out_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk
-                         : p.q_out + token * p.q_out_stride + (int64_t)head * p.dim + 8 * chunk,
-                     pack8(x));
+    for (int e = 0; e < 8; ++e) x[e] = rstd * __builtin_fmaf(far[e], other[e], x[e] * own[e]);
+    if (ok) store_stream16(at(s.out, head * p.dim + 8 * chunk), pack8(x));
   }
 }
 
@@ -218,40 +247,39 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
   constexpr int kSet = 64 / kLanes;
   const int lane = threadIdx.x & 63, chunk = lane & (kLanes - 1), sub = lane / kLanes;
   const bool on = 8 * chunk < p.dim;
-  const uint4 wq = load_weight(p.q_weight, chunk, on), wk = load_weight(p.k_weight, chunk, on);
   const int addr = partner_lane(p, lane, chunk);
   float dwq[8], dwk[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.0f;
   const uint32_t step = gridDim.x * kWavesPerBlock;
   for (uint32_t unit = wave_index(blockIdx.x); unit < (uint32_t)p.units; unit += step) {
-    const uint32_t token32 = unit / (uint32_t)p.slabs;
-    const int64_t token = token32;
-    const int head0 = (int)(unit - token32 * p.slabs) * (kSet * kH) + sub;
+    const Slab s = slab_of<kSet, kH>(p, unit);
     uint4 raw[kH];
     uint2 code[kH];
     float scale[kH], rs[kH];
 #pragma unroll
     for (int i = 0; i < kH; ++i) {
-      const int head = head0 + kSet * i;
+      const int head = s.first + kSet * i + sub;
       raw[i] = make_uint4(0, 0, 0, 0);
       code[i] = make_uint2(0, 0);
       scale[i] = rs[i] = 0.0f;
-      if (on && head < p.heads) {
-        const int64_t row = token * p.heads + head, at = row * p.dim + 8 * chunk;
-        raw[i] = load_stream16(head < p.q_heads ? p.q + token * p.q_stride + (int64_t)head * p.dim + 8 * chunk
-                                                : p.k + token * p.k_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk);
-        code[i] = load_stream8(p.codes + at);
-        scale[i] = p.scales[at >> p.group_shift];
-        rs[i] = p.rstd[row];
+      if (on && head < s.heads) {
+        const int from = head * p.dim + 8 * chunk;
+        raw[i] = load_stream16(at(s.in, from));
+        code[i] = load_stream8(at(p.codes + s.row * p.dim, from));
+        scale[i] = *at(p.scales + ((s.row * p.dim) >> p.group_shift), from >> p.group_shift);
+        rs[i] = *at(p.rstd + s.row, head);
       }
     }
-    const Turn turn = load_turn(p, token, chunk, -1.0f);
+    const Turn turn = load_turn(p, s.token, chunk, -1.0f);
+    float w[8], g[8];
+    unpack8(on ? *reinterpret_cast<const uint4*>(at(s.weight, 8 * chunk)) : make_uint4(0, 0, 0, 0), w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kH; ++i) {
-      const int head = head0 + kSet * i;
-      const bool key = head >= p.q_heads, ok = on && head < p.heads;
-      float d[8], far[8], n[8], w[8];
+      const int head = s.first + kSet * i + sub;
+      float d[8], far[8], n[8];
       if (!turn.live) {   // padding: nothing of it counts, whatever its buffers hold
         raw[i] = make_uint4(0, 0, 0, 0);
         code[i] = make_uint2(0, 0);
@@ -263,25 +291,27 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
       else
         unpack8(from_lane(raw[i], addr), far);
       e4m3_values8(code[i], n);
-      unpack8(pick(key, wq, wk), w);
+      const float sr = scale[i] * rs[i];
       float dot = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         d[e] = __builtin_fmaf(far[e], turn.sin[e], d[e] * turn.cos[e]);
-        n[e] = n[e] * scale[i] * rs[i];
-        const float g = d[e] * n[e];
-        dwq[e] += key ? 0.0f : g;
-        dwk[e] += key ? g : 0.0f;
+        n[e] *= sr;
+        g[e] = __builtin_fmaf(d[e], n[e], g[e]);
         d[e] *= w[e];
         dot = __builtin_fmaf(d[e], n[e], dot);
       }
       const float mean = lanes_sum<kLanes>(dot) * p.inv_dim;
 #pragma unroll
       for (int e = 0; e < 8; ++e) d[e] = rs[i] * __builtin_fmaf(-n[e], mean, d[e]);
-      if (ok)
-        store_stream16(key ? p.k_out + token * p.k_out_stride + (int64_t)(head - p.q_heads) * p.dim + 8 * chunk
-                           : p.q_out + token * p.q_out_stride + (int64_t)head * p.dim + 8 * chunk,
-                       pack8(d));
+      if (on && head < s.heads) store_stream16(at(s.out, head * p.dim + 8 * chunk), pack8(d));
+    }
+    if (s.key) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dwk[e] += g[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) dwq[e] += g[e];
     }
   }
   if (p.partials) {
@@ -296,10 +326,10 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
     }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * p.dim; c += kBlockThreads) {
-      const int at = c < p.dim ? c : 8 * kLanes + c - p.dim;
-      float v = sums[0][at];
+      const int from = c < p.dim ? c : 8 * kLanes + c - p.dim;
+      float v = sums[0][from];
 #pragma unroll
-      for (int i = 1; i < kRows; ++i) v += sums[i][at];
+      for (int i = 1; i < kRows; ++i) v += sums[i][from];
       p.partials[(int64_t)blockIdx.x * 2 * p.dim + c] = v;
     }
   }
@@ -319,28 +349,29 @@ int lanes_for(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
 // four per SIMD.
 struct QkSplit {
   int sets;
-  int32_t slabs;
+  int32_t slabs, q_slabs;
   int64_t units;   // at most kMaxUnits
 };
 
 constexpr int64_t kMaxUnits = 0x7FFFFFFF - kWavesPerBlock * 65536;   // unit + step stays below 2^32
 
-QkSplit split_heads(int64_t tokens, int64_t heads, int64_t dim) {
-  const int64_t sets = (heads + 64 / lanes_for(dim) - 1) / (64 / lanes_for(dim));
-  // a slab costs about half a set more than its sets (tables and weights)
+QkSplit split_heads(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {
+  const int64_t set = 64 / lanes_for(dim);
+  auto slabs = [&](int64_t heads, int64_t h) { return (heads + set * h - 1) / (set * h); };
+  // a slab costs about half a set more than its sets (tables and weight)
   int best = 1;
   int64_t cost = INT64_MAX;
   for (int h = 4; h >= 1; --h) {
-    const int64_t c = (sets + h - 1) / h * (2 * h + 1);
+    const int64_t c = (slabs(q_heads, h) + slabs(k_heads, h)) * (2 * h + 1);
     if (c < cost) cost = c, best = h;
   }
-  if (tokens * ((sets + best - 1) / best) < 4096) best = 1;
-  const int64_t slabs = (sets + best - 1) / best;
-  return {best, (int32_t)slabs, tokens * slabs};
+  if (tokens * (slabs(q_heads, best) + slabs(k_heads, best)) < 4096) best = 1;
+  const int64_t q = slabs(q_heads, best), all = q + slabs(k_heads, best);
+  return {best, (int32_t)all, (int32_t)q, tokens * all};
 }
 
-bool units_ok(int64_t tokens, int64_t heads, int64_t dim) {
-  return tokens <= kMaxUnits && split_heads(tokens, heads, dim).units <= kMaxUnits;
+bool units_ok(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {
+  return tokens <= kMaxUnits && split_heads(tokens, q_heads, k_heads, dim).units <= kMaxUnits;
 }
 
 int64_t qk_parts(int64_t units) {
@@ -382,7 +413,7 @@ coat_status_t check_qk(const coat_qk_shape_t& s) {
     return COAT_ERR_INVALID_VALUE;
   if (s.rot_dim < 16 || s.rot_dim > s.head_dim || s.rot_dim % 16 != 0) return COAT_ERR_INVALID_VALUE;
   if (s.table_rows > INT64_MAX / 4 / s.head_dim) return COAT_ERR_INVALID_VALUE;
-  if (!units_ok(s.tokens, s.q_heads + s.k_heads, s.head_dim)) return COAT_ERR_INVALID_VALUE;
+  if (!units_ok(s.tokens, s.q_heads, s.k_heads, s.head_dim)) return COAT_ERR_INVALID_VALUE;
   return COAT_OK;
 }
 
@@ -392,8 +423,9 @@ void fill(QkParams& p, const coat_qk_shape_t& s, const QkSplit& split) {
   p.table_rows = s.table_rows;
   p.units = (int32_t)split.units;
   p.slabs = split.slabs;
+  p.q_slabs = split.q_slabs;
   p.q_heads = s.q_heads;
-  p.heads = s.q_heads + s.k_heads;
+  p.k_heads = s.k_heads;
   p.dim = s.head_dim;
   p.rot = s.rot_dim;
   p.interleaved = s.interleaved != 0;
@@ -410,7 +442,7 @@ coat_status_t coat_fp8_qk_norm_rope(const coat_qk_norm_rope_args_t* a, hipStream
   const coat_qk_shape_t& s = a->shape;
   const coat_status_t st = check_qk(s);
   if (st != COAT_OK) return st;
-  if (!isfinite(a->eps) || a->eps <= 0.0f) return COAT_ERR_INVALID_VALUE;
+  if (!isfinite(a->eps) || a->eps < 0x1p-126f) return COAT_ERR_INVALID_VALUE;
   if (bad_stride(a->q_stride, s.q_heads, s.head_dim, s.tokens) ||
       bad_stride(a->k_stride, s.k_heads, s.head_dim, s.tokens) ||
       bad_stride(a->q_out_stride, s.q_heads, s.head_dim, s.tokens) ||
@@ -424,7 +456,7 @@ coat_status_t coat_fp8_qk_norm_rope(const coat_qk_norm_rope_args_t* a, hipStream
       !aligned(a->q_weight, 16) || !aligned(a->k_weight, 16) || !aligned(a->cos, 16) || !aligned(a->sin, 16) ||
       !aligned(a->positions, 8) || !aligned(a->codes, 16) || !aligned(a->scales, 4) || !aligned(a->rstd, 4))
     return COAT_ERR_MISALIGNED;
-  const QkSplit split = split_heads(s.tokens, s.q_heads + s.k_heads, s.head_dim);
+  const QkSplit split = split_heads(s.tokens, s.q_heads, s.k_heads, s.head_dim);
   const int64_t blocks = (split.units + kWavesPerBlock - 1) / kWavesPerBlock;
   QkParams p;
   fill(p, s, split);
@@ -453,9 +485,12 @@ coat_status_t coat_fp8_qk_norm_rope(const coat_qk_norm_rope_args_t* a, hipStream
 
 int64_t coat_fp8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads, int64_t head_dim) {
   if (tokens < 0 || heads < 0 || heads > 2 * kMaxHeads || head_dim < 16 || head_dim > kMaxDim || head_dim % 16 != 0 ||
-      !units_ok(tokens, heads, head_dim))
+      tokens > kMaxUnits)
     return -1;
-  return qk_parts(split_heads(tokens, heads, head_dim).units) * 2 * head_dim * (int64_t)sizeof(float);
+  if (tokens == 0 || heads == 0) return 0;
+  // the most units that any division of the heads into queries and keys gives
+  const int64_t set = 64 / lanes_for(head_dim), units = tokens * ((heads + set - 1) / set + 1);
+  return qk_parts(units) * 2 * head_dim * (int64_t)sizeof(float);
 }
 
 coat_status_t coat_fp8_qk_norm_rope_bwd(const coat_qk_norm_rope_bwd_args_t* a, hipStream_t stream) {
@@ -483,7 +518,7 @@ coat_status_t coat_fp8_qk_norm_rope_bwd(const coat_qk_norm_rope_bwd_args_t* a, h
   if (work && dw &&
       a->workspace_bytes < coat_fp8_qk_norm_rope_bwd_workspace(s.tokens, s.q_heads + s.k_heads, s.head_dim))
     return COAT_ERR_INVALID_VALUE;
-  const QkSplit split = split_heads(s.tokens, s.q_heads + s.k_heads, s.head_dim);
+  const QkSplit split = split_heads(s.tokens, s.q_heads, s.k_heads, s.head_dim);
   const int64_t blocks = work ? qk_parts(split.units) : 0;
   hipError_t e = hipSuccess;
   if (work) {

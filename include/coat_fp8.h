@@ -264,7 +264,7 @@ coat_status_t coat_fp8_gemm_bf16(const uint8_t* a, const uint8_t* b,
  * cols is a multiple of group_size, at most 32768; squares are summed in FP32.
  * Errors: NULL_POINTER (args, x, weight; neither y nor y_codes; residual
  * without residual_out or codes without scales, or the reverse),
- * INVALID_VALUE (sizes; eps not finite or <= 0; with y_codes, y_scale not
+ * INVALID_VALUE (sizes; eps not finite or below 2^-126; with y_codes, y_scale not
  * positive and finite or its reciprocal infinite; y_amax without y_codes),
  * GROUP_SIZE, MISALIGNED (16 bytes; scales, rstd and y_amax 4), HIP.
  */
