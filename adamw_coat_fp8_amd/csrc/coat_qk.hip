@@ -252,26 +252,38 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
 #pragma unroll
   for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.0f;
   const uint32_t step = gridDim.x * kWavesPerBlock;
-  for (uint32_t unit = wave_index(blockIdx.x); unit < (uint32_t)p.units; unit += step) {
+  // The next unit's heads are loaded before the current one's are worked on.
+  uint4 raw_n[kH];
+  uint2 code_n[kH];
+  float scale_n[kH], rs_n[kH];
+  auto load = [&](uint32_t unit) __attribute__((always_inline)) {
     const Slab s = slab_of<kSet, kH>(p, unit);
+#pragma unroll
+    for (int i = 0; i < kH; ++i) {
+      const int head = s.first + kSet * i + sub;
+      raw_n[i] = make_uint4(0, 0, 0, 0);
+      code_n[i] = make_uint2(0, 0);
+      scale_n[i] = rs_n[i] = 0.0f;
+      if (on && head < s.heads) {
+        const int from = head * p.dim + 8 * chunk;
+        raw_n[i] = load_stream16(at(s.in, from));
+        code_n[i] = load_stream8(at(p.codes + s.row * p.dim, from));
+        scale_n[i] = *at(p.scales + ((s.row * p.dim) >> p.group_shift), from >> p.group_shift);
+        rs_n[i] = *at(p.rstd + s.row, head);
+      }
+    }
+  };
+  uint32_t unit = wave_index(blockIdx.x);
+  if (unit < (uint32_t)p.units) load(unit);
+  for (; unit < (uint32_t)p.units; unit += step) {
+    const Slab s = slab_of<kSet, kH>(p, unit);
+    const Turn turn = load_turn(p, s.token, chunk, -1.0f);
     uint4 raw[kH];
     uint2 code[kH];
     float scale[kH], rs[kH];
 #pragma unroll
-    for (int i = 0; i < kH; ++i) {
-      const int head = s.first + kSet * i + sub;
-      raw[i] = make_uint4(0, 0, 0, 0);
-      code[i] = make_uint2(0, 0);
-      scale[i] = rs[i] = 0.0f;
-      if (on && head < s.heads) {
-        const int from = head * p.dim + 8 * chunk;
-        raw[i] = load_stream16(at(s.in, from));
-        code[i] = load_stream8(at(p.codes + s.row * p.dim, from));
-        scale[i] = *at(p.scales + ((s.row * p.dim) >> p.group_shift), from >> p.group_shift);
-        rs[i] = *at(p.rstd + s.row, head);
-      }
-    }
-    const Turn turn = load_turn(p, s.token, chunk, -1.0f);
+    for (int i = 0; i < kH; ++i) raw[i] = raw_n[i], code[i] = code_n[i], scale[i] = scale_n[i], rs[i] = rs_n[i];
+    if (unit + step < (uint32_t)p.units) load(unit + step);
     float w[8], g[8];
     unpack8(on ? *reinterpret_cast<const uint4*>(at(s.weight, 8 * chunk)) : make_uint4(0, 0, 0, 0), w);
 #pragma unroll
@@ -338,8 +350,11 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
 constexpr int64_t kMaxHeads = 1 << 16;
 constexpr int64_t kMaxDim = 256;
 
-// Rows of partial sums of the backward pass, a constant for the reasons of
-// the norm's.
+// Most rows of partial sums of the backward pass, and blocks: what the
+// registers hold at one or two sets a slab; three quarters of it at more (a
+// second round of few blocks otherwise: 64 heads of 128 values over 8192
+// tokens take 75.8 us with 1024 blocks, 64.7 with 768).  Constants for the
+// reasons of the norm's.
 constexpr int64_t kQkParts = 1024;
 
 int lanes_for(int64_t dim) { return dim <= 64 ? 8 : dim <= 128 ? 16 : 32; }
@@ -355,14 +370,15 @@ struct QkSplit {
 
 constexpr int64_t kMaxUnits = 0x7FFFFFFF - kWavesPerBlock * 65536;   // unit + step stays below 2^32
 
-QkSplit split_heads(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {
+QkSplit split_heads(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim, int most = 4) {
   const int64_t set = 64 / lanes_for(dim);
   auto slabs = [&](int64_t heads, int64_t h) { return (heads + set * h - 1) / (set * h); };
-  // a slab costs about half a set more than its sets (tables and weight)
+  // a slab costs about one set more than its own (tables and weight); counted as
+  // half a set, 24 and 8 heads of 64 values took 17.7 us and not 14.9
   int best = 1;
   int64_t cost = INT64_MAX;
-  for (int h = 4; h >= 1; --h) {
-    const int64_t c = (slabs(q_heads, h) + slabs(k_heads, h)) * (2 * h + 1);
+  for (int h = most; h >= 1; --h) {
+    const int64_t c = (slabs(q_heads, h) + slabs(k_heads, h)) * (h + 1);
     if (c < cost) cost = c, best = h;
   }
   if (tokens * (slabs(q_heads, best) + slabs(k_heads, best)) < 4096) best = 1;
@@ -371,12 +387,12 @@ QkSplit split_heads(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t di
 }
 
 bool units_ok(int64_t tokens, int64_t q_heads, int64_t k_heads, int64_t dim) {
-  return tokens <= kMaxUnits && split_heads(tokens, q_heads, k_heads, dim).units <= kMaxUnits;
+  return tokens <= kMaxUnits && split_heads(tokens, q_heads, k_heads, dim, 1).units <= kMaxUnits;
 }
 
-int64_t qk_parts(int64_t units) {
-  const int64_t blocks = (units + kWavesPerBlock - 1) / kWavesPerBlock;
-  return blocks < kQkParts ? blocks : kQkParts;
+int64_t qk_parts(int64_t units, int sets) {
+  const int64_t blocks = (units + kWavesPerBlock - 1) / kWavesPerBlock, most = sets > 2 ? kQkParts * 3 / 4 : kQkParts;
+  return blocks < most ? blocks : most;
 }
 
 const void* qk_kernel_for(int lanes, int sets, bool backward) {
@@ -490,7 +506,7 @@ int64_t coat_fp8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads, int64
   if (tokens == 0 || heads == 0) return 0;
   // the most units that any division of the heads into queries and keys gives
   const int64_t set = 64 / lanes_for(head_dim), units = tokens * ((heads + set - 1) / set + 1);
-  return qk_parts(units) * 2 * head_dim * (int64_t)sizeof(float);
+  return qk_parts(units, 1) * 2 * head_dim * (int64_t)sizeof(float);
 }
 
 coat_status_t coat_fp8_qk_norm_rope_bwd(const coat_qk_norm_rope_bwd_args_t* a, hipStream_t stream) {
@@ -519,7 +535,7 @@ coat_status_t coat_fp8_qk_norm_rope_bwd(const coat_qk_norm_rope_bwd_args_t* a, h
       a->workspace_bytes < coat_fp8_qk_norm_rope_bwd_workspace(s.tokens, s.q_heads + s.k_heads, s.head_dim))
     return COAT_ERR_INVALID_VALUE;
   const QkSplit split = split_heads(s.tokens, s.q_heads, s.k_heads, s.head_dim);
-  const int64_t blocks = work ? qk_parts(split.units) : 0;
+  const int64_t blocks = work ? qk_parts(split.units, split.sets) : 0;
   hipError_t e = hipSuccess;
   if (work) {
     QkParams p;
