@@ -61,16 +61,20 @@ struct WgradParams {
   int32_t n_tiles, k_tiles;
   int32_t steps;         // steps of all rows, ceil(M / 64)
   int32_t splits;
+  int32_t whole;         // tiles of the order computed whole; each later one as two halves
   int32_t out;
   float scale;
 };
 
-template <int kWN, int kWK, int kJ, int kI>
+// kLds: bytes of a stage's dy panel in the LDS, or 0 for what the tile needs.
+template <int kWN_, int kWK_, int kJ_, int kI_, int kLds = 0>
 struct Tile {
+  static constexpr int kWN = kWN_, kWK = kWK_, kJ = kJ_, kI = kI_;
   static constexpr int kWaves = kWN * kWK, kThreads = 64 * kWaves;
   static constexpr int kBN = 32 * kWN * kJ, kBK = 32 * kWK * kI;
   static constexpr int kA = kStep * kBN * 2, kB = kStep * kBK;   // bytes of a stage's panels
   static constexpr int kLA = kA / 1024 / kWaves, kLB = kB / 1024 / kWaves;
+  static constexpr int kLdsA = kLds ? kLds : kA;
 };
 
 // A dy row holds kBN values; its 64-byte chunks are XORed with m % 4, so that
@@ -106,7 +110,7 @@ __device__ __forceinline__ uint8_t* lds_array() {
 }
 
 template <class T, int kSt>
-__device__ __forceinline__ uint8_t* dy_stage() { return lds_array<T::kA, kSt>(); }
+__device__ __forceinline__ uint8_t* dy_stage() { return lds_array<T::kLdsA, kSt>(); }
 
 template <class T, int G, int kSt>
 __device__ __forceinline__ uint8_t* code_stage() { return lds_array<T::kB + 256 * Stage<T, G>::kSlots, 3 + kSt>(); }
@@ -153,24 +157,14 @@ __device__ __forceinline__ uint32_t xcd_contiguous32(uint32_t b, uint32_t nb) {
   return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
 }
 
-// G = 0: one scale.
-template <class T, int kWK, int kJ, int kI, int G>
-__global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p) {
+// Computes the tile of dW at (n0, k0), over the steps of `part`.  G = 0: one
+// scale.
+template <class T, int G>
+__device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n0, const int64_t k0, const uint32_t part) {
   using S = Stage<T, G>;
-  constexpr int kBN = T::kBN, kBK = T::kBK;
+  constexpr int kBN = T::kBN, kBK = T::kBK, kWK = T::kWK, kJ = T::kJ, kI = T::kI;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave / kWK, wk = wave % kWK;
-  // Tile order: an XCD takes a contiguous run; inside it eight k tiles are
-  // walked for each n tile, so the 32 tiles an XCD works on at once share
-  // about 4 dy panels and 8 code panels (half as wide) in its L2.
-  // (32-bit numbers: a block's share of them is scalar work of a few cycles)
-  const uint32_t n_tiles = (uint32_t)p.n_tiles, k_tiles = (uint32_t)p.k_tiles, tiles = n_tiles * k_tiles;
-  const uint32_t order = (uint32_t)xcd_contiguous32(blockIdx.x, gridDim.x);
-  const uint32_t part = order / tiles, local = order - part * tiles;
-  const uint32_t band = local / (8 * n_tiles), first_k = 8 * band;
-  const uint32_t wide = k_tiles - first_k < 8 ? k_tiles - first_k : 8;
-  const uint32_t in_band = local - band * 8 * n_tiles, row = in_band / wide;
-  const int64_t n0 = (int64_t)row * kBN, k0 = (int64_t)(first_k + in_band - row * wide) * kBK;
   const int step0 = p.splits == 1 ? 0 : (int)((int64_t)p.steps * part / p.splits);
   const int step1 = p.splits == 1 ? p.steps : (int)((int64_t)p.steps * (part + 1) / p.splits);
 
@@ -406,6 +400,51 @@ __global__ __launch_bounds__(T::kThreads) void wgrad_kernel(const WgradParams p)
   }
 }
 
+// Tile order: an XCD takes a contiguous run; inside it eight k tiles are
+// walked for each n tile, so the 32 tiles an XCD works on at once share about
+// 4 dy panels and 8 code panels (half as wide) in its L2.  (32-bit numbers: a
+// block's share of them is scalar work of a few cycles.)
+template <class T>
+__device__ __forceinline__ void tile_at(const WgradParams& p, uint32_t local, int64_t& n0, int64_t& k0) {
+  const uint32_t n_tiles = (uint32_t)p.n_tiles, k_tiles = (uint32_t)p.k_tiles;
+  const uint32_t band = local / (8 * n_tiles), first_k = 8 * band;
+  const uint32_t wide = k_tiles - first_k < 8 ? k_tiles - first_k : 8;
+  const uint32_t in_band = local - band * 8 * n_tiles, row = in_band / wide;
+  n0 = (int64_t)row * T::kBN;
+  k0 = (int64_t)(first_k + in_band - row * wide) * T::kBK;
+}
+
+using Large = Tile<2, 4, 4, 2>;             // 256 x 256, eight waves of 128 x 64
+using Half = Tile<2, 4, 2, 2, Large::kA>;   // 128 x 256, eight waves of 64 x 64
+using Small = Tile<2, 2, 2, 2>;             // 128 x 128, four waves of 64 x 64
+
+// Blocks 0 .. whole - 1 compute whole tiles, the blocks behind them halves of
+// the remaining ones: a last round that would be at most half full takes half
+// a round's time.  (1376 tiles on 256 compute units: XX us against 1099.)
+template <int G>
+__global__ __launch_bounds__(Large::kThreads) void wgrad_large_kernel(const WgradParams p) {
+  int64_t n0, k0;
+  const uint32_t b = blockIdx.x, whole = (uint32_t)p.whole;
+  if (b < whole) {
+    tile_at<Large>(p, xcd_contiguous32(b, whole), n0, k0);
+    wgrad_tile<Large, G>(p, n0, k0, 0);
+  } else {
+    const uint32_t order = xcd_contiguous32(b - whole, gridDim.x - whole);
+    tile_at<Large>(p, whole + (order >> 1), n0, k0);
+    n0 += Half::kBN * (order & 1);
+    if (n0 < p.N) wgrad_tile<Half, G>(p, n0, k0, 0);
+  }
+}
+
+template <int G>
+__global__ __launch_bounds__(Small::kThreads) void wgrad_small_kernel(const WgradParams p) {
+  int64_t n0, k0;
+  const uint32_t tiles = (uint32_t)p.n_tiles * (uint32_t)p.k_tiles;
+  const uint32_t order = xcd_contiguous32(blockIdx.x, gridDim.x), part = order / tiles;
+  tile_at<Small>(p, order - part * tiles, n0, k0);
+  wgrad_tile<Small, G>(p, n0, k0, part);
+}
+
 // Adds the partial sums of the splits in order, scales and stores.
 __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* partials, int splits, int64_t size, void* dw,
                                                          int out, float scale) {
@@ -435,13 +474,10 @@ __global__ __launch_bounds__(256) void wgrad_zero_kernel(void* dw, int64_t bytes
     *reinterpret_cast<uint4*>((uint8_t*)dw + at) = make_uint4(0, 0, 0, 0);
 }
 
-using Large = Tile<2, 4, 4, 2>;   // 256 x 256, eight waves of 128 x 64
-using Small = Tile<2, 2, 2, 2>;   // 128 x 128, four waves of 64 x 64
-
 template <int G>
-const void* large_fn() { return reinterpret_cast<const void*>(&wgrad_kernel<Large, 4, 4, 2, G>); }
+const void* large_fn() { return reinterpret_cast<const void*>(&wgrad_large_kernel<G>); }
 template <int G>
-const void* small_fn() { return reinterpret_cast<const void*>(&wgrad_kernel<Small, 2, 2, 2, G>); }
+const void* small_fn() { return reinterpret_cast<const void*>(&wgrad_small_kernel<G>); }
 
 const void* wgrad_kernel_for(bool large, int32_t g) {
   switch (g) {
@@ -550,8 +586,12 @@ coat_status_t coat_fp8_weight_grad(const coat_weight_grad_args_t* a, hipStream_t
   p.out = pl.splits > 1 ? (int)kPartial : out;
   p.scale = a->x_scales ? 1.0f : a->x_scale;
   void* args[] = {&p};
+  // the last round of large tiles in halves where that fills it
+  const int64_t tiles = (int64_t)pl.n_tiles * pl.k_tiles, rest = pl.large ? tiles % kUnits : 0;
+  const int64_t halves = 2 * rest <= kUnits ? rest : 0;
+  p.whole = (int32_t)(tiles - halves);
   e = hipLaunchKernel(wgrad_kernel_for(pl.large, a->x_scales ? a->group_size : 0),
-                      dim3((unsigned)((int64_t)pl.n_tiles * pl.k_tiles * pl.splits)),
+                      dim3((unsigned)((tiles + halves) * pl.splits)),
                       dim3(pl.large ? Large::kThreads : Small::kThreads), args, 0, stream);
   if (e == hipSuccess && pl.splits > 1) {
     const float* partials = (const float*)a->workspace;
