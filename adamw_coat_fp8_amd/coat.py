@@ -84,7 +84,15 @@ def _packer(structure):
     flat = []
     for _, t in structure._fields_:
         flat += [u for _, u in t._fields_] if issubclass(t, ctypes.Structure) else [t]
-    return struct.Struct("@" + "".join(codes[t] for t in flat)).pack
+    pack = struct.Struct("@" + "".join(codes[t] for t in flat)).pack
+
+    def packed(*values):
+        try:
+            return pack(*values)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"an argument does not fit its C type: {e}") from None
+
+    return packed
 
 
 class RMSNormArgs(ctypes.Structure):
@@ -497,7 +505,7 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, *, y: Optional[t
              residual_out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
              scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
              group_size: int = 128, stream=None):
-    """RMS norm of h = x (+ residual, written to residual_out) into y (BF16)
+    """RMS norm of h = x (+ residual, written to residual_out, which may be residual) into y (BF16)
     and/or y_codes (E4M3 under the one scale y_scale; y_amax is raised to the
     largest |y|).  codes and scales, if given, receive h's checkpoint and rstd
     the rows' reciprocal root mean squares, for rms_norm_bwd."""
@@ -617,16 +625,29 @@ def _heads(t: torch.Tensor, name: str, like=None):
 
 def _qk_sizes(q, k, q_other, k_other, cos, sin, names):
     """Sizes and strides that both passes take from their heads and tables."""
-    tokens, q_heads, dim, q_stride = _heads(q, names[0])
-    k_tokens, k_heads, k_dim, k_stride = _heads(k, names[1])
-    if k_tokens != tokens or k_dim != dim:
-        raise ValueError(f"{names[0]} and {names[1]} disagree on tokens or head_dim")
-    q_other_stride = _heads(q_other, names[2], q.shape)[3]
-    k_other_stride = _heads(k_other, names[3], k.shape)[3]
+    try:   # the usual case in one look
+        qs, ks = q.shape, k.shape
+        tokens, q_heads, dim = qs
+        k_heads = ks[1]
+        a, b, c, d = q.stride(), k.stride(), q_other.stride(), k_other.stride()
+        plain = (tokens > 0 and ks[0] == tokens and ks[2] == dim and q_other.shape == qs and k_other.shape == ks
+                 and a[1] == b[1] == c[1] == d[1] == dim and a[2] == b[2] == c[2] == d[2] == 1
+                 and (tokens == 1 or a[0] >= q_heads * dim <= c[0] and b[0] >= k_heads * dim <= d[0])
+                 and q.dtype in BF16 and k.dtype in BF16 and q_other.dtype in BF16 and k_other.dtype in BF16)
+    except (AttributeError, ValueError, IndexError):
+        plain = False
+    if plain:
+        strides = (a[0], b[0], c[0], d[0]) if tokens > 1 else (q_heads * dim, k_heads * dim) * 2
+    else:
+        tokens, q_heads, dim, q_stride = _heads(q, names[0])
+        k_tokens, k_heads, k_dim, k_stride = _heads(k, names[1])
+        if k_tokens != tokens or k_dim != dim:
+            raise ValueError(f"{names[0]} and {names[1]} disagree on tokens or head_dim")
+        strides = (q_stride, k_stride, _heads(q_other, names[2], q.shape)[3], _heads(k_other, names[3], k.shape)[3])
     table_rows, half = _shape2(cos, "cos")
     if _shape2(sin, "sin") != cos.shape:
         raise ValueError("cos and sin differ in shape")
-    return tokens, q_heads, k_heads, dim, table_rows, 2 * half, q_stride, k_stride, q_other_stride, k_other_stride
+    return (tokens, q_heads, k_heads, dim, table_rows, 2 * half, *strides)
 
 
 I64_DTYPES = (torch.int64,)

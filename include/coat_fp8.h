@@ -272,7 +272,7 @@ typedef struct coat_rms_norm_args {
   const uint16_t* x;         /* rows x cols BF16                             */
   const uint16_t* residual;  /* rows x cols BF16, or NULL                    */
   const uint16_t* weight;    /* cols BF16                                    */
-  uint16_t* residual_out;    /* h (written), with residual                   */
+  uint16_t* residual_out;    /* h (written), with residual; may be residual  */
   uint16_t* y;               /* BF16 y (written), or NULL                    */
   uint8_t* y_codes;          /* y under one scale (written), or NULL         */
   float* y_amax;             /* optional, see above                          */

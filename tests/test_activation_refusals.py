@@ -243,6 +243,14 @@ def test_binding_rms_norm(coat):
     refuses("codes holds", bwd, codes=u8(4, 255))
 
 
+def test_binding_values_that_do_not_fit(coat):
+    for values in ((0,) * 10 + (1 << 70, 1, 1e-5, 1.0, 128), (0,) * 10 + (1, 1, 1e-5, 1.0, 1 << 40)):
+        refuses("does not fit", coat._pack_rms_norm, *values)
+    # a number past FP32's range is infinite there, and refused as such
+    assert coat.lib.coat_fp8_rms_norm(coat._pack_rms_norm(*(A,) * 10, 4, 256, 1e300, 1.0, 128), None) == INVAL
+    assert len(coat._pack_rms_norm(*(0,) * 10, 1, 1, 1e-5, 1.0, 128)) <= ctypes.sizeof(coat.RMSNormArgs)
+
+
 def test_binding_swiglu(coat):
     refuses("device", coat.swiglu, u8(4, 256), f32(4, 2), h=z(4, 128))
     refuses("even", coat.swiglu, u8(4, 255), f32(4, 2), h=z(4, 128))
