@@ -177,6 +177,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
+// v^-1/2 for normal v: the hardware's (one ulp off) and one Newton step, which
+// leaves little more than the last rounding.
+__device__ __forceinline__ float inv_sqrt(float v) {
+  const float r = __builtin_amdgcn_rsqf(v);
+  const float s = __builtin_fmaf(0.5f * r, __builtin_fmaf(-v * r, r, 1.0f), r);
+  return v > 0x1.fffffep127f ? 0.0f : s;   // infinity
+}
+
 __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
   v = lanes_max_u32<16>(v);
   const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);

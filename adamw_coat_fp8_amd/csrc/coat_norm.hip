@@ -147,7 +147,7 @@ __global__ __launch_bounds__(kMost) void rms_norm_kernel(const NormParams p) {
 #pragma unroll
       for (int i = 0; i < kC; ++i) load(row + gridDim.x, i);
     }
-    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(block_sum<kMost>(ss, slot), p.inv_cols, p.eps));
+    const float rstd = inv_sqrt(__builtin_fmaf(block_sum<kMost>(ss, slot), p.inv_cols, p.eps));
     if (p.rstd && t == 0) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < kC; ++i) {

@@ -213,7 +213,7 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_kernel(const QkPar
     float ss = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(x[e], x[e], ss);
-    float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(lanes_sum<kLanes>(ss), p.inv_dim, p.eps));
+    float rstd = inv_sqrt(__builtin_fmaf(lanes_sum<kLanes>(ss), p.inv_dim, p.eps));
     if (!turn.live) rstd = 0.0f;
     if (p.codes) {
       float scale;
