@@ -12,7 +12,7 @@
 #include <stdint.h>
 #include <string.h>
 
-#include "coat_elem.h"
+#include "coat_common.h"
 
 using namespace coat;
 
@@ -51,6 +51,46 @@ struct ActParams {
   int64_t groups_per_row;
   int32_t t_store;  // bytes per store into the transpose: 16, 8 or 4 (rows a multiple of it), else 1
 };
+
+// Largest BF16 magnitude (as its 15 bits) among the 8 values of a chunk:
+// sign-cleared BF16 patterns order like the magnitudes they encode.
+__device__ __forceinline__ uint32_t bf16x8_max_mag(uint4 r) {
+  const uint32_t a = max(r.x & 0x7FFFu, (r.x >> 16) & 0x7FFFu);
+  const uint32_t b = max(r.y & 0x7FFFu, (r.y >> 16) & 0x7FFFu);
+  const uint32_t c = max(r.z & 0x7FFFu, (r.z >> 16) & 0x7FFFu);
+  const uint32_t d = max(r.w & 0x7FFFu, (r.w >> 16) & 0x7FFFu);
+  return max(max(a, b), max(c, d));
+}
+
+__device__ __forceinline__ uint32_t act_pack4(uint32_t w0, uint32_t w1, const GroupQuot& d) {
+  const float q0 = group_quot(bf16_lo(w0), d), q1 = group_quot(bf16_hi(w0), d);
+  const float q2 = group_quot(bf16_lo(w1), d), q3 = group_quot(bf16_hi(w1), d);
+  int v = __builtin_amdgcn_cvt_pk_fp8_f32(q0, q1, 0, false);
+  v = __builtin_amdgcn_cvt_pk_fp8_f32(q2, q3, v, true);
+  return (uint32_t)v;
+}
+
+// Streaming accesses of the quantizer: every byte is read or written once, so
+// the loads and stores are nontemporal.  Measured on MI355X with inputs that
+// do not fit in the last-level cache, this lifts the transposing kernel from
+// about 4.6 to 5.1 TB/s at 8192 x 11008.
+typedef unsigned u32x2v __attribute__((ext_vector_type(2)));
+typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint4 load_stream16(const void* p) {
+  const u32x4v v = __builtin_nontemporal_load(reinterpret_cast<const u32x4v*>(p));
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+__device__ __forceinline__ void store_stream8(void* p, uint2 v) {
+  const u32x2v w = {v.x, v.y};
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x2v*>(p));
+}
+
+__device__ __forceinline__ void store_stream16(void* p, uint4 v) {
+  const u32x4v w = {v.x, v.y, v.z, v.w};
+  __builtin_nontemporal_store(w, reinterpret_cast<u32x4v*>(p));
+}
 
 // LDS tile: kRows rows of 32 dwords.  The dword column is XOR-swizzled by the
 // row's 16-row block so that the transpose phase's column reads (one dword

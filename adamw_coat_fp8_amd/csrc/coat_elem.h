@@ -15,9 +15,8 @@ typedef unsigned u32x2v __attribute__((ext_vector_type(2)));
 typedef unsigned u32x4v __attribute__((ext_vector_type(4)));
 
 // Streaming accesses: every byte is read or written once, so the loads and
-// stores are nontemporal.  Measured on MI355X with inputs that do not fit in
-// the last-level cache, this lifts the transposing activation quantizer from
-// about 4.6 to 5.1 TB/s at 8192 x 11008.
+// stores are nontemporal, as in the activation quantizer (whose own file has
+// the measurement).
 __device__ __forceinline__ uint4 load_stream16(const void* p) {
   const u32x4v v = __builtin_nontemporal_load(reinterpret_cast<const u32x4v*>(p));
   return make_uint4(v.x, v.y, v.z, v.w);

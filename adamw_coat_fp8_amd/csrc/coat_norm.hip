@@ -33,6 +33,10 @@ namespace {
 // reduced.  The sum of squares is FP32: eight values of a lane in order,
 // then lanes, then waves (LDS, two slots in turn, one barrier a row).  A
 // checkpoint group lies on G/8 neighbouring lanes of one 16-lane DPP row.
+//
+// Bound by HBM: 8192 x 4096 with residual, E4M3 output and checkpoint (8.03
+// bytes a value) takes 48.5 us, 5.56 TB/s; vector instructions issue in 38% of
+// the cycles.  A grid of one block a row, without the loads ahead, took 51.5.
 
 constexpr int64_t kMaxCols = 32768;
 
@@ -197,6 +201,11 @@ __global__ __launch_bounds__(kMost) void rms_norm_kernel(const NormParams p) {
 // columns up in registers, in FP32, writing one row of partial sums at its
 // end.  A second launch adds those up in a fixed order, so the result does
 // not depend on timing.
+//
+// 8192 x 4096 with d_residual: 41.4 us (5.7 TB/s) and 4.1 for the second
+// launch, most of it latency.  Few rows a block cost more: 4097 x 5120 (17
+// rows a block) 23.5 + 4.0 us, 4.6 TB/s.  Two rows at a time, for more loads in
+// flight, needs twice the registers and took 63 us where one takes 45.
 
 struct NormBwdParams {
   const uint16_t* dy;

@@ -35,6 +35,9 @@ namespace {
 // arithmetic, which had bound the kernel.
 // A token whose position is outside the table is padding: everything written
 // for it is zero.
+//
+// 8192 tokens, 64 heads of 128 values, with checkpoint: 59.6 us, 5.74 TB/s, at
+// 65% vector issue (67 us before the weights were folded in).
 
 struct QkParams {
   const uint16_t* q;        // forward: heads; backward: their output gradients
@@ -241,7 +244,8 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_kernel(const QkPar
 //   dn = dy w,  dx = rstd (dn - n mean(dn n)),  dw = sum over tokens and heads of dy n
 // Waves walk (token, slab) units with a stride and keep dy n of their chunk
 // in FP32 registers, queries and keys apart; a block joins its lanes' sums in
-// the LDS in a fixed order and writes one row of partial sums.
+// the LDS in a fixed order and writes one row of partial sums.  64 heads of 128
+// values over 8192 tokens: 64.7 us, 5.3 TB/s, 4 of them the second launch.
 template <int kLanes, int kH>
 __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const QkParams p) {
   constexpr int kSet = 64 / kLanes;
