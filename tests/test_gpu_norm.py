@@ -13,7 +13,8 @@ EPS = 1e-5
 # one wave a row up to 1024 threads of four chunks; odd rows; more rows than blocks
 SHAPES = [(1, 16, 16), (3, 48, 16), (5, 512, 128), (2, 528, 16), (7, 1024, 64), (9, 1040, 16), (4, 2048, 32),
           (1, 4096, 128), (33, 4096, 128), (600, 4064, 32), (5, 4112, 16), (3, 8192, 64), (2, 11008, 128),
-          (2, 16384, 128), (2, 16400, 16), (3, 32768, 128), (2100, 256, 64)]
+          (2, 16384, 128), (2, 16400, 16), (3, 32768, 128), (2100, 256, 64), (128, 512, 64), (129, 512, 16), (500, 2048, 32),
+          (513, 4096, 128)]
 
 
 @pytest.fixture(autouse=True)
@@ -122,9 +123,10 @@ def backward(dy, codes, scales, rstd, w, G, d_residual=None, dw=True, accumulate
 
 
 def chain(rows):
-    """FP32 additions behind one value of dw: the rows of one of 512 blocks,
-    8 partial sums of a slice, 6 joins, and the product's roundings."""
-    return -(-rows // 512) + 8 + 6 + 4
+    """FP32 additions behind one value of dw: the rows of one of at least 256
+    blocks, 8 partial sums of a slice, 6 joins, and the product's roundings; up
+    to 512 rows may go in slices of at most 32, and 6 joins."""
+    return max(-(-rows // 256) + 8, 32 if rows <= 512 else 0) + 6 + 4
 
 
 @pytest.mark.parametrize("rows,cols,G", SHAPES)
