@@ -84,9 +84,8 @@ __device__ __forceinline__ void load4(const float* p, float* f) {
 }
 
 // dir = 1 forward, -1 for the transposed rotation of the backward pass.
-__device__ __forceinline__ Turn load_turn(const QkParams& p, int64_t token, int chunk, float dir) {
+__device__ __forceinline__ Turn load_turn(const QkParams& p, int64_t pos, int chunk, float dir) {
   Turn r;
-  const int64_t pos = p.positions[token];
   r.live = pos >= 0 && pos < p.table_rows;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -189,7 +188,7 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_kernel(const QkPar
     raw[i] = make_uint4(0, 0, 0, 0);
     if (on && head < s.heads) raw[i] = load_stream16(at(s.in, head * p.dim + 8 * chunk));
   }
-  const Turn turn = load_turn(p, s.token, chunk, 1.0f);
+  const Turn turn = load_turn(p, p.positions[s.token], chunk, 1.0f);
   const int addr = partner_lane(p, lane, chunk), lanes = 1 << (p.group_shift - 3);
   float own[8], other[8];   // what a value and its partner are multiplied with, but for rstd
   {
@@ -256,12 +255,15 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
 #pragma unroll
   for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.0f;
   const uint32_t step = gridDim.x * kWavesPerBlock;
-  // The next unit's heads are loaded before the current one's are worked on.
+  // The next unit's heads and position are loaded before the current one's
+  // are worked on.
   uint4 raw_n[kH];
   uint2 code_n[kH];
   float scale_n[kH], rs_n[kH];
+  int64_t pos_n = 0;
   auto load = [&](uint32_t unit) __attribute__((always_inline)) {
     const Slab s = slab_of<kSet, kH>(p, unit);
+    pos_n = p.positions[s.token];
 #pragma unroll
     for (int i = 0; i < kH; ++i) {
       const int head = s.first + kSet * i + sub;
@@ -281,7 +283,7 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
   if (unit < (uint32_t)p.units) load(unit);
   for (; unit < (uint32_t)p.units; unit += step) {
     const Slab s = slab_of<kSet, kH>(p, unit);
-    const Turn turn = load_turn(p, s.token, chunk, -1.0f);
+    const Turn turn = load_turn(p, pos_n, chunk, -1.0f);
     uint4 raw[kH];
     uint2 code[kH];
     float scale[kH], rs[kH];
