@@ -44,7 +44,7 @@ namespace {
 // Bound by the matrix cores and the power they may draw: 8192 x 22016 x 4096
 // under one scale takes 1028 us (1.437 PFLOP/s; a library product of the same
 // sizes in BF16 takes 1163 us with both operands contraction-minor and 1410 as
-// they lie here), the MFMAs busy 78% of the cycles at about 1.6 GHz.  With
+// they lie here), the MFMAs busy 81% of the cycles at about 1.7 GHz.  With
 // group scales the expansion is 16 vector instructions a fragment and not 4,
 // and takes 1250 us (1.18 PFLOP/s).  A 128 x 128 tile by eight waves of
 // 64 x 32 is bound by LDS reads (2048 cubed: 21.2 us against 19.9).
