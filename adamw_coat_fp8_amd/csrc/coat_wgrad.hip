@@ -499,9 +499,13 @@ __global__ __launch_bounds__(256) void wgrad_join_kernel(const float* partials, 
   const int64_t at = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
   if (at >= size) return;
   float4 v = *reinterpret_cast<const float4*>(partials + at);
-  for (int s = 1; s < splits; ++s) {
-    const float4 o = *reinterpret_cast<const float4*>(partials + s * size + at);
-    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  for (int s = 1; s < splits; s += 8) {   // eight loads in flight at a time
+    float4 o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      o[i] = s + i < splits ? *reinterpret_cast<const float4*>(partials + (s + i) * size + at) : make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v.x += o[i].x, v.y += o[i].y, v.z += o[i].z, v.w += o[i].w;
   }
   v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
   if (out == kBF16) {
@@ -539,6 +543,7 @@ const void* wgrad_kernel_for(bool large, int32_t g) {
 
 constexpr int64_t kMaxDim = 1 << 24;     // 64 rows of dy stay below 2^32 bytes
 constexpr int64_t kMaxTiles = 1 << 23;   // of 128 x 128: a launch's threads stay below 2^32
+constexpr int64_t kLargeTiles = 208;
 constexpr int64_t kUnits = 256;          // compute units of the device the split is made for
 
 struct Plan {
@@ -546,15 +551,17 @@ struct Plan {
   int32_t n_tiles, k_tiles, splits;
 };
 
-// Large tiles where they fill the compute units once, else small ones (two
-// blocks to a unit).  Where even those leave units empty and there are rows
+// Large tiles where they fill most of the compute units once, else small ones
+// (two blocks to a unit): a round of large tiles takes 190 us at 8192 rows,
+// small ones 0.227 each, which meet at 208 large tiles (240 of them, 8192 x
+// 3840 x 4096: XX us, and 218 as small ones).  Where even those leave units empty and there are rows
 // for it, the rows are split, 256 rows to a part at least, and the parts
 // joined from the workspace.  A function of the sizes alone, so that the
 // workspace and the order of the sums are.
 Plan plan(int64_t M, int64_t N, int64_t K) {
   Plan p;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  p.large = up(N, Large::kBN) * up(K, Large::kBK) >= kUnits;
+  p.large = up(N, Large::kBN) * up(K, Large::kBK) >= kLargeTiles;
   p.n_tiles = (int32_t)up(N, p.large ? Large::kBN : Small::kBN);
   p.k_tiles = (int32_t)up(K, p.large ? Large::kBK : Small::kBK);
   const int64_t tiles = (int64_t)p.n_tiles * p.k_tiles;
