@@ -543,7 +543,6 @@ const void* wgrad_kernel_for(bool large, int32_t g) {
 
 constexpr int64_t kMaxDim = 1 << 24;     // 64 rows of dy stay below 2^32 bytes
 constexpr int64_t kMaxTiles = 1 << 23;   // of 128 x 128: a launch's threads stay below 2^32
-constexpr int64_t kLargeTiles = 208;
 constexpr int64_t kUnits = 256;          // compute units of the device the split is made for
 
 struct Plan {
@@ -551,17 +550,21 @@ struct Plan {
   int32_t n_tiles, k_tiles, splits;
 };
 
-// Large tiles where they fill most of the compute units once, else small ones
-// (two blocks to a unit): a round of large tiles takes 190 us at 8192 rows,
-// small ones 0.227 each, which meet at 208 large tiles (240 of them, 8192 x
-// 3840 x 4096: XX us, and 218 as small ones).  Where even those leave units empty and there are rows
-// for it, the rows are split, 256 rows to a part at least, and the parts
-// joined from the workspace.  A function of the sizes alone, so that the
-// workspace and the order of the sums are.
+// Small tiles as long as each has a compute unit to itself (2048 x 2048 over
+// 8192 rows: 60 us, 69 as large ones).  Beyond that two share a unit, and large
+// tiles, which read half as much a product and run as halves where there are
+// few, are faster: 72 of them (2304 x 2048) 76 us against 88 as small ones, 121
+// (2816 x 2816) 99 against 108, 240 (3840 x 4096) 181 against 211.  Not where
+// they would multiply over a quarter more padding: 272 x 16640 takes 128 us in
+// large tiles and 107 in small, 128 x 65536 198 and 152.  Where even small ones
+// leave units empty and there are rows for it, the rows are split, 256 rows to
+// a part at least, and the parts joined from the workspace.  A function of the
+// sizes alone, so that the workspace and the order of the sums are.
 Plan plan(int64_t M, int64_t N, int64_t K) {
   Plan p;
   auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
-  p.large = up(N, Large::kBN) * up(K, Large::kBK) >= kLargeTiles;
+  const int64_t small = up(N, Small::kBN) * up(K, Small::kBK);
+  p.large = small > kUnits && 16 * up(N, Large::kBN) * up(K, Large::kBK) <= 5 * small;
   p.n_tiles = (int32_t)up(N, p.large ? Large::kBN : Small::kBN);
   p.k_tiles = (int32_t)up(K, p.large ? Large::kBK : Small::kBK);
   const int64_t tiles = (int64_t)p.n_tiles * p.k_tiles;

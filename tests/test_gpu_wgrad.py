@@ -35,7 +35,8 @@ def product(dy, x):
 # one and several row splits; 256 tiles of 256 x 256 (the large ones) with edges
 SHAPES = [(1, 16, 16), (2, 16, 128), (63, 128, 128), (64, 144, 128), (65, 128, 256), (128, 272, 384), (129, 16, 640),
           (193, 400, 128), (256, 128, 128), (511, 48, 256), (700, 512, 640), (1024, 128, 128), (4000, 128, 256),
-          (2085, 656, 128), (1, 4096, 4096), (70, 4112, 4096), (200, 3856, 4224), (333, 2048, 2048), (130, 16, 16384)]
+          (2085, 656, 128), (1, 4096, 4096), (70, 4112, 4096), (200, 3856, 4224), (333, 2048, 2048), (130, 16, 16384),
+          (130, 2816, 2816), (70, 2064, 2176), (200, 3328, 3328), (33, 128, 33280), (65, 144, 33280)]
 
 
 def integers(m, n, k, seed):
