@@ -192,7 +192,8 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_kernel(const QkPar
   const int addr = partner_lane(p, lane, chunk), lanes = 1 << (p.group_shift - 3);
   float own[8], other[8];   // what a value and its partner are multiplied with, but for rstd
   {
-    const uint4 w = on ? *reinterpret_cast<const uint4*>(at(s.weight, 8 * chunk)) : make_uint4(0, 0, 0, 0);
+    uint4 w = on ? *reinterpret_cast<const uint4*>(at(s.weight, 8 * chunk)) : make_uint4(0, 0, 0, 0);
+    if (!turn.live) w = make_uint4(0, 0, 0, 0);   // padding stays zero whatever the weight holds
     float f[8], g[8];
     unpack8(w, f);
     if (p.interleaved)
@@ -291,14 +292,16 @@ __global__ __launch_bounds__(kBlockThreads) void qk_norm_rope_bwd_kernel(const Q
     for (int i = 0; i < kH; ++i) raw[i] = raw_n[i], code[i] = code_n[i], scale[i] = scale_n[i], rs[i] = rs_n[i];
     if (unit + step < (uint32_t)p.units) load(unit + step);
     float w[8], g[8];
-    unpack8(on ? *reinterpret_cast<const uint4*>(at(s.weight, 8 * chunk)) : make_uint4(0, 0, 0, 0), w);
+    uint4 rw = on ? *reinterpret_cast<const uint4*>(at(s.weight, 8 * chunk)) : make_uint4(0, 0, 0, 0);
+    if (!turn.live) rw = make_uint4(0, 0, 0, 0);
+    unpack8(rw, w);
 #pragma unroll
     for (int e = 0; e < 8; ++e) g[e] = 0.0f;
 #pragma unroll
     for (int i = 0; i < kH; ++i) {
       const int head = s.first + kSet * i + sub;
       float d[8], far[8], n[8];
-      if (!turn.live) {   // padding: nothing of it counts, whatever its buffers hold
+      if (!turn.live) {   // padding: nothing of it counts, whatever its buffers and the weight hold
         raw[i] = make_uint4(0, 0, 0, 0);
         code[i] = make_uint2(0, 0);
         scale[i] = rs[i] = 0.0f;
