@@ -247,6 +247,13 @@ def _stream(stream) -> Optional[int]:
     return int(stream)
 
 
+def _fits_c_int(group_size):
+    """ctypes cuts a number to the argument's 32 bits: the size that the
+    library would see is then not the one the buffers were checked for."""
+    if not -(1 << 31) <= group_size < 1 << 31:
+        raise ValueError(f"group_size {group_size} does not fit its C type")
+
+
 def num_groups(n: int, group_size: int) -> int:
     return (n + group_size - 1) // group_size
 
@@ -269,6 +276,7 @@ class QuantState:
         return FP8State(_ptr(self.codes), _ptr(self.scale), _ptr(self.k))
 
     def check(self, n: int, group_size: int, name: str):
+        _fits_c_int(group_size)
         _need(self.codes, f"{name}.codes", CODE_DTYPES, n)
         _need(self.scale, f"{name}.scale", F32_DTYPES, num_groups(n, group_size))
         _need(self.k, f"{name}.k", F32_DTYPES, num_groups(n, group_size))
@@ -390,6 +398,7 @@ def quantize_act(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor,
     if x.dim() != 2:
         raise ValueError("quantize_act expects a 2-D (rows, cols) tensor")
     rows, cols = x.shape
+    _fits_c_int(group_size)
     _need(x, "x", BF16_DTYPES, 0)
     _need(codes, "codes", CODE_DTYPES, rows * cols)
     _need(scales, "scales", F32_DTYPES, rows * (cols // max(group_size, 1)))
@@ -410,6 +419,7 @@ def gemm_group_quant(a: torch.Tensor, b: torch.Tensor, a_scale: float, b_scale: 
     N = b.shape[0]
     if b.shape[1] != K:
         raise ValueError("a and b disagree on K")
+    _fits_c_int(group_size)
     _need(a, "a", CODE_DTYPES, 0)
     _need(b, "b", CODE_DTYPES, 0)
     _need(codes, "codes", CODE_DTYPES, M * N)
@@ -596,6 +606,7 @@ def swiglu_bwd(dh: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, d_ga
     """Gradient of swiglu from its checkpoint: d_gate_up (BF16), the gates'
     gradients first in each row."""
     rows, cols = _shape2(dh, "dh")
+    _fits_c_int(group_size)
     (a, b, c, d), current = _addresses((
         (dh, "dh", BF16, 0), (codes, "codes", CODES, 2 * rows * cols),
         (scales, "scales", F32, 2 * rows * _groups(cols, group_size)),
