@@ -743,6 +743,8 @@ def weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales, dw: torch.Tensor,
         x_scale = scales
     else:
         raise ValueError("scales must be a float32 tensor or a number")
+    if not isinstance(dw, torch.Tensor):
+        raise ValueError("dw must be a torch.Tensor")
     ws_bytes = _workspace(workspace, weight_grad_workspace(rows, n, k))
     (py, px, ps, pw, ws), current = _addresses((
         (dy, "dy", BF16, 0), (codes, "codes", CODES, 0),

@@ -36,3 +36,23 @@ def test_group_size_past_a_c_int(coat, G):
     for call in calls:
         with pytest.raises(ValueError, match="does not fit"):
             call()
+
+
+def on_device(monkeypatch, coat):
+    """The binding's checks as they go for buffers on the current device:
+    every one is taken, at address 0x10000, and the library is not called."""
+    calls = []
+    monkeypatch.setattr(coat, "_addresses", lambda buffers, heads=(): (
+        [0 if b[0] is None else 0x10000 for b in (*buffers, *heads)], 0))
+    monkeypatch.setattr(coat, "_launch", lambda fn, packed, stream, current: calls.append(packed))
+    return calls
+
+
+def test_weight_grad_without_dw(monkeypatch, coat):
+    calls = on_device(monkeypatch, coat)
+    coat.weight_grad(bf16(4, 128), u8(4, 128), 0.5, torch.zeros(128, 128))
+    assert len(calls) == 1
+    for dw in (None, 3.0):
+        with pytest.raises(ValueError, match="dw must be"):
+            coat.weight_grad(bf16(4, 128), u8(4, 128), 0.5, dw)
+    assert len(calls) == 1
