@@ -531,10 +531,13 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, *, y: Optional[t
 
 def rms_norm_bwd_workspace(rows: int, cols: int) -> int:
     """Bytes of workspace rms_norm_bwd needs for a weight gradient."""
-    return _workspace_bytes(lib.coat_fp8_rms_norm_bwd_workspace(rows, cols))
+    return _workspace_bytes(lib.coat_fp8_rms_norm_bwd_workspace, rows, cols)
 
 
-def _workspace_bytes(n: int) -> int:
+def _workspace_bytes(fn, *sizes: int) -> int:
+    if max(sizes) >= 1 << 63 or min(sizes) < 0:   # (ctypes would cut them to 64 bits)
+        _check(COAT_ERR_INVALID_VALUE)
+    n = fn(*sizes)
     if n < 0:
         _check(COAT_ERR_INVALID_VALUE)
     return n
@@ -691,7 +694,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
 def qk_norm_rope_bwd_workspace(tokens: int, heads: int, head_dim: int) -> int:
     """Bytes of workspace qk_norm_rope_bwd needs for weight gradients (heads:
     queries and keys)."""
-    return _workspace_bytes(lib.coat_fp8_qk_norm_rope_bwd_workspace(tokens, heads, head_dim))
+    return _workspace_bytes(lib.coat_fp8_qk_norm_rope_bwd_workspace, tokens, heads, head_dim)
 
 
 def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, codes: torch.Tensor,
@@ -722,7 +725,7 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, codes: torch.Te
 
 def weight_grad_workspace(rows: int, n: int, k: int) -> int:
     """Bytes of workspace weight_grad needs (0: none)."""
-    return _workspace_bytes(lib.coat_fp8_weight_grad_workspace(rows, n, k))
+    return _workspace_bytes(lib.coat_fp8_weight_grad_workspace, rows, n, k)
 
 
 def weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales, dw: torch.Tensor, *,

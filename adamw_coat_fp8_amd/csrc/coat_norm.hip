@@ -495,11 +495,14 @@ int64_t norm_parts(int64_t rows, int64_t cols) {
   return balanced(rows, 256 * (threads >= 512 ? 1 : threads >= 128 ? 512 / threads : 4));
 }
 
+bool norm_sizes_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && cols >= 0 && cols <= kMaxCols && rows <= INT64_MAX / 8 / kMaxCols;
+}
+
 coat_status_t check_norm_shape(int64_t rows, int64_t cols, int32_t group_size) {
   if (rows < 0 || cols < 0) return COAT_ERR_INVALID_VALUE;
   if (!valid_group_size(group_size)) return COAT_ERR_GROUP_SIZE;
-  if (cols % group_size != 0 || cols > kMaxCols) return COAT_ERR_INVALID_VALUE;
-  if (rows > INT64_MAX / 8 / kMaxCols) return COAT_ERR_INVALID_VALUE;
+  if (cols % group_size != 0 || !norm_sizes_ok(rows, cols)) return COAT_ERR_INVALID_VALUE;
   return COAT_OK;
 }
 
@@ -566,7 +569,7 @@ coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* a, hipStream_t strea
 }
 
 int64_t coat_fp8_rms_norm_bwd_workspace(int64_t rows, int64_t cols) {
-  if (rows < 0 || cols < 0 || cols > kMaxCols) return -1;
+  if (!norm_sizes_ok(rows, cols) || cols % 16 != 0) return -1;
   return cols == 0 ? 0 : norm_parts(rows, cols) * cols * (int64_t)sizeof(float);
 }
 

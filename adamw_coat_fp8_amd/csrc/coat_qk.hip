@@ -513,8 +513,9 @@ int64_t coat_fp8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads, int64
       tokens > kMaxUnits)
     return -1;
   if (tokens == 0 || heads == 0) return 0;
-  // the most units that any division of the heads into queries and keys gives
-  const int64_t set = 64 / lanes_for(head_dim), units = tokens * ((heads + set - 1) / set + 1);
+  // the fewest and the most units that a division of the heads into queries and keys gives
+  const int64_t set = 64 / lanes_for(head_dim), least = tokens * ((heads + set - 1) / set), units = least + tokens;
+  if (least > kMaxUnits) return -1;
   return qk_parts(units, 1) * 2 * head_dim * (int64_t)sizeof(float);
 }
 

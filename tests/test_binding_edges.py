@@ -56,3 +56,32 @@ def test_weight_grad_without_dw(monkeypatch, coat):
         with pytest.raises(ValueError, match="dw must be"):
             coat.weight_grad(bf16(4, 128), u8(4, 128), 0.5, dw)
     assert len(calls) == 1
+
+
+I64 = (1 << 63) - 1
+
+
+@pytest.mark.parametrize("rows,cols", [(I64, 16), (I64 - 100, 4096), (1 << 60, 32768), (4, 24), (4, 8), (0, 8),
+                                       ((1 << 64) + 4, 4096), (4, (1 << 64) + 4096)])
+def test_norm_workspace_of_sizes_that_the_call_refuses(coat, rows, cols):
+    with pytest.raises((coat.CoatError, ValueError)):
+        coat.rms_norm_bwd_workspace(rows, cols)
+
+
+@pytest.mark.parametrize("tokens,heads,dim", [((1 << 31) - 300000, 8, 128), ((1 << 29), 64, 128), (1 << 20, 1 << 17, 256),
+                                              ((1 << 64) + 4, 8, 128), (I64, 1, 16)])
+def test_heads_workspace_of_sizes_that_the_call_refuses(coat, tokens, heads, dim):
+    """However the heads divide into queries and keys."""
+    with pytest.raises((coat.CoatError, ValueError)):
+        coat.qk_norm_rope_bwd_workspace(tokens, heads, dim)
+
+
+def test_weight_grad_workspace_past_64_bits(coat):
+    for sizes in (((1 << 64) + 64, 128, 128), (64, (1 << 64) + 128, 128), (64, 128, (1 << 64) + 128)):
+        with pytest.raises((coat.CoatError, ValueError)):
+            coat.weight_grad_workspace(*sizes)
+
+
+def test_workspaces_at_the_largest_sizes(coat):
+    assert coat.rms_norm_bwd_workspace(I64 // 8 // 32768, 4096) == coat.rms_norm_bwd_workspace(1 << 40, 4096) > 0
+    assert coat.qk_norm_rope_bwd_workspace(1 << 26, 64, 128) == 1024 * 2 * 128 * 4
