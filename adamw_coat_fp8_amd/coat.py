@@ -570,7 +570,7 @@ def rms_norm_bwd(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, rs
                  d_residual: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                  accumulate: bool = False, group_size: int = 128, stream=None):
     """Gradient of rms_norm from its checkpoint: dx (BF16, d_residual added if
-    given) and, if given, dw (FP32, written or accumulated; needs
+    given; not dy itself, which is read again after it is written) and, if given, dw (FP32, written or accumulated; needs
     rms_norm_bwd_workspace(rows, cols) bytes of workspace)."""
     rows, cols = _shape2(dy, "dy")
     n = rows * cols

@@ -349,8 +349,8 @@ __global__ __launch_bounds__(kMost) void rms_norm_bwd_kernel(const NormBwdParams
 // Few rows: one launch and no partial sums.  Blocks 0 .. rows - 1 take a row
 // each; every block behind them takes the weight gradient of 128 columns: 16
 // threads of eight columns, blockDim / 16 slices of the rows, which join in
-// the LDS in a fixed order.  The rows are read a second time, from the L2.  A
-// call this small is as long as its launches: 1 to 512 rows of 4096 take 7.7
+// the LDS in a fixed order.  The rows are read a second time, by blocks that
+// may run before or after the row's own, so dx must not be dy.  A call this small is as long as its launches: 1 to 512 rows of 4096 take 7.7
 // us, with two launches 10.7.  At more than about 32 rows a slice the second
 // reading shows (256 x 512, 64 rows a slice: 13.2 us against 11.0).
 constexpr int kFewCols = 128;
@@ -587,6 +587,7 @@ coat_status_t coat_fp8_rms_norm_bwd(const coat_rms_norm_bwd_args_t* a, hipStream
     return COAT_ERR_MISALIGNED;
   if (a->dw && a->rows > 0 && a->workspace_bytes < coat_fp8_rms_norm_bwd_workspace(a->rows, a->cols))
     return COAT_ERR_INVALID_VALUE;
+  if (a->rows > 0 && (const void*)a->dx == (const void*)a->dy) return COAT_ERR_INVALID_VALUE;   // (see the kernel of few rows)
   const bool few = a->dw && a->rows > 0 && few_rows(a->rows, norm_shape(a->cols, true).threads);
   const int64_t blocks = norm_parts(a->rows, a->cols);
   hipError_t e = hipSuccess;

@@ -292,9 +292,9 @@ coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* args,
  *   dx = rstd * (dn - n * mean(dn * n)) (+ d_residual),
  *   dw = sum over rows of dy * n.
  * d_residual is the gradient that reaches residual_out from elsewhere; dx is
- * then the gradient of both x and residual.
+ * then the gradient of both x and residual.  dx must not be dy.
  * Errors: as above (codes, scales and rstd are required; workspace with dw;
- * INVALID_VALUE for a workspace that is too small).
+ * INVALID_VALUE for a workspace that is too small and for dx == dy).
  */
 typedef struct coat_rms_norm_bwd_args {
   const uint16_t* dy;          /* rows x cols BF16                           */

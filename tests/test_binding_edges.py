@@ -85,3 +85,14 @@ def test_weight_grad_workspace_past_64_bits(coat):
 def test_workspaces_at_the_largest_sizes(coat):
     assert coat.rms_norm_bwd_workspace(I64 // 8 // 32768, 4096) == coat.rms_norm_bwd_workspace(1 << 40, 4096) > 0
     assert coat.qk_norm_rope_bwd_workspace(1 << 26, 64, 128) == 1024 * 2 * 128 * 4
+
+
+def test_norm_backward_over_its_own_input(coat):
+    """Up to 512 rows other blocks read dy after a row's dx is written."""
+    import ctypes
+    A, B = 0x10000, 0x20000
+    base = dict(dy=A, codes=A, scales=A, rstd=A, weight=A, rows=4, cols=256, group_size=128, workspace=B,
+                workspace_bytes=1 << 20)
+    for change in (dict(dx=A, dw=B), dict(dx=A), dict(dx=A, rows=100000, dw=B, workspace_bytes=1 << 30)):
+        a = coat.RMSNormBwdArgs(**{**base, **change})
+        assert coat.lib.coat_fp8_rms_norm_bwd(ctypes.byref(a), None) == coat.COAT_ERR_INVALID_VALUE
