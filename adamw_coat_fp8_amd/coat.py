@@ -243,6 +243,9 @@ def _stream(stream) -> Optional[int]:
         # 3 us, as long as a small kernel
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != torch.cuda.current_device():
+            raise ValueError(f"stream is on cuda:{stream.device_index}, but the current device "
+                             f"is cuda:{torch.cuda.current_device()}")
         return stream.cuda_stream
     return int(stream)
 

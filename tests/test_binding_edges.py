@@ -96,3 +96,15 @@ def test_norm_backward_over_its_own_input(coat):
     for change in (dict(dx=A, dw=B), dict(dx=A), dict(dx=A, rows=100000, dw=B, workspace_bytes=1 << 30)):
         a = coat.RMSNormBwdArgs(**{**base, **change})
         assert coat.lib.coat_fp8_rms_norm_bwd(ctypes.byref(a), None) == coat.COAT_ERR_INVALID_VALUE
+
+
+def test_stream_of_another_device(monkeypatch, coat):
+    class Stream:
+        def __init__(self, device_index):
+            self.device_index, self.cuda_stream = device_index, 77
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert coat._stream(Stream(1)) == 77 and coat._stream(77) == 77
+    with pytest.raises(ValueError, match="cuda:0.*cuda:1"):
+        coat._stream(Stream(0))
