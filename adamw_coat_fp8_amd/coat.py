@@ -473,7 +473,7 @@ def _addresses(buffers, heads=()):
                 continue
             d = t.get_device()
             if d != dev:
-                if dev is not None or d < 0 or d != torch._C._cuda_getDevice():
+                if dev is not None or d < 0 or d != torch.cuda.current_device():
                     return _refuse(buffers, heads)
                 dev = d
             if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < n:

@@ -108,3 +108,16 @@ def test_stream_of_another_device(monkeypatch, coat):
     assert coat._stream(Stream(1)) == 77 and coat._stream(77) == 77
     with pytest.raises(ValueError, match="cuda:0.*cuda:1"):
         coat._stream(Stream(0))
+
+
+def test_current_device_by_its_public_name(monkeypatch, coat):
+    """The seven activation calls' check of the device, without torch's
+    private query."""
+    class Tensor:
+        dtype = torch.bfloat16
+        get_device, is_contiguous, numel, data_ptr = (lambda s: 1), (lambda s: True), (lambda s: 8), (lambda s: 0x10000)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 70 + d, raising=False)
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    assert coat._addresses(((Tensor(), "x", coat.BF16, 8), (None, "y", coat.F32, 8))) == ([0x10000, 0], 71)
