@@ -737,7 +737,8 @@ def weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales, dw: torch.Tensor,
     """dw = dy^T X for a linear layer whose input X (rows x K) was kept as E4M3
     codes: with group scales (a float32 tensor, rows x K/group_size) or under
     one scale (a number).  dy is rows x N BF16, dw N x K BF16 or float32; a
-    float32 dw can be accumulated into.  Needs weight_grad_workspace bytes."""
+    float32 dw can be accumulated into.  Group scales round X to BF16 for a
+    BF16 dw; a float32 one holds it to 2^-16, in twice the products.  Needs weight_grad_workspace bytes."""
     rows, n = _shape2(dy, "dy")
     x_rows, k = _shape2(codes, "codes")
     if x_rows != rows:

@@ -29,8 +29,13 @@ namespace {
 // each lane its column.  The codes become BF16 in registers, on the way into
 // the MFMA: under one scale their values are exact in BF16 and the scale
 // multiplies the FP32 result; with group scales, which change along m, the
-// product code * S is rounded to BF16 (2^-9 of a value that E4M3 had already
-// rounded by up to 2^-4).  Sums are FP32 in the matrix cores.
+// product code * S is rounded to BF16 (by up to 2^-8 of a value that E4M3 had
+// already rounded by up to 2^-4).  That rounding alone leaves a relative error
+// of 1.7e-3 (norms, random scales): as much as rounding the result to BF16
+// does, 2.3e-3 together, and all the error of an FP32 result.  So an FP32
+// result takes code * S in two BF16 parts (the second what the first left) and
+// two MFMAs: 2.6e-6, at 1.78 times the time (8192 x 4096 x 4096, G = 128: 411 us
+// against 230); a BF16 result takes one.  Sums are FP32 in the matrix cores.
 //
 // A block computes a kBN x kBK tile of dW; kWN x kWK waves own kJ x kI tiles
 // of 32 x 32.  64 rows a step, three LDS stages.  A step is four substeps of
@@ -46,7 +51,7 @@ namespace {
 // sizes in BF16 takes 1163 us with both operands contraction-minor and 1410 as
 // they lie here), the MFMAs busy 81% of the cycles at about 1.7 GHz.  With
 // group scales the expansion is 16 vector instructions a fragment and not 4,
-// and takes 1250 us (1.18 PFLOP/s).  A 128 x 128 tile by eight waves of
+// and takes 1265 us (1.17 PFLOP/s), with an FP32 result 2252.  A 128 x 128 tile by eight waves of
 // 64 x 32 is bound by LDS reads (2048 cubed: 21.2 us against 19.9).
 
 constexpr int kStep = 64;   // rows per pipeline step
@@ -131,6 +136,7 @@ __device__ __forceinline__ uint8_t* code_stage() { return lds_array<T::kB + 256 
 template <class T, int G, int kSt, bool kLast>
 __device__ __forceinline__ void load_one(const WgradParams& p, int step, int step1, int wave, int lane, int q,
                                          const uint32_t (&off)[T::kLA + T::kLB + Stage<T, G>::kLS]) {
+#if __HIP_DEVICE_COMPILE__   // (the host has no type for a buffer's description)
   const int64_t m0 = (int64_t)(kLast && step >= step1 ? step1 - 1 : step) * kStep;
   const int last = (int)(p.M - m0 < kStep ? p.M - m0 : kStep) - 1;
   auto at = [&](int row, uint32_t stride) __attribute__((always_inline)) {
@@ -157,6 +163,7 @@ __device__ __forceinline__ void load_one(const WgradParams& p, int step, int ste
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, code_stage<T, G, kSt>() + T::kB + 256 * (Stage<T, G>::kLS * wave + i), 4,
                                              at(lane, 4u * (uint32_t)p.groups), 0, 0, 0);
   }
+#endif
 }
 
 // xcd_contiguous for 32-bit indexes.
@@ -166,8 +173,8 @@ __device__ __forceinline__ uint32_t xcd_contiguous32(uint32_t b, uint32_t nb) {
 }
 
 // Computes the tile of dW at (n0, k0), over the steps of `part`.  G = 0: one
-// scale.
-template <class T, int G>
+// scale.  kFine: X in two BF16 parts.
+template <class T, int G, bool kFine>
 __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n0, const int64_t k0, const uint32_t part) {
   using S = Stage<T, G>;
   constexpr int kBN = T::kBN, kBK = T::kBK, kWK = T::kWK, kJ = T::kJ, kI = T::kI;
@@ -231,6 +238,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n
   v2i xw[kI];                   // codes of the substep being read
   float4 slo[kI], shi[kI];      // and their scales
   u32x4v x[2][kI];
+  u32x4v rest[kFine ? 2 : 1][kI];   // what BF16 left of x
   int dy_off[kJ], x_off[kI], s_off[kI];
 #pragma unroll
   for (int j = 0; j < kJ; ++j) {
@@ -269,14 +277,18 @@ __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n
       const int g = G >= 32 * kI ? 0 : i;
       const auto v = q & 1 ? __builtin_amdgcn_cvt_pk_f32_fp8(xw[i][q / 2], true) : __builtin_amdgcn_cvt_pk_f32_fp8(xw[i][q / 2], false);
       const float4 sc = q < 2 ? slo[g] : shi[g];
-      x[f][i][q] = q & 1 ? bf16_pack2(v[0] * sc.z, v[1] * sc.w) : bf16_pack2(v[0] * sc.x, v[1] * sc.y);
+      const float v0 = v[0] * (q & 1 ? sc.z : sc.x), v1 = v[1] * (q & 1 ? sc.w : sc.y);
+      const uint32_t w = bf16_pack2(v0, v1);
+      x[f][i][q] = w;
+      if constexpr (kFine) rest[f][i][q] = bf16_pack2(v0 - bf16_lo(w), v1 - bf16_hi(w));
     }
   };
   auto mma = [&](int f, int n) __attribute__((always_inline)) {
     const int i = n / kJ, j = n % kJ;
-    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-        __builtin_bit_cast(v8bf, x[f][i]), __builtin_bit_cast(v8bf, __builtin_shufflevector(dlo[f][j], dhi[f][j], 0, 1, 2, 3, 4, 5, 6, 7)),
-        acc[i][j], 0, 0, 0);
+    const v8bf d = __builtin_bit_cast(v8bf, __builtin_shufflevector(dlo[f][j], dhi[f][j], 0, 1, 2, 3, 4, 5, 6, 7));
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, x[f][i]), d, acc[i][j], 0, 0, 0);
+    if constexpr (kFine)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, rest[f][i]), d, acc[i][j], 0, 0, 0);
   };
   // The MFMAs of fragment set f, with substep s of a stage read into the other
   // set between them: the codes first, expanded dword by dword behind the
@@ -469,28 +481,28 @@ using Small = Tile<2, 2, 2, 2>;             // 128 x 128, four waves of 64 x 64
 // the remaining ones: a last round that would be at most half full takes half
 // a round's time (1376 tiles on 256 compute units: 1067 us against 1105; 320
 // tiles: 146 against 176).
-template <int G>
+template <int G, bool kFine>
 __global__ __launch_bounds__(Large::kThreads) void wgrad_large_kernel(const WgradParams p) {
   int64_t n0, k0;
   const uint32_t b = blockIdx.x, whole = (uint32_t)p.whole;
   if (b < whole) {
     tile_at<Large>(p, xcd_contiguous32(b, whole), n0, k0);
-    wgrad_tile<Large, G>(p, n0, k0, 0);
+    wgrad_tile<Large, G, kFine>(p, n0, k0, 0);
   } else {
     const uint32_t order = xcd_contiguous32(b - whole, gridDim.x - whole);
     tile_at<Large>(p, whole + (order >> 1), n0, k0);
     n0 += Half::kBN * (order & 1);
-    if (n0 < p.N) wgrad_tile<Half, G>(p, n0, k0, 0);
+    if (n0 < p.N) wgrad_tile<Half, G, kFine>(p, n0, k0, 0);
   }
 }
 
-template <int G>
+template <int G, bool kFine>
 __global__ __launch_bounds__(Small::kThreads) void wgrad_small_kernel(const WgradParams p) {
   int64_t n0, k0;
   const uint32_t tiles = (uint32_t)p.n_tiles * (uint32_t)p.k_tiles;
   const uint32_t order = xcd_contiguous32(blockIdx.x, gridDim.x), part = order / tiles;
   tile_at<Small>(p, order - part * tiles, n0, k0);
-  wgrad_tile<Small, G>(p, n0, k0, part);
+  wgrad_tile<Small, G, kFine>(p, n0, k0, part);
 }
 
 // Adds the partial sums of the splits in order, scales and stores.
@@ -526,18 +538,20 @@ __global__ __launch_bounds__(256) void wgrad_zero_kernel(void* dw, int64_t bytes
     *reinterpret_cast<uint4*>((uint8_t*)dw + at) = make_uint4(0, 0, 0, 0);
 }
 
-template <int G>
-const void* large_fn() { return reinterpret_cast<const void*>(&wgrad_large_kernel<G>); }
-template <int G>
-const void* small_fn() { return reinterpret_cast<const void*>(&wgrad_small_kernel<G>); }
+template <int G, bool kFine>
+const void* wgrad_fn(bool large) {
+  return large ? reinterpret_cast<const void*>(&wgrad_large_kernel<G, kFine>)
+               : reinterpret_cast<const void*>(&wgrad_small_kernel<G, kFine>);
+}
 
-const void* wgrad_kernel_for(bool large, int32_t g) {
+// g: the group size, 0 for one scale.
+const void* wgrad_kernel_for(bool large, int32_t g, bool fine) {
   switch (g) {
-    case 0: return large ? large_fn<0>() : small_fn<0>();
-    case 16: return large ? large_fn<16>() : small_fn<16>();
-    case 32: return large ? large_fn<32>() : small_fn<32>();
-    case 64: return large ? large_fn<64>() : small_fn<64>();
-    default: return large ? large_fn<128>() : small_fn<128>();
+    case 0: return wgrad_fn<0, false>(large);
+    case 16: return fine ? wgrad_fn<16, true>(large) : wgrad_fn<16, false>(large);
+    case 32: return fine ? wgrad_fn<32, true>(large) : wgrad_fn<32, false>(large);
+    case 64: return fine ? wgrad_fn<64, true>(large) : wgrad_fn<64, false>(large);
+    default: return fine ? wgrad_fn<128, true>(large) : wgrad_fn<128, false>(large);
   }
 }
 
@@ -648,7 +662,7 @@ coat_status_t coat_fp8_weight_grad(const coat_weight_grad_args_t* a, hipStream_t
   const int64_t tiles = (int64_t)pl.n_tiles * pl.k_tiles, rest = pl.large ? tiles % kUnits : 0;
   const int64_t halves = 2 * rest <= kUnits ? rest : 0;
   p.whole = (int32_t)(tiles - halves);
-  e = hipLaunchKernel(wgrad_kernel_for(pl.large, a->x_scales ? a->group_size : 0),
+  e = hipLaunchKernel(wgrad_kernel_for(pl.large, a->x_scales ? a->group_size : 0, out != kBF16),
                       dim3((unsigned)((tiles + halves) * pl.splits)),
                       dim3(pl.large ? Large::kThreads : Small::kThreads), args, 0, stream);
   if (e == hipSuccess && pl.splits > 1) {

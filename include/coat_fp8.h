@@ -448,8 +448,9 @@ int64_t coat_fp8_qk_norm_rope_bwd_workspace(int64_t tokens, int64_t heads,
  *   dW[n][k] = sum over rows m of dy[m][n] * X[m][k],
  * X = code * S per group (x_scales) or code * x_scale (x_scales NULL),
  * accumulated in FP32 on the matrix cores.  Under one scale the codes' values
- * are exact in BF16 and x_scale multiplies the FP32 sum; code * S is rounded
- * to BF16 (by at most 2^-8 of it) before it is multiplied.
+ * are exact in BF16 and x_scale multiplies the FP32 sum.  With group scales
+ * code * S is rounded to BF16 for dw_bf16 (by at most 2^-8 of it); for dw_f32
+ * it goes in as two BF16 values, which hold it to 2^-16, in twice the products.
  * N and K multiples of 16, K of group_size with x_scales; both at most 2^24.
  * Exactly one of dw_bf16 and dw_f32 is given; accumulate needs dw_f32.
  * M == 0 gives a zero gradient.  The workspace may be NULL when the workspace
