@@ -166,6 +166,14 @@ __device__ __forceinline__ void load_one(const WgradParams& p, int step, int ste
 #endif
 }
 
+// Between a wave's writes to its part of the LDS and its reads of what other
+// lanes wrote there (and back): nothing for the hardware, which keeps a wave's
+// accesses in order, but the compiler may otherwise exchange them.
+__device__ __forceinline__ void wave_meet() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // xcd_contiguous for 32-bit indexes.
 __device__ __forceinline__ uint32_t xcd_contiguous32(uint32_t b, uint32_t nb) {
   const uint32_t q = nb / 8, r = nb % 8, xcd = b % 8, local = b / 8;
@@ -408,6 +416,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n
   auto chunk_at = [&](int row, int c) __attribute__((always_inline)) { return 128 * row + 16 * (c ^ ((row >> 1) & 7)); };
   // each 16-byte chunk of the staged rows: fn(row, chunk of the row, its bytes)
   auto rows_out = [&](auto fn) __attribute__((always_inline)) {
+    wave_meet();
 #pragma unroll
     for (int r = 0; r < kRows / 8; ++r) {
       const int row = 8 * r + (lane >> 3), c = lane & 7;
@@ -437,6 +446,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n
     float* dw = (float*)p.dw + (p.out == kPartial ? part * N * K : 0);
 #pragma unroll
     for (int i = 0; i < kI; ++i) {
+      if (i > 0) wave_meet();   // the rows of the last pass are read
 #pragma unroll
       for (int j = 0; j < kJ; ++j)
 #pragma unroll
