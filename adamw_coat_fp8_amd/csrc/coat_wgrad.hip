@@ -398,9 +398,10 @@ __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n
   // LDS of its own, in rows of 128 bytes (64 values in BF16, in one pass; 32 in
   // FP32, a pass for each i), and stores whole 128-byte lines.  (Stores of the
   // runs as they are took 3.7 us of a 7.8 us call of one step.)  The 16-byte
-  // chunks are XORed with row / 2 % 8, and on rows with bit 4 set the 8-byte
-  // halves of a chunk swapped: writes of 32 rows and reads of rows both meet
-  // all banks evenly.
+  // chunks are XORed with row % 8, and on rows with bit 3 set the 8-byte halves
+  // of a chunk swapped: 8-byte writes go 16 rows at a time, 16-byte writes and
+  // reads 8 chunks, each time all of 128 different bytes of the banks (counted:
+  // no conflicts; XORed with row / 2 % 8, two rows met, 4 cycles a write).
   __syncthreads();   // every wave is done with the stages
   constexpr int kRows = 32 * kJ, kBytes = 128 * kRows, kPer = T::kLdsA / kBytes;
   uint8_t* own = wave < kPer       ? dy_stage<T, 0>() + kBytes * wave
@@ -413,7 +414,7 @@ __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n
   }
   const float scale = p.out == kPartial ? 1.0f : p.scale;
   const int64_t wave_n = n0 + kRows * wn, wave_k = k0 + 32 * kI * wk;
-  auto chunk_at = [&](int row, int c) __attribute__((always_inline)) { return 128 * row + 16 * (c ^ ((row >> 1) & 7)); };
+  auto chunk_at = [&](int row, int c) __attribute__((always_inline)) { return 128 * row + 16 * (c ^ (row & 7)); };
   // each 16-byte chunk of the staged rows: fn(row, chunk of the row, its bytes)
   auto rows_out = [&](auto fn) __attribute__((always_inline)) {
     wave_meet();
@@ -433,12 +434,12 @@ __device__ __forceinline__ void wgrad_tile(const WgradParams& p, const int64_t n
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int row = 32 * j + (lane & 31);
-          *reinterpret_cast<uint2*>(own + chunk_at(row, 4 * i + q) + 8 * (half ^ ((row >> 4) & 1))) =
+          *reinterpret_cast<uint2*>(own + chunk_at(row, 4 * i + q) + 8 * (half ^ ((row >> 3) & 1))) =
               make_uint2(bf16_pack2(acc[i][j][4 * q] * scale, acc[i][j][4 * q + 1] * scale),
                          bf16_pack2(acc[i][j][4 * q + 2] * scale, acc[i][j][4 * q + 3] * scale));
         }
     rows_out([&](int row, int c, uint4 v) __attribute__((always_inline)) {
-      if ((row >> 4) & 1) v = make_uint4(v.z, v.w, v.x, v.y);
+      if ((row >> 3) & 1) v = make_uint4(v.z, v.w, v.x, v.y);
       const int64_t n = wave_n + row, k = wave_k + 8 * c;
       if (n < N && k < K) store_stream16((uint16_t*)p.dw + n * K + k, v);
     });
