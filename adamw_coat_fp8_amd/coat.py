@@ -236,12 +236,17 @@ def _on_device(**tensors):
                              f"is cuda:{dev}")
 
 
+# The current device, and torch's current stream on a device as a raw handle.
+# torch's own queries cost about 0.1 us per call, its public ones 0.3 and 3 us,
+# as long as a small kernel; those are taken where a torch lacks the others.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # torch's current stream on the current device, as a raw handle: this
-        # query costs about 0.1 us per call, torch.cuda.current_stream() about
-        # 3 us, as long as a small kernel
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         if stream.device_index != torch.cuda.current_device():
             raise ValueError(f"stream is on cuda:{stream.device_index}, but the current device "
@@ -473,7 +478,7 @@ def _addresses(buffers, heads=()):
                 continue
             d = t.get_device()
             if d != dev:
-                if dev is not None or d < 0 or d != torch.cuda.current_device():
+                if dev is not None or d < 0 or d != _current_device():
                     return _refuse(buffers, heads)
                 dev = d
             if t.dtype not in dtypes or not t.is_contiguous() or t.numel() < n:
@@ -485,7 +490,7 @@ def _addresses(buffers, heads=()):
             out.append(t.data_ptr())
     except AttributeError:   # not a tensor
         return _refuse(buffers, heads)
-    return out, torch._C._cuda_getCurrentRawStream(dev)
+    return out, _raw_stream(dev)
 
 
 def _refuse(buffers, heads):

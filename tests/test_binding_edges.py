@@ -1,4 +1,7 @@
 """Calls that the binding has to refuse, or must not trip over, on the CPU."""
+import importlib.util
+import sys
+
 import pytest
 import torch
 
@@ -110,14 +113,22 @@ def test_stream_of_another_device(monkeypatch, coat):
         coat._stream(Stream(0))
 
 
-def test_current_device_by_its_public_name(monkeypatch, coat):
-    """The seven activation calls' check of the device, without torch's
-    private query."""
+def test_without_torchs_private_queries(monkeypatch, coat):
+    """A torch that lacks them is served by its public ones."""
     class Tensor:
         dtype = torch.bfloat16
         get_device, is_contiguous, numel, data_ptr = (lambda s: 1), (lambda s: True), (lambda s: 8), (lambda s: 0x10000)
 
+    class Stream:
+        cuda_stream = 71
+
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
-    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 70 + d, raising=False)
-    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
-    assert coat._addresses(((Tensor(), "x", coat.BF16, 8), (None, "y", coat.F32, 8))) == ([0x10000, 0], 71)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream() if device == 1 else None)
+    spec = importlib.util.spec_from_file_location("coat_on_another_torch", coat.__file__)
+    other = importlib.util.module_from_spec(spec)
+    monkeypatch.setitem(sys.modules, spec.name, other)
+    spec.loader.exec_module(other)
+    assert other._addresses(((Tensor(), "x", other.BF16, 8), (None, "y", other.F32, 8))) == ([0x10000, 0], 71)
+    assert other._stream(None) == 71
