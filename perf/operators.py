@@ -396,6 +396,8 @@ def _package():
 
 def _own_norm(s):
     fp8, ckpt = s["out"] == "fp8", s["ckpt"]
+    if fp8:
+        s["amax"].zero_()   # the call raises what it holds: a new maximum starts at 0
     _package().rms_norm(s["x"], s["weight"], EPS, residual=s["residual"], residual_out=s["sum"],
                         y=None if fp8 else s["y"], y_codes=s["y"] if fp8 else None, y_scale=s["y_scale"],
                         y_amax=s["amax"] if fp8 else None, codes=s["codes"] if ckpt else None,
@@ -417,6 +419,8 @@ def _own_norm_bwd(s):
 
 def _own_act(s):
     fp8 = s["out"] == "fp8"
+    if fp8:
+        s["amax"].zero_()
     _package().swiglu(s["codes"], s["scales"], gate_up=s["gate_up"], h=None if fp8 else s["h"],
                       h_codes=s["h"] if fp8 else None, h_scale=s["h_scale"], h_amax=s["amax"] if fp8 else None,
                       group_size=s["G"])
