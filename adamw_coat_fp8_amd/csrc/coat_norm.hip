@@ -95,9 +95,11 @@ __device__ __forceinline__ float block_sum(float v, int slot) {
   return v;
 }
 
-template <int kMost, int kC>
-__global__ __launch_bounds__(kMost) void rms_norm_kernel(const NormParams p) {
-  const int t = threadIdx.x, threads = blockDim.x;
+// kRows: rows that a block takes at once, one wave each (they need no barrier).
+template <int kMost, int kC, int kRows = 1>
+__global__ __launch_bounds__(kMost * kRows) void rms_norm_kernel(const NormParams p) {
+  static_assert(kRows == 1 || kMost == 64, "a row of one wave");
+  const int t = kRows > 1 ? threadIdx.x & 63 : threadIdx.x, threads = kRows > 1 ? 64 : blockDim.x;
   const int cols = p.cols, lanes = 1 << (p.group_shift - 3);
   bool ok[kC];
   int col[kC];
@@ -127,15 +129,17 @@ __global__ __launch_bounds__(kMost) void rms_norm_kernel(const NormParams p) {
     for (int e = 0; e < 8; ++e) f[e] += r[e];
     return pack8(f);
   };
+  const int64_t stride = (int64_t)gridDim.x * kRows;
   int64_t row = blockIdx.x;
-  if (kKeep) {
+  if constexpr (kRows > 1) row = row * kRows + __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  if (kKeep && (kRows == 1 || row < p.rows)) {
 #pragma unroll
     for (int i = 0; i < kC; ++i) load(row, i), load_weight(i);
   }
 
   float top = 0.0f;
   int slot = 0;
-  for (; row < p.rows; row += gridDim.x, slot ^= 1) {
+  for (; row < p.rows; row += stride, slot ^= 1) {
     uint4 raw[kC];
     float ss = 0.0f;
 #pragma unroll
@@ -147,9 +151,9 @@ __global__ __launch_bounds__(kMost) void rms_norm_kernel(const NormParams p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
     }
-    if (kKeep && row + gridDim.x < p.rows) {
+    if (kKeep && row + stride < p.rows) {
 #pragma unroll
-      for (int i = 0; i < kC; ++i) load(row + gridDim.x, i);
+      for (int i = 0; i < kC; ++i) load(row + stride, i);
     }
     const float rstd = inv_sqrt(__builtin_fmaf(block_sum<kMost>(ss, slot), p.inv_cols, p.eps));
     if (p.rstd && t == 0) p.rstd[row] = rstd;
@@ -471,6 +475,12 @@ NormShape norm_shape(int64_t cols, bool backward) {
 
 enum NormKernel { kForward, kBackward, kBackwardFew };
 
+// Rows of one wave with a maximum to raise: four to a block where there are
+// many, a quarter of the atomics (16384 x 512: 10.0 us against 13.4, 300 x 256: 4.0
+// against 5.6; up to 128 blocks, or without a maximum, one to a block is 0.2
+// to 0.4 us better).
+constexpr int kWaveRows = 4;
+
 const void* norm_kernel_for(NormShape s, NormKernel which) {
 #define COAT_NORM(T, C)                                                                       \
   if (s.most == T && s.chunks == C)                                                           \
@@ -564,7 +574,11 @@ coat_status_t coat_fp8_rms_norm(const coat_rms_norm_args_t* a, hipStream_t strea
   // 28 waves with one chunk a thread, 16 with more
   const int64_t blocks = balanced(a->rows, (int64_t)cus * ((s.chunks == 1 ? 28 : 16) * 64 / s.threads));
   void* args[] = {&p};
-  e = hipLaunchKernel(norm_kernel_for(s, kForward), dim3((unsigned)blocks), dim3(s.threads), args, 0, stream);
+  if (s.most == 64 && a->y_amax && blocks > 128)
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&rms_norm_kernel<64, 1, kWaveRows>),
+                        dim3((unsigned)((blocks + kWaveRows - 1) / kWaveRows)), dim3(64 * kWaveRows), args, 0, stream);
+  else
+    e = hipLaunchKernel(norm_kernel_for(s, kForward), dim3((unsigned)blocks), dim3(s.threads), args, 0, stream);
   return e == hipSuccess ? COAT_OK : hip_fail(e);
 }
 
