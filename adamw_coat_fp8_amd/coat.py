@@ -523,10 +523,11 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float, *, y: Optional[t
              residual_out: Optional[torch.Tensor] = None, codes: Optional[torch.Tensor] = None,
              scales: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
              group_size: int = 128, stream=None):
-    """RMS norm of h = x (+ residual, written to residual_out, which may be residual) into y (BF16)
-    and/or y_codes (E4M3 under the one scale y_scale; y_amax is raised to the
-    largest |y|).  codes and scales, if given, receive h's checkpoint and rstd
-    the rows' reciprocal root mean squares, for rms_norm_bwd."""
+    """RMS norm of h = x (+ residual, written to residual_out, which may be
+    residual) into y (BF16) and/or y_codes (E4M3 under the one scale y_scale;
+    y_amax is raised to the largest |y|).  codes and scales, if given, receive
+    h's checkpoint and rstd the rows' reciprocal root mean squares, for
+    rms_norm_bwd."""
     rows, cols = _shape2(x, "x")
     n = rows * cols
     p, current = _addresses((
@@ -578,8 +579,9 @@ def rms_norm_bwd(dy: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, rs
                  d_residual: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                  accumulate: bool = False, group_size: int = 128, stream=None):
     """Gradient of rms_norm from its checkpoint: dx (BF16, d_residual added if
-    given; not dy itself, which is read again after it is written) and, if given, dw (FP32, written or accumulated; needs
-    rms_norm_bwd_workspace(rows, cols) bytes of workspace)."""
+    given; not dy itself, which other blocks still read) and, if given, dw
+    (FP32, written or accumulated; needs rms_norm_bwd_workspace(rows, cols)
+    bytes of workspace)."""
     rows, cols = _shape2(dy, "dy")
     n = rows * cols
     ws_bytes = _workspace(workspace, rms_norm_bwd_workspace(rows, cols) if dw is not None else 0)

@@ -35,8 +35,11 @@ namespace {
 // checkpoint group lies on G/8 neighbouring lanes of one 16-lane DPP row.
 //
 // Bound by HBM: 8192 x 4096 with residual, E4M3 output and checkpoint (8.03
-// bytes a value) takes 48.5 us, 5.56 TB/s; vector instructions issue in 38% of
-// the cycles.  A grid of one block a row, without the loads ahead, took 51.5.
+// bytes a value) takes 48.5 to 49.0 us, 5.5 TB/s, raising a maximum 0.7 more;
+// vector instructions issue in 39% of the cycles.  A grid of one block a row,
+// without the loads ahead, took 51.5.  4096 x 8192 5.7 TB/s, 2048 x 16384 5.5;
+// past 16384 columns, where the chunks of a row spill from the registers (108
+// bytes a lane), 3 TB/s (1000 x 32768: 85 us).
 
 constexpr int64_t kMaxCols = 32768;
 
@@ -206,10 +209,12 @@ __global__ __launch_bounds__(kMost * kRows) void rms_norm_kernel(const NormParam
 // end.  A second launch adds those up in a fixed order, so the result does
 // not depend on timing.
 //
-// 8192 x 4096 with d_residual: 41.4 us (5.7 TB/s) and 4.1 for the second
-// launch, most of it latency.  Few rows a block cost more: 4097 x 5120 (17
-// rows a block) 23.5 + 4.0 us, 4.6 TB/s.  Two rows at a time, for more loads in
-// flight, needs twice the registers and took 63 us where one takes 45.
+// 8192 x 4096 with d_residual: 42.5 us (5.5 TB/s) and 4.5 for the second
+// launch, most of it latency.  One row is in flight a unit, so shorter ones
+// without d_residual reach less: 4097 x 5120 24.0 + 4.6 us, 4.5 TB/s.  Two rows
+// at a time need twice the registers and took 62.8 us where one takes 45.8.
+// Past 16384 columns the chunks of a row spill (368 bytes a lane), and each
+// phase waits for its loads: 1000 x 32768 with d_residual 197 us, 1.2 TB/s.
 
 struct NormBwdParams {
   const uint16_t* dy;
@@ -353,10 +358,13 @@ __global__ __launch_bounds__(kMost) void rms_norm_bwd_kernel(const NormBwdParams
 // Few rows: one launch and no partial sums.  Blocks 0 .. rows - 1 take a row
 // each; every block behind them takes the weight gradient of 128 columns: 16
 // threads of eight columns, blockDim / 16 slices of the rows, which join in
-// the LDS in a fixed order.  The rows are read a second time, by blocks that
-// may run before or after the row's own, so dx must not be dy.  A call this small is as long as its launches: 1 to 512 rows of 4096 take 7.7
-// us, with two launches 10.7.  At more than about 32 rows a slice the second
-// reading shows (256 x 512, 64 rows a slice: 13.2 us against 11.0).
+// the LDS in a fixed order.  The rows are read a second time, on other XCDs
+// than the first for the most part, so from behind the L2s; and by blocks that
+// may run before or after the row's own, so dx must not be dy.  A call this
+// small is as long as its launches: 1 to 512 rows of 4096 take 7.7 us, with two
+// launches 10.7.  At more than about 32 rows a slice the second reading shows
+// (256 x 512, 64 rows a slice: 13.2 us against 11.0).  (The workspace is asked
+// for all the same: its size is one function of the rows and columns.)
 constexpr int kFewCols = 128;
 constexpr int64_t kFewRows = 512;
 
@@ -453,11 +461,15 @@ int64_t balanced(int64_t rows, int64_t most) {
 }
 
 // The instance for a row, and its threads: whole waves, as few as hold the
-// row.  One chunk a thread up to 8192 columns: fewer registers, so that two
-// blocks of independent rows share a CU (backward, 4097 x 5120: 34 us with two
-// chunks, 28 with one); only the forward pass of 2049 to 4096 columns is
-// better with two chunks and four waves (8192 x 4096 with residual and
-// checkpoint: 49.2 us against 50.8; without them 24.2 against 23.5).
+// row.  One chunk a thread up to 8192 columns: as many bytes in flight from
+// twice the waves, which hide more of each other (backward, 4097 x 5120, one
+// block a unit: 34 us with two chunks and five waves, 28 with one and ten).
+// Only the forward pass of 2049 to 4096 columns is better with two chunks, in
+// half the waves, of which a CU then holds more rows: 8192 rows with residual,
+// checkpoint and E4M3 output 28.3 us against 32.9 at 2176 columns, 32.2 : 36.1
+// at 2560, 35.4 : 39.4 at 2816, 39.5 : 44.7 at 3328, 42.0 : 47.1 at 3584,
+// 48.3 : 49.4 at 4096; 1024 rows 5.5 : 5.2, 5.7 : 5.3, 5.8 : 6.9, 6.1 : 7.4,
+// 6.2 : 8.0, 7.2 : 7.4; one row 3.1 : 2.9 throughout.
 struct NormShape {
   int most, chunks, threads;
 };

@@ -36,8 +36,8 @@ namespace {
 // A token whose position is outside the table is padding: everything written
 // for it is zero.
 //
-// 8192 tokens, 64 heads of 128 values, with checkpoint: 59.6 us, 5.74 TB/s, at
-// 65% vector issue (67 us before the weights were folded in).
+// 8192 tokens, 64 heads of 128 values, with checkpoint: 59.9 us, 5.71 TB/s, at
+// 69% vector issue (67 us before the weights were folded in).
 
 struct QkParams {
   const uint16_t* q;        // forward: heads; backward: their output gradients
@@ -55,7 +55,7 @@ struct QkParams {
   float* scales;
   float* rstd;
   float* partials;          // backward: gridDim.x rows of 2 D, or NULL
-  int64_t tokens, table_rows;
+  int64_t table_rows;
   int32_t units;            // (token, slab) pairs, < 2^31
   int32_t slabs, q_slabs;   // slabs of heads of a token, and those of queries
   int32_t q_heads, k_heads;
@@ -444,7 +444,6 @@ coat_status_t check_qk(const coat_qk_shape_t& s) {
 
 void fill(QkParams& p, const coat_qk_shape_t& s, const QkSplit& split) {
   memset(&p, 0, sizeof(p));
-  p.tokens = s.tokens;
   p.table_rows = s.table_rows;
   p.units = (int32_t)split.units;
   p.slabs = split.slabs;

@@ -34,8 +34,8 @@ namespace {
 // of 1.7e-3 (norms, random scales): as much as rounding the result to BF16
 // does, 2.3e-3 together, and all the error of an FP32 result.  So an FP32
 // result takes code * S in two BF16 parts (the second what the first left) and
-// two MFMAs: 2.6e-6, at 1.78 times the time (8192 x 4096 x 4096, G = 128: 411 us
-// against 230); a BF16 result takes one.  Sums are FP32 in the matrix cores.
+// two MFMAs: 2.6e-6, at 1.78 times the time (8192 x 4096 x 4096, G = 128: 403 us
+// against 226); a BF16 result takes one.  Sums are FP32 in the matrix cores.
 //
 // A block computes a kBN x kBK tile of dW; kWN x kWK waves own kJ x kI tiles
 // of 32 x 32.  64 rows a step, three LDS stages.  A step is four substeps of
@@ -47,11 +47,13 @@ namespace {
 // load has two steps and more to arrive.
 //
 // Bound by the matrix cores and the power they may draw: 8192 x 22016 x 4096
-// under one scale takes 1028 us (1.437 PFLOP/s; a library product of the same
-// sizes in BF16 takes 1163 us with both operands contraction-minor and 1410 as
-// they lie here), the MFMAs busy 81% of the cycles at about 1.7 GHz.  With
-// group scales the expansion is 16 vector instructions a fragment and not 4,
-// and takes 1265 us (1.17 PFLOP/s), with an FP32 result 2252.  A 128 x 128 tile by eight waves of
+// under one scale takes 1021 us (1.446 PFLOP/s; timed in turn with it, a
+// library product of the same sizes in BF16 takes 1048 us with both operands
+// contraction-minor and 1402 as they lie here; 1015 to 1078 us from one run and
+// card to the next, up to 1257 in single calls after a pause), the MFMAs busy
+// 81% of the cycles at about 1.7 GHz.  With group scales the expansion is 16
+// vector instructions a fragment and not 4, and takes 1252 us (1.18 PFLOP/s),
+// with an FP32 result 2185.  A 128 x 128 tile by eight waves of
 // 64 x 32 is bound by LDS reads (2048 cubed: 21.2 us against 19.9).
 
 constexpr int kStep = 64;   // rows per pipeline step

@@ -244,7 +244,9 @@ coat_status_t coat_fp8_gemm_bf16(const uint8_t* a, const uint8_t* b,
  *   - *_amax, if given, is raised to the largest magnitude (before the scale)
  *     of the FP32 values that were rounded to codes; it must hold a
  *     non-negative value before (0 to start a new maximum).  A NaN is not
- *     counted (its code is NaN).
+ *     counted (its code is NaN).  The scales y_scale and h_scale are values of
+ *     the call: a captured graph keeps those it was captured with, and a scale
+ *     made from a maximum takes a copy to the host.
  *   - Gradients of weights are FP32 and sums over rows in a fixed order.
  *     accumulate != 0 adds them to what the array holds, else they overwrite
  *     it.  A weight gradient pointer may be NULL (a frozen weight).
@@ -253,15 +255,16 @@ coat_status_t coat_fp8_gemm_bf16(const uint8_t* a, const uint8_t* b,
  *     read before it is written nor of use afterwards.  Calls, or replays of
  *     captured graphs, that share one must not overlap.
  *   - A NaN or infinity reaches no output outside its row (qk: its head,
- *     swiglu: its value) except the weight gradients; the scale of its group
- *     in a checkpoint is not finite.
+ *     swiglu: its value) except the weight gradients, and in a checkpoint its
+ *     group, whose codes are NaN and whose scale is not finite.
  */
 
 /*
  * RMS norm of a residual stream with a checkpoint of its input:
  *   h = bf16(x + residual), or x without a residual,
  *   rstd = (mean(h^2) + eps)^-1/2,  y = h * rstd * weight.
- * cols is a multiple of group_size, at most 32768; squares are summed in FP32.
+ * cols is a multiple of group_size, at most 32768; squares are summed in FP32
+ * (where that sum overflows rstd is 0).
  * Errors: NULL_POINTER (args, x, weight; neither y nor y_codes; residual
  * without residual_out or codes without scales, or the reverse),
  * INVALID_VALUE (sizes; eps not finite or below 2^-126; with y_codes, y_scale not
