@@ -40,6 +40,9 @@ EXPORTED_SYMBOLS = (
     "coat_fp8_swiglu", "coat_fp8_swiglu_bwd", "coat_fp8_qk_norm_rope",
     "coat_fp8_qk_norm_rope_bwd", "coat_fp8_qk_norm_rope_bwd_workspace",
     "coat_fp8_weight_grad", "coat_fp8_weight_grad_workspace",
+    "coat_fp8_embedding", "coat_fp8_embedding_bwd", "coat_fp8_embedding_bwd_workspace",
+    "coat_fp8_cross_entropy", "coat_fp8_cross_entropy_workspace",
+    "coat_fp8_cross_entropy_bwd", "coat_fp8_cross_entropy_bwd_workspace",
 )
 
 
@@ -133,6 +136,26 @@ class WeightGradArgs(ctypes.Structure):
                        "f32: x_scale, i32: group_size accumulate")
 
 
+class EmbeddingArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: table table_codes tokens out, i64: rows vocab cols, f32: table_scale scale")
+
+
+class EmbeddingBwdArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: dy tokens dw_bf16 dw_f32 workspace, i64: workspace_bytes rows vocab cols, "
+                       "f32: scale, i32: accumulate")
+
+
+class CrossEntropyArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: x x_codes weight weight_codes targets loss lse workspace, i64: workspace_bytes "
+                       "rows vocab cols, f32: x_scale weight_scale logit_scale z_loss")
+
+
+class CrossEntropyBwdArgs(ctypes.Structure):
+    _fields_ = _fields("ptr: d_loss x x_codes weight weight_codes targets lse dx dw_bf16 dw_f32 workspace, "
+                       "i64: workspace_bytes rows vocab cols, f32: x_scale weight_scale logit_scale z_loss, "
+                       "i32: accumulate")
+
+
 def _load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise ImportError(
@@ -157,7 +180,8 @@ def _load(path: str = LIB_PATH):
     lib.coat_fp8_gemm_group_quant.argtypes = [vp, vp, f32, f32, i64, i64, i64, i32, vp, vp, vp, vp]
     lib.coat_fp8_gemm_bf16.restype = ctypes.c_int
     lib.coat_fp8_gemm_bf16.argtypes = [vp, vp, f32, f32, i64, i64, i64, vp, vp]
-    for name in ("rms_norm", "rms_norm_bwd", "swiglu", "qk_norm_rope", "qk_norm_rope_bwd", "weight_grad"):
+    for name in ("rms_norm", "rms_norm_bwd", "swiglu", "qk_norm_rope", "qk_norm_rope_bwd", "weight_grad",
+                 "embedding", "embedding_bwd", "cross_entropy", "cross_entropy_bwd"):
         fn = getattr(lib, f"coat_fp8_{name}")
         fn.restype = ctypes.c_int
         fn.argtypes = [vp, vp]   # a structure by reference, or its packed bytes
@@ -169,6 +193,12 @@ def _load(path: str = LIB_PATH):
     lib.coat_fp8_qk_norm_rope_bwd_workspace.argtypes = [i64, i64, i64]
     lib.coat_fp8_weight_grad_workspace.restype = i64
     lib.coat_fp8_weight_grad_workspace.argtypes = [i64, i64, i64]
+    lib.coat_fp8_embedding_bwd_workspace.restype = i64
+    lib.coat_fp8_embedding_bwd_workspace.argtypes = [i64, i64, i64]
+    lib.coat_fp8_cross_entropy_workspace.restype = i64
+    lib.coat_fp8_cross_entropy_workspace.argtypes = [i64, i64, i64]
+    lib.coat_fp8_cross_entropy_bwd_workspace.restype = i64
+    lib.coat_fp8_cross_entropy_bwd_workspace.argtypes = [i64, i64, i64, i64, i32, i32]
     lib.coat_status_string.restype = ctypes.c_char_p
     lib.coat_status_string.argtypes = [ctypes.c_int]
     lib.coat_last_hip_error.restype = ctypes.c_char_p
@@ -771,3 +801,124 @@ def weight_grad(dy: torch.Tensor, codes: torch.Tensor, scales, dw: torch.Tensor,
 
 
 DW_DTYPES = BF16_DTYPES + F32_DTYPES
+
+
+# ----------------------------------------------------------- the vocabulary
+
+_pack_embedding, _pack_embedding_bwd = _packer(EmbeddingArgs), _packer(EmbeddingBwdArgs)
+_pack_cross_entropy, _pack_cross_entropy_bwd = _packer(CrossEntropyArgs), _packer(CrossEntropyBwdArgs)
+MATRIX_DTYPES = BF16_DTYPES + CODE_DTYPES
+
+
+def embedding(table: torch.Tensor, tokens: torch.Tensor, out: torch.Tensor, *, table_scale: float = 1.0,
+              scale: float = 1.0, stream=None):
+    """out[r] = scale * table[tokens[r]] (BF16) for a table (vocab x cols) in
+    BF16 or in E4M3 codes under the one scale table_scale.  tokens is int64;
+    one outside the table is padding and gets zeros."""
+    vocab, cols = _shape2(table, "table")
+    rows = tokens.numel() if isinstance(tokens, torch.Tensor) else 0
+    (pt, pi, po), current = _addresses((
+        (table, "table", MATRIX_DTYPES, 0), (tokens, "tokens", I64_DTYPES, 0), (out, "out", BF16, rows * cols)))
+    codes = table.dtype in CODE_DTYPES
+    _launch(lib.coat_fp8_embedding,
+            _pack_embedding(0 if codes else pt, pt if codes else 0, pi, po, rows, vocab, cols, table_scale, scale),
+            stream, current)
+
+
+def embedding_bwd_workspace(rows: int, vocab: int, cols: int) -> int:
+    """Bytes of workspace embedding_bwd needs."""
+    return _workspace_bytes(lib.coat_fp8_embedding_bwd_workspace, rows, vocab, cols)
+
+
+def embedding_bwd(dy: torch.Tensor, tokens: torch.Tensor, dw: torch.Tensor, *, scale: float = 1.0,
+                  workspace: Optional[torch.Tensor] = None, accumulate: bool = False, stream=None):
+    """Gradient of embedding: dw[v] = scale * the sum of dy's rows whose token
+    is v (dy rows x cols BF16; dw vocab x cols in BF16 or float32; a float32 dw
+    can be accumulated into).  Needs embedding_bwd_workspace bytes."""
+    rows, cols = _shape2(dy, "dy")
+    vocab, w_cols = _shape2(dw, "dw")
+    if w_cols != cols:
+        raise ValueError("dy and dw disagree on the columns")
+    ws_bytes = _workspace(workspace, embedding_bwd_workspace(rows, vocab, cols))
+    (py, pi, pw, ws), current = _addresses((
+        (dy, "dy", BF16, 0), (tokens, "tokens", I64_DTYPES, rows), (dw, "dw", DW_DTYPES, 0),
+        (workspace, "workspace", ANY, 0)))
+    f32 = dw.dtype == torch.float32
+    _launch(lib.coat_fp8_embedding_bwd,
+            _pack_embedding_bwd(py, pi, 0 if f32 else pw, pw if f32 else 0, ws, ws_bytes, rows, vocab, cols, scale,
+                                accumulate), stream, current)
+
+
+def _projection(x, weight):
+    """Sizes that both passes take from the hidden states and the weights, and
+    whether they are codes."""
+    rows, cols = _shape2(x, "x")
+    vocab, w_cols = _shape2(weight, "weight")
+    if w_cols != cols:
+        raise ValueError("x and weight disagree on the columns")
+    codes = x.dtype in CODE_DTYPES
+    if codes != (weight.dtype in CODE_DTYPES):
+        raise ValueError("x and weight are both BF16 or both E4M3 codes")
+    return rows, vocab, cols, codes
+
+
+def cross_entropy_workspace(rows: int, vocab: int, cols: int) -> int:
+    """Bytes of workspace cross_entropy needs."""
+    return _workspace_bytes(lib.coat_fp8_cross_entropy_workspace, rows, vocab, cols)
+
+
+def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, loss: torch.Tensor,
+                  lse: Optional[torch.Tensor] = None, *, x_scale: float = 1.0, weight_scale: float = 1.0,
+                  logit_scale: float = 1.0, z_loss: float = 0.0, workspace: Optional[torch.Tensor] = None,
+                  stream=None):
+    """Softmax cross entropy of the logits logit_scale * x @ weight.T, which
+    are never stored: loss[r] = lse - logits[r, targets[r]] + z_loss * lse^2
+    (float32), with lse their log-sum-exp, written for cross_entropy_bwd if
+    given.  x (rows x cols) and weight (vocab x cols) are both BF16, or both
+    E4M3 codes under x_scale and weight_scale.  A row whose target (int64) is
+    outside the vocabulary has no loss.  Needs cross_entropy_workspace bytes."""
+    rows, vocab, cols, codes = _projection(x, weight)
+    ws_bytes = _workspace(workspace, cross_entropy_workspace(rows, vocab, cols))
+    p, current = _addresses((
+        (x, "x", MATRIX_DTYPES, 0), (weight, "weight", MATRIX_DTYPES, 0), (targets, "targets", I64_DTYPES, rows),
+        (loss, "loss", F32, rows), (lse, "lse", F32, rows), (workspace, "workspace", ANY, 0)))
+    px, pw = p[0], p[1]
+    _launch(lib.coat_fp8_cross_entropy,
+            _pack_cross_entropy(*((0, px, 0, pw) if codes else (px, 0, pw, 0)), *p[2:], ws_bytes, rows, vocab, cols,
+                                x_scale, weight_scale, logit_scale, z_loss), stream, current)
+
+
+def cross_entropy_bwd_workspace(rows: int, vocab: int, cols: int, *, piece: int = 8192, codes: bool = False,
+                                f32: bool = False) -> int:
+    """Bytes of workspace cross_entropy_bwd needs to go through the vocabulary
+    in pieces of `piece` rows (codes: x and weight are E4M3; f32: dw is
+    float32).  Larger pieces are faster; the least it takes is piece=1's."""
+    if not 0 < piece < 1 << 63:
+        raise ValueError("piece must be positive")
+    return _workspace_bytes(lambda *sizes: lib.coat_fp8_cross_entropy_bwd_workspace(*sizes, piece, codes, f32),
+                            rows, vocab, cols)
+
+
+def cross_entropy_bwd(d_loss: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
+                      lse: torch.Tensor, dx: Optional[torch.Tensor], dw: Optional[torch.Tensor] = None, *,
+                      x_scale: float = 1.0, weight_scale: float = 1.0, logit_scale: float = 1.0,
+                      z_loss: float = 0.0, workspace: Optional[torch.Tensor] = None, accumulate: bool = False,
+                      stream=None):
+    """Gradients of cross_entropy for the gradient d_loss (float32) of each
+    row's loss: dx (BF16) and dw (vocab x cols in BF16, or float32, which can
+    be accumulated into); either may be None.  The logits are computed again,
+    as many vocabulary rows at a time as the workspace holds
+    (cross_entropy_bwd_workspace).  Their gradient is rounded to BF16, or for a
+    float32 dw held to 2^-16 in twice the products."""
+    rows, vocab, cols, codes = _projection(x, weight)
+    f32 = isinstance(dw, torch.Tensor) and dw.dtype == torch.float32
+    ws_bytes = _workspace(workspace, cross_entropy_bwd_workspace(rows, vocab, cols, piece=1, codes=codes, f32=f32))
+    p, current = _addresses((
+        (d_loss, "d_loss", F32, rows), (x, "x", MATRIX_DTYPES, 0), (weight, "weight", MATRIX_DTYPES, 0),
+        (targets, "targets", I64_DTYPES, rows), (lse, "lse", F32, rows), (dx, "dx", BF16, rows * cols),
+        (dw, "dw", DW_DTYPES, vocab * cols), (workspace, "workspace", ANY, 0)))
+    pd, px, pw, pt, pl, pdx, pdw, ws = p
+    _launch(lib.coat_fp8_cross_entropy_bwd,
+            _pack_cross_entropy_bwd(pd, *((0, px, 0, pw) if codes else (px, 0, pw, 0)), pt, pl, pdx,
+                                    0 if f32 else pdw, pdw if f32 else 0, ws, ws_bytes, rows, vocab, cols, x_scale,
+                                    weight_scale, logit_scale, z_loss, accumulate), stream, current)

@@ -1,0 +1,319 @@
+// coat_tile.h -- the matrix-core tile that the cross entropy's products share
+// (not part of the C ABI).
+//
+// A block computes a kBM x kBN tile of C[m][n] = sum over k of A(m, k) B(n, k).
+// Each operand lies in memory either with k fastest ("minor": rows of k, BF16
+// or E4M3) or with k slowest ("slow": k rows of m or n values, BF16).  A step
+// of the pipeline is 128 bytes of k for minor operands, 64 BF16 values or 128
+// codes, so a stage's panel of R rows takes 128 R bytes either way.  Panels go
+// from global memory straight into the LDS as they lie; the MFMA's operands
+// are read from minor panels as 16-byte chunks and from slow ones by the LDS's
+// transposing reads, which hand each lane eight consecutive k of its column.
+//
+// Two stages.  A step is two phases, one for each half of its k.  Phase 0 runs
+// on fragment set 0 while set 1 is read; then every wave waits for its reads
+// and for its loads into the other stage, and the block meets; phase 1 runs on
+// set 1 while set 0 of the next step is read from the other stage and the
+// loads of the step after next go into this one.
+//
+// The MFMA takes B as its first operand, so each 32 x 32 result is a tile of
+// C^T: register 4 q + s of acc[i][j] is C[row][col] with
+//   row = 32 kI wm + 32 i + lane % 32,  col = 32 kJ wn + 32 j + 8 q + 4 (lane / 32) + s,
+// runs of four columns a lane, and lanes l and l ^ 32 hold all the wave's
+// columns of a row.
+#ifndef COAT_TILE_H
+#define COAT_TILE_H
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "coat_elem.h"
+
+namespace coat {
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+// kWM x kWN waves of kI x kJ tiles of 32 x 32.  kArrA: bytes of an LDS array
+// of A, for tiles that share a kernel's arrays with a larger one.
+template <int kWM_, int kWN_, int kI_, int kJ_, int kArrA_ = 0>
+struct MmaTile {
+  static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kJ = kJ_;
+  static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
+  static constexpr int kBM = 32 * kWM * kI, kBN = 32 * kWN * kJ;
+  static constexpr int kA = 128 * kBM, kB = 128 * kBN;               // bytes of a stage's panels
+  static constexpr int kLA = kA / 1024 / kWaves, kLB = kB / 1024 / kWaves;   // loads of a wave
+  static constexpr int kArrA = kArrA_ ? kArrA_ : kA;
+};
+
+// The four LDS arrays of a kernel, A and B of the two stages.  Being distinct
+// objects, the compiler can tell the loads into one stage from the reads of
+// the other, and does not wait for loads in flight before it reads.
+template <int kBytes, int kWhich>
+__device__ __forceinline__ uint8_t* mma_array() {
+  __shared__ __attribute__((aligned(1024))) uint8_t bytes[kBytes];
+  return bytes;
+}
+
+template <class T, int kWhich>
+__device__ __forceinline__ uint8_t* mma_part() {
+  return mma_array<kWhich % 2 == 0 ? T::kArrA : T::kB, kWhich>();
+}
+
+// Minor panels: the 16-byte chunk of a 128-byte row is XORed with (row / 2) % 8,
+// slow ones: the 64-byte chunk of a row with k % 4; then no read meets a bank
+// twice (slow rows are multiples of 256 bytes).
+__device__ __forceinline__ int minor_swz(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int slow_chunk(int k, int c64) { return c64 ^ (k & 3); }
+
+// Byte offsets of a lane's loads into a minor panel of kBlock rows: row(r)
+// gives the byte offset of the panel's row r.
+template <int kLoads, class Row>
+__device__ __forceinline__ void minor_offsets(int wave, int lane, Row row, uint32_t (&off)[kLoads]) {
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int r = 8 * (kLoads * wave + i) + (lane >> 3);
+    off[i] = row(r) + 16u * (uint32_t)((lane & 7) ^ minor_swz(r));
+  }
+}
+
+// Those of a slow panel of kCols columns: k rows of `stride` bytes; columns
+// from `valid` on (a multiple of 8) re-load the last chunk, and rows from
+// `k_rows` on the last row.
+template <int kLoads, int kCols>
+__device__ __forceinline__ void slow_offsets(int wave, int lane, uint32_t stride, int64_t valid, int k_rows,
+                                             uint32_t (&off)[kLoads]) {
+#pragma unroll
+  for (int i = 0; i < kLoads; ++i) {
+    const int byte = 1024 * (kLoads * wave + i) + 16 * lane, k = byte / (2 * kCols), c16 = byte % (2 * kCols) / 16;
+    const int col = 8 * (4 * slow_chunk(k, c16 >> 2) + (c16 & 3));
+    off[i] = (uint32_t)(k < k_rows ? k : k_rows - 1) * stride + 2u * (uint32_t)(col < valid ? col : (int)valid - 8);
+  }
+}
+
+template <class T>
+__device__ __forceinline__ void mma_zero(v16f (&acc)[T::kI][T::kJ]) {
+#pragma unroll
+  for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+    for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+}
+
+// Adds the products of `steps` steps.  a(step), b(step): the panels' base
+// addresses (uniform); aoff, boff: the lane's offsets; blast: those of B in
+// steps for which b_last(step) holds.  The block has met at the end, and no
+// load is in flight.
+template <class T, bool kFP8, bool kASlow, bool kBSlow, class A, class B, class Last>
+__device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A a, const uint32_t (&aoff)[T::kLA], B b,
+                                        const uint32_t (&boff)[T::kLB], const uint32_t (&blast)[T::kLB], Last b_last) {
+#if __HIP_DEVICE_COMPILE__   // (the host has no type for a buffer's description)
+  constexpr int kI = T::kI, kJ = T::kJ, kLA = T::kLA, kLB = T::kLB, kL = kLA + kLB;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % T::kWM, wn = wave / T::kWM;
+  const int half = lane >> 5, l32 = lane & 31;
+  if (steps <= 0) {
+    __syncthreads();
+    return;
+  }
+  auto rsrc = [](const void* p) __attribute__((always_inline)) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)0xFFFFFFFF, 0x00020000);
+  };
+  struct From {
+    __amdgpu_buffer_rsrc_t a, b;
+    bool last;
+  };
+  // (past the last step the last one is fetched again, into a stage that is not read)
+  auto from = [&](int step) __attribute__((always_inline)) {
+    const int s = step < steps ? step : steps - 1;
+    return From{rsrc(a(s)), rsrc(b(s)), kBSlow ? (bool)b_last(s) : false};
+  };
+  auto load1 = [&](const From& f, auto S, int q) __attribute__((always_inline)) {
+    constexpr int st = decltype(S)::value;
+    if (q < kLA) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(f.a, mma_part<T, 2 * st>() + 1024 * (kLA * wave + q), 16, (int)aoff[q],
+                                               0, 0, 0);
+    } else {
+      const int i = q - kLA;
+      const uint32_t off = kBSlow && f.last ? blast[i] : boff[i];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(f.b, mma_part<T, 2 * st + 1>() + 1024 * (kLB * wave + i), 16, (int)off,
+                                               0, 0, 0);
+    }
+  };
+
+  // Fragments: [set][tile][chunk].  Phase kk of a step takes 32 bytes a lane
+  // and tile, the chunks 4 kk + 2 half + {0, 1} of a minor row: for BF16 the
+  // k 32 kk + 16 half + 8 {0, 1} + 0..7, which slow panels are read at too.
+  // (Offsets are single opaque values: the compiler follows an address back
+  // over a few additions only.)
+  uint4 fa[2][kI][2], fb[2][kJ][2];
+  int a_at[kI], b_at[kJ];
+  const int t16 = lane & 15, col16 = (lane >> 4) & 1;
+  auto slow_at = [&](int first, int cols) __attribute__((always_inline)) {
+    const int c = first + 16 * col16 + 4 * (t16 & 3), k = 16 * half + (t16 >> 2);
+    return k * 2 * cols + 64 * slow_chunk(k, c >> 5) + 2 * (c & 31);
+  };
+#pragma unroll
+  for (int i = 0; i < kI; ++i) {
+    const int first = 32 * (kI * wm + i);
+    a_at[i] = kASlow ? slow_at(first, T::kBM) : 128 * (first + l32);
+    asm volatile("" : "+v"(a_at[i]));
+  }
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
+    const int first = 32 * (kJ * wn + j);
+    b_at[j] = kBSlow ? slow_at(first, T::kBN) : 128 * (first + l32);
+    asm volatile("" : "+v"(b_at[j]));
+  }
+  // (32 i and 32 j rows further the swizzle is the same)
+  int chunk_at[2][2];
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) chunk_at[kk][e] = 16 * ((4 * kk + 2 * half + e) ^ minor_swz(l32));
+  auto slow4 = [&](const uint8_t* panel, int at) __attribute__((always_inline)) {
+    const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(panel + at));
+    return __builtin_bit_cast(uint2, v);
+  };
+  // Reads of a phase: first the chunks 0 of every tile, B before A, then the
+  // chunks 1; a chunk of a slow panel is two reads.
+  constexpr int kNA = kASlow ? 2 : 1, kNB = kBSlow ? 2 : 1, kSet = kJ * kNB + kI * kNA, kR = 2 * kSet;
+  auto read1 = [&](int f, const uint8_t* As, const uint8_t* Bs, int kk, int r) __attribute__((always_inline)) {
+    const int e = r / kSet, t = r % kSet;
+    if (t < kJ * kNB) {
+      const int j = t / kNB;
+      if constexpr (kBSlow) {
+        const uint2 v = slow4(Bs, b_at[j] + (32 * kk + 8 * e + 4 * (t % 2)) * 2 * T::kBN);
+        if (t % 2 == 0) fb[f][j][e].x = v.x, fb[f][j][e].y = v.y;
+        else fb[f][j][e].z = v.x, fb[f][j][e].w = v.y;
+      } else {
+        fb[f][j][e] = *reinterpret_cast<const uint4*>(Bs + b_at[j] + chunk_at[kk][e]);
+      }
+    } else {
+      const int u = t - kJ * kNB, i = u / kNA;
+      if constexpr (kASlow) {
+        const uint2 v = slow4(As, a_at[i] + (32 * kk + 8 * e + 4 * (u % 2)) * 2 * T::kBM);
+        if (u % 2 == 0) fa[f][i][e].x = v.x, fa[f][i][e].y = v.y;
+        else fa[f][i][e].z = v.x, fa[f][i][e].w = v.y;
+      } else {
+        fa[f][i][e] = *reinterpret_cast<const uint4*>(As + a_at[i] + chunk_at[kk][e]);
+      }
+    }
+  };
+  auto as_v8 = [](const uint4* v) __attribute__((always_inline)) {
+    return v8i{(int)v[0].x, (int)v[0].y, (int)v[0].z, (int)v[0].w,
+               (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
+  };
+  constexpr int kTiles = kI * kJ, kMF = kFP8 ? kTiles : 2 * kTiles;
+  auto mma1 = [&](int f, int n) __attribute__((always_inline)) {
+    const int i = n % kTiles / kJ, j = n % kJ, e = n / kTiles;
+    if constexpr (kFP8)
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(as_v8(fb[f][j]), as_v8(fa[f][i]), acc[i][j], 0, 0, 0,
+                                                                  0, 0, 0);
+    else
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fb[f][j][e]),
+                                                          __builtin_bit_cast(v8bf, fa[f][i][e]), acc[i][j], 0, 0, 0);
+  };
+  auto kstep = [&](int step, auto S) __attribute__((always_inline)) {
+    constexpr int st = decltype(S)::value;
+    const uint8_t *As = mma_part<T, 2 * st>(), *Bs = mma_part<T, 2 * st + 1>();
+    const uint8_t *An = mma_part<T, 2 * (1 - st)>(), *Bn = mma_part<T, 2 * (1 - st) + 1>();
+#pragma unroll
+    for (int n = 0; n < kMF; ++n) {
+      mma1(0, n);
+#pragma unroll
+      for (int r = n * kR / kMF; r < (n + 1) * kR / kMF; ++r) read1(1, As, Bs, 1, r);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const From next = from(step + 2);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kMF; ++n) {
+      mma1(1, n);
+#pragma unroll
+      for (int r = n * kR / kMF; r < (n + 1) * kR / kMF; ++r) read1(0, An, Bn, 0, r);
+#pragma unroll
+      for (int q = n * kL / kMF; q < (n + 1) * kL / kMF; ++q) load1(next, S, q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  // vmcnt(kL): the loads of stage 1 may stay in flight (vmcnt in bits 3:0 and
+  // 15:14, expcnt in 6:4, lgkmcnt in 11:8)
+  static_assert(kL < 64, "vmcnt holds at most 63");
+  constexpr int kStage1InFlight = (kL & 15) | ((kL >> 4) << 14) | (7 << 4) | (15 << 8);
+  {
+    const From f0 = from(0), f1 = from(1);
+#pragma unroll
+    for (int q = 0; q < kL; ++q) load1(f0, S0{}, q);
+#pragma unroll
+    for (int q = 0; q < kL; ++q) load1(f1, S1{}, q);
+  }
+  __builtin_amdgcn_s_waitcnt(kStage1InFlight);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+#pragma unroll
+  for (int r = 0; r < kR; ++r) read1(0, mma_part<T, 0>(), mma_part<T, 1>(), 0, r);
+  int step = 0;
+  for (; step + 1 < steps; step += 2) {
+    kstep(step, S0{});
+    kstep(step + 1, S1{});
+  }
+  if (step < steps) kstep(step, S0{});
+  __builtin_amdgcn_s_waitcnt(0);   // no load into the LDS outlives the loop
+  __syncthreads();
+#endif
+}
+
+// A BF16 tile through the LDS, so that it leaves in whole 16-byte chunks of
+// rows.  word(i, j, q) gives the four values of a run, packed; out(row, chunk,
+// bytes) takes chunk `chunk` (8 columns) of row `row` of the tile.  The block
+// must have met before and meets inside.  Chunks are XORed with row % 16 (or
+// the chunks of a shorter row): 8-byte writes of 32 rows and 16-byte reads
+// meet no bank conflicts.
+template <class T, class Word, class Out>
+__device__ __forceinline__ void tile_out_bf16(Word word, Out out) {
+  constexpr int kRowBytes = 2 * T::kBN, kChunks = kRowBytes / 16, kMask = (kChunks < 16 ? kChunks : 16) - 1;
+  constexpr int kRows = T::kArrA / kRowBytes;   // rows of an LDS array
+  static_assert(kRows % 32 == 0 && kRows * 4 >= T::kBM && T::kB >= T::kArrA, "the tile fits the arrays");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
+  auto part = [](int q) __attribute__((always_inline)) {
+    return q == 0 ? mma_part<T, 0>() : q == 1 ? mma_part<T, 1>() : q == 2 ? mma_part<T, 2>() : mma_part<T, 3>();
+  };
+  auto at = [](int row, int c) __attribute__((always_inline)) { return row % kRows * kRowBytes + 16 * (c ^ (row & kMask)); };
+#pragma unroll
+  for (int i = 0; i < T::kI; ++i) {
+    const int first = 32 * (T::kI * wm + i), row = first + l32;
+    uint8_t* tile = part(first / kRows);
+#pragma unroll
+    for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint2*>(tile + at(row, 4 * (T::kJ * wn + j) + q) + 8 * half) = word(i, j, q);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < T::kBM * kChunks / T::kThreads; ++k) {
+    const int task = k * T::kThreads + threadIdx.x, row = task / kChunks, c = task % kChunks;
+    out(row, c, *reinterpret_cast<const uint4*>(part(row / kRows) + at(row, c)));
+  }
+}
+
+// xcd_contiguous for 32-bit indexes.
+__device__ __forceinline__ uint32_t xcd_contiguous32(uint32_t b, uint32_t nb) {
+  const uint32_t q = nb / 8, r = nb % 8, xcd = b % 8, local = b / 8;
+  return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
+}
+
+}  // namespace coat
+
+#endif  // COAT_TILE_H

@@ -481,6 +481,147 @@ coat_status_t coat_fp8_weight_grad(const coat_weight_grad_args_t* args,
 /* Bytes of workspace for that call, or -1 for sizes it refuses. */
 int64_t coat_fp8_weight_grad_workspace(int64_t M, int64_t N, int64_t K);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The vocabulary: the operators at the two ends of a model, which read a
+ * vocab x cols matrix (one matrix where the two are tied) and whose gradients
+ * the optimizer step above takes.
+ *
+ * Matrices are BF16, or E4M3 codes under one scale (code * scale).  A token or
+ * target outside [0, vocab) is padding: its rows of outputs are zero, what its
+ * rows of inputs hold (NaN included) reaches nothing, and it adds to no
+ * gradient.  vocab at most 2^22, cols 65536, rows 2^23; rows * cols at most
+ * 2^33 and vocab * cols 2^34.  Gradients of the matrix are BF16 (written) or
+ * FP32 (written or, with accumulate, added to); sums are FP32 and their order
+ * is fixed by the sizes and inputs, no float is added by an atomic.
+ */
+
+/*
+ * Embedding lookup: out[r] = bf16(scale * table[tokens[r]]).
+ * scale * table_scale is rounded to FP32 once.  cols a multiple of 16.
+ * Errors: NULL_POINTER (args; tokens, out, table with vocab > 0),
+ * INVALID_VALUE (sizes, both tables, a scale not finite), MISALIGNED (16
+ * bytes; tokens 8), HIP.
+ */
+typedef struct coat_embedding_args {
+  const uint16_t* table;       /* vocab x cols BF16, or NULL                 */
+  const uint8_t* table_codes;  /* vocab x cols E4M3 under table_scale        */
+  const int64_t* tokens;       /* rows                                       */
+  uint16_t* out;               /* rows x cols BF16 (written)                 */
+  int64_t rows, vocab, cols;
+  float table_scale, scale;    /* table_scale: 1 for a BF16 table            */
+} coat_embedding_args_t;
+
+coat_status_t coat_fp8_embedding(const coat_embedding_args_t* args,
+                                 hipStream_t stream);
+
+/*
+ * Its gradient: dw[v] = scale * sum of dy[r] over the rows with tokens[r] = v,
+ * summed in FP32 in the rows' order (32 rows of a token to a partial sum);
+ * rows of tokens that do not occur are zero, or left as they are with
+ * accumulate.  Errors: as above (workspace with rows > 0; INVALID_VALUE for
+ * dw_bf16 with dw_f32 or accumulate and for a workspace that is too small).
+ */
+typedef struct coat_embedding_bwd_args {
+  const uint16_t* dy;      /* rows x cols BF16                               */
+  const int64_t* tokens;   /* rows                                           */
+  uint16_t* dw_bf16;       /* vocab x cols BF16 (written), or NULL           */
+  float* dw_f32;           /* vocab x cols FP32, or NULL                     */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t rows, vocab, cols;
+  float scale;
+  int32_t accumulate;
+} coat_embedding_bwd_args_t;
+
+coat_status_t coat_fp8_embedding_bwd(const coat_embedding_bwd_args_t* args,
+                                     hipStream_t stream);
+
+/* Bytes of workspace for that call, or -1 for sizes it refuses. */
+int64_t coat_fp8_embedding_bwd_workspace(int64_t rows, int64_t vocab,
+                                         int64_t cols);
+
+/*
+ * Softmax cross entropy of hidden states x against a vocabulary, from the
+ * output projection's weights, without the logits in memory:
+ *   l[v] = logit_scale * x . w[v],  lse = log sum over v of exp(l[v]),
+ *   loss = lse - l[target] + z_loss * lse^2.
+ * x and weight are both BF16 or both E4M3 (x_scale, weight_scale: 1 for
+ * BF16); products are summed in FP32 on the matrix cores, the exponentials'
+ * sums in FP32.  cols a multiple of 64 for BF16, 128 for E4M3.  Rows without a
+ * target get loss 0 and lse 0 and cost no products.  A NaN or infinity in a
+ * row of x reaches that row's results alone.
+ * Errors: NULL_POINTER (args; x, weight, targets, loss, workspace),
+ * INVALID_VALUE (sizes; BF16 with E4M3; a scale, or the product of the three,
+ * that is not positive, finite and at least 2^-126; z_loss not finite; a
+ * workspace that is too small; vocab or cols 0 with rows), MISALIGNED (16
+ * bytes; targets 8, loss and lse 4), HIP.
+ */
+typedef struct coat_cross_entropy_args {
+  const uint16_t* x;            /* rows x cols BF16, or NULL                 */
+  const uint8_t* x_codes;       /* rows x cols E4M3, or NULL                 */
+  const uint16_t* weight;       /* vocab x cols BF16, or NULL                */
+  const uint8_t* weight_codes;  /* vocab x cols E4M3, or NULL                */
+  const int64_t* targets;       /* rows                                      */
+  float* loss;                  /* rows FP32 (written)                       */
+  float* lse;                   /* rows FP32 (written), or NULL              */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t rows, vocab, cols;
+  float x_scale, weight_scale, logit_scale, z_loss;
+} coat_cross_entropy_args_t;
+
+coat_status_t coat_fp8_cross_entropy(const coat_cross_entropy_args_t* args,
+                                     hipStream_t stream);
+
+/* Bytes of workspace for that call, or -1 for sizes it refuses. */
+int64_t coat_fp8_cross_entropy_workspace(int64_t rows, int64_t vocab,
+                                         int64_t cols);
+
+/*
+ * Its gradients, with d = d_loss of the row and the lse that the call above
+ * wrote:
+ *   g[v] = d ((1 + 2 z_loss lse) exp(l[v] - lse) - [v = target]),
+ *   dx = logit_scale * g W,  dw = logit_scale * g^T x.
+ * The logits are computed again, a piece of the vocabulary at a time: as few
+ * pieces as the workspace holds (the FP32 sums of dx depend on their number).
+ * g, divided by the largest |d|, is rounded to BF16 (by at most 2^-8 of it)
+ * for dx and a BF16 dw; an FP32 dw takes it in two BF16 parts, which hold it
+ * to 2^-16, in twice the products.  dx or the dw pointers may be NULL.
+ * Errors: as above (lse and d_loss required; neither dx nor dw is
+ * NULL_POINTER; dw_bf16 with dw_f32 or accumulate is INVALID_VALUE).
+ */
+typedef struct coat_cross_entropy_bwd_args {
+  const float* d_loss;          /* rows FP32                                 */
+  const uint16_t* x;            /* as above                                  */
+  const uint8_t* x_codes;
+  const uint16_t* weight;
+  const uint8_t* weight_codes;
+  const int64_t* targets;
+  const float* lse;             /* rows FP32                                 */
+  uint16_t* dx;                 /* rows x cols BF16 (written), or NULL       */
+  uint16_t* dw_bf16;            /* vocab x cols BF16 (written), or NULL      */
+  float* dw_f32;                /* vocab x cols FP32, or NULL                */
+  void* workspace;
+  int64_t workspace_bytes;
+  int64_t rows, vocab, cols;
+  float x_scale, weight_scale, logit_scale, z_loss;
+  int32_t accumulate;
+} coat_cross_entropy_bwd_args_t;
+
+coat_status_t coat_fp8_cross_entropy_bwd(
+    const coat_cross_entropy_bwd_args_t* args, hipStream_t stream);
+
+/*
+ * Bytes of workspace for that call with pieces of `piece` vocabulary rows
+ * (rounded up to a multiple of 256; 1 gives the least that it takes, vocab
+ * what one piece takes), or -1 for sizes it refuses.  codes: x and weight are
+ * E4M3; f32: dw is FP32.
+ */
+int64_t coat_fp8_cross_entropy_bwd_workspace(int64_t rows, int64_t vocab,
+                                             int64_t cols, int64_t piece,
+                                             int32_t codes, int32_t f32);
+
 /* Static, NUL-terminated description of a status code. */
 const char* coat_status_string(coat_status_t status);
 

@@ -1,0 +1,101 @@
+"""The vocabulary operators from their formulas in 64 bits (plain torch), and
+the error bounds their tests use.
+
+Bounds (F = 2^-24, a rounding to FP32).  The matrix cores add 16 products (64
+codes) to an accumulator at a time and may truncate: a product of a sum of n
+passes at most n / 16 + 64 roundings of 2 F, relative to the sum of the
+products' magnitudes.  The hardware's exp2 and log2 are taken as 2 F off, its
+sums of exponentials pass at most 64 + strips / 16 roundings.
+"""
+import torch
+
+from activation_ref import BF16, F, code_values
+
+PADDING = -100
+
+
+def tokens(n, vocab, g, padding=0):
+    """Random tokens, some more common than others; `padding` of them outside [0, vocab)."""
+    t = (torch.rand(n, generator=g).square() * vocab).long().clamp(max=vocab - 1)
+    if padding:
+        at = torch.randperm(n, generator=g)[:padding]
+        t[at] = torch.tensor([PADDING, -1, vocab, vocab + 5, 1 << 40, -(1 << 40)])[torch.arange(padding) % 6]
+    return t
+
+
+def live_rows(targets, vocab):
+    return (targets >= 0) & (targets < vocab)
+
+
+def lookup(table, ids, scale):
+    """table in 64 bits; zeros for padding."""
+    live = live_rows(ids, table.shape[0])
+    out = torch.zeros(len(ids), table.shape[1], dtype=torch.float64)
+    out[live] = table[ids[live]] * scale
+    return out
+
+
+def lookup_bwd(dy, ids, vocab, scale):
+    """The gradient, the sums of magnitudes and the number of terms."""
+    live = live_rows(ids, vocab)
+    dw = torch.zeros(vocab, dy.shape[1], dtype=torch.float64)
+    size = torch.zeros_like(dw)
+    count = torch.zeros(vocab, dtype=torch.float64)
+    d = dy[live].double() * scale
+    dw.index_add_(0, ids[live], d)
+    size.index_add_(0, ids[live], d.abs())
+    count.index_add_(0, ids[live], torch.ones(int(live.sum()), dtype=torch.float64))
+    return dw, size, count[:, None]
+
+
+def values(t, scale):
+    return (code_values(t) if t.dtype == torch.uint8 else t.double()) * scale
+
+
+class Entropy:
+    """Loss, lse and gradients of every row with a target, with the bounds.
+
+    x, w: the matrices' values in 64 bits (scales in them)."""
+
+    def __init__(self, x, w, targets, logit_scale=1.0, z=0.0):
+        self.vocab, self.z, self.c = w.shape[0], z, logit_scale
+        self.live = live_rows(targets, self.vocab)
+        self.rows = len(targets)
+        self.x, self.w, self.t = x[self.live], w, targets[self.live]
+        k = x.shape[1]
+        self.l = logit_scale * (self.x @ w.t())
+        size = logit_scale * (self.x.abs() @ w.abs().t())
+        # a logit: the product, three scales' product and log2(e) in FP32, one multiplication
+        self.l_err = (k / 16 + 64) * 2 * F * size + 6 * F * self.l.abs()
+        self.lse = torch.logsumexp(self.l, 1) if len(self.t) else self.l.new_zeros(0)
+        at = self.l.gather(1, self.t[:, None])[:, 0]
+        big = self.l.abs().amax(1) if len(self.t) else self.lse
+        err = self.l_err.amax(1) if len(self.t) else self.lse
+        sums = (64 + self.vocab / 64 / 16 + 8) * 2 * F
+        self.lse_err = err + sums + 8 * F * (big + self.lse.abs() + 24)
+        self.loss = self.lse - at + z * self.lse ** 2
+        self.loss_err = (2 * err + sums + 12 * F * (big + self.lse.abs() + 24)
+                         + abs(z) * (2 * self.lse.abs() * self.lse_err + 4 * F * self.lse ** 2))
+
+    def spread(self, v):
+        out = torch.zeros((self.rows,) + v.shape[1:], dtype=torch.float64)
+        out[self.live] = v
+        return out
+
+    def gradients(self, d_loss, lse, parts=1, pieces=1):
+        """dx, dw and their bounds, for the given lse (what the kernel reads).
+        parts: BF16 parts that dw takes g in (dx takes one)."""
+        d, lse = d_loss[self.live].double()[:, None], lse[self.live].double()[:, None]
+        p = torch.exp(self.l - lse)
+        hot = torch.zeros_like(p).scatter_(1, self.t[:, None], 1.0) if len(self.t) else p
+        coef = 1.0 + 2.0 * self.z * lse
+        g = d * (coef * p - hot)
+        # exp(l - lse): the argument's error, exp2's, the coefficient's roundings
+        rel = torch.expm1(self.l_err + 6 * F * (self.l.abs() + lse.abs())) + 8 * F
+        err = d.abs() * (coef.abs() * p * rel + 8 * F * (coef.abs() * p + hot))
+        n_dx, n_dw = self.vocab / 16 + 64 + 64 + pieces, len(self.t) / 8 + 128 + 64
+        dx_err = (err + BF16 * (g.abs() + err)) @ self.w.abs() + n_dx * 2 * F * (g.abs() @ self.w.abs())
+        held = BF16 if parts == 1 else BF16 * BF16
+        dw_err = (err + held * (g.abs() + err)).t() @ self.x.abs() + n_dw * 2 * F * (g.abs().t() @ self.x.abs())
+        c = self.c
+        return (self.spread(c * (g @ self.w)), c * (g.t() @ self.x), self.spread(c * dx_err), c * dw_err)
