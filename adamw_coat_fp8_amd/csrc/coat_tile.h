@@ -153,30 +153,28 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
   // (Offsets are single opaque values: the compiler follows an address back
   // over a few additions only.)
   uint4 fa[2][kI][2], fb[2][kJ][2];
-  int a_at[kI], b_at[kJ];
   const int t16 = lane & 15, col16 = (lane >> 4) & 1;
+  // minor: the first tile's chunks of phase 0 ([e]; phase 1 flips bit 6), other
+  // tiles 4096 bytes further; slow: the tiles ([i], [j]), phases and chunks
+  // whole rows further
+  int a_at[kASlow ? kI : 2], b_at[kBSlow ? kJ : 2];
   auto slow_at = [&](int first, int cols) __attribute__((always_inline)) {
     const int c = first + 16 * col16 + 4 * (t16 & 3), k = 16 * half + (t16 >> 2);
     return k * 2 * cols + 64 * slow_chunk(k, c >> 5) + 2 * (c & 31);
   };
+  auto minor_at = [&](int first, int e) __attribute__((always_inline)) {
+    return 128 * (first + l32) + 16 * ((2 * half + e) ^ minor_swz(l32));
+  };
 #pragma unroll
-  for (int i = 0; i < kI; ++i) {
-    const int first = 32 * (kI * wm + i);
-    a_at[i] = kASlow ? slow_at(first, T::kBM) : 128 * (first + l32);
+  for (int i = 0; i < (kASlow ? kI : 2); ++i) {
+    a_at[i] = kASlow ? slow_at(32 * (kI * wm + i), T::kBM) : minor_at(32 * kI * wm, i);
     asm volatile("" : "+v"(a_at[i]));
   }
 #pragma unroll
-  for (int j = 0; j < kJ; ++j) {
-    const int first = 32 * (kJ * wn + j);
-    b_at[j] = kBSlow ? slow_at(first, T::kBN) : 128 * (first + l32);
+  for (int j = 0; j < (kBSlow ? kJ : 2); ++j) {
+    b_at[j] = kBSlow ? slow_at(32 * (kJ * wn + j), T::kBN) : minor_at(32 * kJ * wn, j);
     asm volatile("" : "+v"(b_at[j]));
   }
-  // (32 i and 32 j rows further the swizzle is the same)
-  int chunk_at[2][2];
-#pragma unroll
-  for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) chunk_at[kk][e] = 16 * ((4 * kk + 2 * half + e) ^ minor_swz(l32));
   auto slow4 = [&](const uint8_t* panel, int at) __attribute__((always_inline)) {
     const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(panel + at));
     return __builtin_bit_cast(uint2, v);
@@ -193,7 +191,7 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
         if (t % 2 == 0) fb[f][j][e].x = v.x, fb[f][j][e].y = v.y;
         else fb[f][j][e].z = v.x, fb[f][j][e].w = v.y;
       } else {
-        fb[f][j][e] = *reinterpret_cast<const uint4*>(Bs + b_at[j] + chunk_at[kk][e]);
+        fb[f][j][e] = *reinterpret_cast<const uint4*>(Bs + (b_at[e] ^ (64 * kk)) + 4096 * j);
       }
     } else {
       const int u = t - kJ * kNB, i = u / kNA;
@@ -202,7 +200,7 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
         if (u % 2 == 0) fa[f][i][e].x = v.x, fa[f][i][e].y = v.y;
         else fa[f][i][e].z = v.x, fa[f][i][e].w = v.y;
       } else {
-        fa[f][i][e] = *reinterpret_cast<const uint4*>(As + a_at[i] + chunk_at[kk][e]);
+        fa[f][i][e] = *reinterpret_cast<const uint4*>(As + (a_at[e] ^ (64 * kk)) + 4096 * i);
       }
     }
   };
