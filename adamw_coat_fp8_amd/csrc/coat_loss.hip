@@ -37,7 +37,9 @@ constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 using Large = MmaTile<4, 2, 2, 4>;              // 256 x 256, eight waves of 64 x 128
 using Half = MmaTile<4, 2, 1, 4, Large::kA>;    // 128 x 256, eight waves of 32 x 128
-using Thin = MmaTile<1, 2, 2, 1>;               // 64 x 64, two waves of 64 x 32
+template <int kI>
+using Thin = MmaTile<1, 2, kI, 1, 0, 5>;        // 32 kI x 64, two waves, five stages
+constexpr int kThinCols = 64, kThinStrip = 32;
 
 constexpr int kGroupM = 4;        // tile rows that are walked together
 constexpr int kUnits = 256;       // compute units of the device the plans are made for
@@ -203,15 +205,16 @@ struct LogitParams {
   int32_t steps, n_tiles;
   float scale2;             // log2(e) times what a product is multiplied by
   // loss
-  float2* part;             // [strip][ld]: largest logit and sum of exponentials
+  float2* part;             // largest logit and sum of exponentials of each strip and row
+  int64_t strip_step, row_step;
   float* at_target;         // the target's logit of each row
   const int32_t* target;    // of listed rows, or NULL
   const int64_t* targets;
-  int64_t ld;               // rows of part; values of a row of g
   // gradient
   const RowInfo* info;
-  uint16_t* g;
+  uint16_t* g;              // rows of ld values
   uint16_t* g_rest;         // what BF16 left of g, or NULL
+  int64_t ld;
   int32_t v0;               // first vocabulary row of the piece
 };
 
@@ -241,8 +244,11 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
   }, boff);
   v16f acc[T::kI][T::kJ];
   mma_zero<T>(acc);
-  mma_run<T, kFP8, false, false>(acc, p.steps, [&](int s) { return a0 + 128 * (int64_t)s; }, aoff,
-                                 [&](int s) { return b0 + 128 * (int64_t)s; }, boff, boff, [](int) { return false; });
+  if constexpr (T::kStages > 2)
+    mma_stream<T, kFP8>(acc, p.steps, a0, aoff, b0, boff);
+  else
+    mma_run<T, kFP8, false, false>(acc, p.steps, [&](int s) { return a0 + 128 * (int64_t)s; }, aoff,
+                                   [&](int s) { return b0 + 128 * (int64_t)s; }, boff, boff, [](int) { return false; });
 
   const int64_t col0 = n0 + 32 * T::kJ * wn;          // the wave's first column
   const int64_t valid = p.N - col0;                    // of its columns
@@ -274,7 +280,7 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
           sum[r % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], p.scale2, -top));
       const float all = pair_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
       const bool stored = row < live;
-      if (stored && half == 0) p.part[(n0 / (32 * T::kJ) + wn) * p.ld + row] = make_float2(top, all);
+      if (stored && half == 0) p.part[(n0 / (32 * T::kJ) + wn) * p.strip_step + row * p.row_step] = make_float2(top, all);
       // the target's logit, where it lies in the lane's columns
       int64_t t = -1;
       if (stored) t = p.target ? (int64_t)p.target[row] : p.targets[row];
@@ -361,62 +367,94 @@ __global__ __launch_bounds__(Large::kThreads) void logit_large_kernel(const Logi
   }
 }
 
-// At most 64 rows.
-template <bool kFP8, bool kGrad>
-__global__ __launch_bounds__(Thin::kThreads) void logit_thin_kernel(const LogitParams p) {
+// At most 32 kI rows.
+template <bool kFP8, bool kGrad, int kI>
+__global__ __launch_bounds__(128) void logit_thin_kernel(const LogitParams p) {
   const int64_t live = p.header ? p.header->live : p.M;
   if (live == 0) return;
-  logit_tile<Thin, kFP8, kGrad>(p, live, 0, (int64_t)xcd_contiguous32(blockIdx.x, gridDim.x) * Thin::kBN);
+  logit_tile<Thin<kI>, kFP8, kGrad>(p, live, 0, (int64_t)xcd_contiguous32(blockIdx.x, gridDim.x) * kThinCols);
 }
 
 struct JoinParams {
   const float2* part;
+  int64_t strip_step, row_step;
   const float* at_target;
   const int32_t* place;     // of each row in the list, or NULL
   const int64_t* targets;
   float* loss;
   float* lse;               // or NULL
-  int64_t M, V, ld;
+  int64_t M, V;
   int32_t strips;
   float z;
 };
 
-// Joins the strips of 16 rows; 16 threads a row.
+// Joins strips g, g + kBy, .. of a row, eight loads in flight.
+template <int kBy>
+__device__ __forceinline__ float2 join_strips(const JoinParams& p, int64_t at, int g) {
+  const float2* part = p.part + at * p.row_step;
+  float top = -FLT_MAX, sum = 0.0f;
+  for (int s = g; s < p.strips; s += 8 * kBy) {
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = s + i * kBy < p.strips ? part[(s + i * kBy) * p.strip_step] : make_float2(-FLT_MAX, 0.0f);
+    float m = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i].x);
+    sum *= __builtin_amdgcn_exp2f(top - m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += v[i].y * __builtin_amdgcn_exp2f(v[i].x - m);
+    top = m;
+  }
+  return make_float2(top, sum);
+}
+
+__device__ __forceinline__ void store_loss(const JoinParams& p, int64_t row, int64_t at, float top, float sum) {
+  float loss = 0.0f, lse = 0.0f;
+  if (at >= 0) {
+    const float log2s = __builtin_amdgcn_logf(sum);
+    lse = kLn2 * (top + log2s);
+    loss = kLn2 * ((top - p.at_target[at]) + log2s) + p.z * lse * lse;
+  }
+  p.loss[row] = loss;
+  if (p.lse) p.lse[row] = lse;
+}
+
+__device__ __forceinline__ int64_t place_of(const JoinParams& p, int64_t row) {
+  const int64_t target = p.targets[row];
+  if (target < 0 || target >= p.V) return -1;
+  return p.place ? p.place[row] : row;
+}
+
+// 16 rows, 16 threads each.
 __global__ __launch_bounds__(256) void loss_join_kernel(const JoinParams p) {
   __shared__ float2 part[16][17];
   const int t = threadIdx.x, r16 = t & 15, g = t >> 4;
   const int64_t row = (int64_t)blockIdx.x * 16 + r16;
-  int64_t at = -1;
-  if (row < p.M) {
-    const int64_t target = p.targets[row];
-    if (target >= 0 && target < p.V) at = p.place ? p.place[row] : row;
-  }
-  float top = -FLT_MAX, sum = 0.0f;
-  if (at >= 0) {
-#pragma unroll 4
-    for (int s = g; s < p.strips; s += 16) {
-      const float2 v = p.part[s * p.ld + at];
-      const float m = fmaxf(top, v.x);
-      sum = sum * __builtin_amdgcn_exp2f(top - m) + v.y * __builtin_amdgcn_exp2f(v.x - m);
-      top = m;
-    }
-  }
-  part[r16][g] = make_float2(top, sum);
+  const int64_t at = row < p.M ? place_of(p, row) : -1;
+  part[r16][g] = at >= 0 ? join_strips<16>(p, at, g) : make_float2(-FLT_MAX, 0.0f);
   __syncthreads();
   if (t >= 16 || row >= p.M) return;
-  float loss = 0.0f, lse = 0.0f;
+  float top = -FLT_MAX, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, part[r16][i].x);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum += part[r16][i].y * __builtin_amdgcn_exp2f(part[r16][i].x - top);
+  store_loss(p, row, at, top, sum);
+}
+
+// Few rows: a wave each.
+__global__ __launch_bounds__(64) void loss_join_few_kernel(const JoinParams p) {
+  const int64_t row = blockIdx.x, at = place_of(p, row);
+  float top = -FLT_MAX, sum = 0.0f;
   if (at >= 0) {
-    float m = -FLT_MAX, s = 0.0f;
+    const float2 v = join_strips<64>(p, at, threadIdx.x);
+    top = v.x;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = fmaxf(m, part[r16][i].x);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s += part[r16][i].y * __builtin_amdgcn_exp2f(part[r16][i].x - m);
-    const float log2s = __builtin_amdgcn_logf(s);
-    lse = kLn2 * (m + log2s);
-    loss = kLn2 * ((m - p.at_target[at]) + log2s) + p.z * lse * lse;
+    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+    sum = lanes_sum<64>(v.y * __builtin_amdgcn_exp2f(v.x - top));
   }
-  p.loss[row] = loss;
-  if (p.lse) p.lse[row] = lse;
+  if (threadIdx.x == 0) store_loss(p, row, at, top, sum);
 }
 
 // -------------------------------------------------- products with g
@@ -600,7 +638,7 @@ struct LossSpace {
   int32_t *list, *place, *target;
   float* at_target;
   float2* part;
-  int64_t ld, bytes;
+  int64_t strip_step, row_step, bytes;
   int32_t strips;
 };
 
@@ -622,9 +660,10 @@ LossSpace loss_space(void* base, int64_t M, int64_t V) {
     s.place = c.take<int32_t>(4 * M);
     s.target = c.take<int32_t>(4 * M);
   }
-  s.ld = round_up(M, 16);
-  s.strips = (int32_t)(thin ? up(V, Thin::kBN) * Thin::kWN : up(V, Large::kBN) * Large::kWN);
-  s.part = c.take<float2>(8 * s.ld * s.strips);
+  s.strips = (int32_t)(thin ? up(V, kThinCols) * (kThinCols / kThinStrip) : up(V, Large::kBN) * Large::kWN);
+  s.row_step = thin ? s.strips : 1;
+  s.strip_step = thin ? 1 : round_up(M, 16);
+  s.part = c.take<float2>(8 * (thin ? M : s.strip_step) * s.strips);
   s.bytes = c.used;
   return s;
 }
@@ -724,9 +763,13 @@ hipError_t launch(const void* fn, int64_t blocks, int threads, void* params, hip
 template <bool kGrad>
 hipError_t launch_logits(LogitParams& p, bool fp8, hipStream_t stream) {
   if (p.M <= kThinRows) {
-    const void* fn = fp8 ? reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad>)
-                         : reinterpret_cast<const void*>(&logit_thin_kernel<false, kGrad>);
-    return launch(fn, up(kGrad ? p.ld : p.N, Thin::kBN), Thin::kThreads, &p, stream);
+    // (g has 64 rows for the products at least)
+    constexpr int kLeast = kGrad ? 2 : 1;
+    const void* fns[] = {reinterpret_cast<const void*>(&logit_thin_kernel<false, kGrad, kLeast>),
+                         reinterpret_cast<const void*>(&logit_thin_kernel<false, kGrad, 2>),
+                         reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad, kLeast>),
+                         reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad, 2>)};
+    return launch(fns[2 * fp8 + (p.M > 32)], up(p.N, kThinCols), 128, &p, stream);
   }
   const void* fn = fp8 ? reinterpret_cast<const void*>(&logit_large_kernel<true, kGrad>)
                        : reinterpret_cast<const void*>(&logit_large_kernel<false, kGrad>);
@@ -790,7 +833,8 @@ coat_status_t coat_fp8_cross_entropy(const coat_cross_entropy_args_t* a, hipStre
     p.target = s.target;
     p.list = s.list;
     p.header = s.header;
-    p.ld = s.ld;
+    p.strip_step = s.strip_step;
+    p.row_step = s.row_step;
     if (s.list) {
       PrepParams q;
       memset(&q, 0, sizeof(q));
@@ -815,10 +859,12 @@ coat_status_t coat_fp8_cross_entropy(const coat_cross_entropy_args_t* a, hipStre
       j.lse = a->lse ? a->lse + m0 : nullptr;
       j.M = rows;
       j.V = V;
-      j.ld = s.ld;
+      j.strip_step = s.strip_step;
+      j.row_step = s.row_step;
       j.strips = s.strips;
       j.z = a->z_loss;
-      e = launch(reinterpret_cast<const void*>(&loss_join_kernel), up(rows, 16), 256, &j, stream);
+      e = s.list ? launch(reinterpret_cast<const void*>(&loss_join_kernel), up(rows, 16), 256, &j, stream)
+                 : launch(reinterpret_cast<const void*>(&loss_join_few_kernel), rows, 64, &j, stream);
     }
   }
   return e == hipSuccess ? COAT_OK : hip_fail(e);

@@ -40,10 +40,11 @@ typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 // kWM x kWN waves of kI x kJ tiles of 32 x 32.  kArrA: bytes of an LDS array
-// of A, for tiles that share a kernel's arrays with a larger one.
-template <int kWM_, int kWN_, int kI_, int kJ_, int kArrA_ = 0>
+// of A, for tiles that share a kernel's arrays with a larger one.  kStages: of
+// mma_stream; 2 for mma_run.
+template <int kWM_, int kWN_, int kI_, int kJ_, int kArrA_ = 0, int kStages_ = 2>
 struct MmaTile {
-  static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kJ = kJ_;
+  static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kJ = kJ_, kStages = kStages_;
   static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
   static constexpr int kBM = 32 * kWM * kI, kBN = 32 * kWN * kJ;
   static constexpr int kA = 128 * kBM, kB = 128 * kBN;               // bytes of a stage's panels
@@ -51,18 +52,25 @@ struct MmaTile {
   static constexpr int kArrA = kArrA_ ? kArrA_ : kA;
 };
 
-// The four LDS arrays of a kernel, A and B of the two stages.  Being distinct
+// The LDS arrays of a kernel: A and B of two stages (arrays 0 to 3), or with
+// more stages an array for each, A's panel and B's behind it.  Being distinct
 // objects, the compiler can tell the loads into one stage from the reads of
-// the other, and does not wait for loads in flight before it reads.
+// the other, and does not wait for loads in flight before it reads (it keeps
+// apart seven such objects at most).
 template <int kBytes, int kWhich>
 __device__ __forceinline__ uint8_t* mma_array() {
   __shared__ __attribute__((aligned(1024))) uint8_t bytes[kBytes];
   return bytes;
 }
 
+template <class T>
+constexpr int mma_part_bytes(int which) {
+  return T::kStages > 2 ? T::kA + T::kB : which % 2 == 0 ? T::kArrA : T::kB;
+}
+
 template <class T, int kWhich>
 __device__ __forceinline__ uint8_t* mma_part() {
-  return mma_array<kWhich % 2 == 0 ? T::kArrA : T::kB, kWhich>();
+  return mma_array<mma_part_bytes<T>(kWhich), kWhich>();
 }
 
 // Minor panels: the 16-byte chunk of a 128-byte row is XORed with (row / 2) % 8,
@@ -271,6 +279,104 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
 #endif
 }
 
+// The same for minor operands in a thin tile, which waits for memory and not
+// for the MFMAs: kStages stages in a ring, kStages - 1 steps of loads in
+// flight, one barrier a step.
+template <class T, bool kFP8>
+__device__ __forceinline__ void mma_stream(v16f (&acc)[T::kI][T::kJ], int steps, const uint8_t* a,
+                                           const uint32_t (&aoff)[T::kLA], const uint8_t* b,
+                                           const uint32_t (&boff)[T::kLB]) {
+#if __HIP_DEVICE_COMPILE__
+  constexpr int kI = T::kI, kJ = T::kJ, kLA = T::kLA, kLB = T::kLB, kL = kLA + kLB, kS = T::kStages;
+  static_assert(kS > 2 && kS <= 7 && kL * (kS - 1) < 64, "stages and loads in flight");
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
+  int a_at[2], b_at[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int chunk = 16 * ((2 * half + e) ^ minor_swz(l32));
+    a_at[e] = 128 * (32 * kI * wm + l32) + chunk;
+    b_at[e] = T::kA + 128 * (32 * kJ * wn + l32) + chunk;
+    asm volatile("" : "+v"(a_at[e]), "+v"(b_at[e]));
+  }
+  auto load = [&](int step, auto S) __attribute__((always_inline)) {
+    constexpr int st = decltype(S)::value;
+    const int64_t at = 128 * (int64_t)(step < steps ? step : steps - 1);
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(a + at), (short)0, (int)0xFFFFFFFF, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc((void*)(b + at), (short)0, (int)0xFFFFFFFF, 0x00020000);
+#pragma unroll
+    for (int q = 0; q < kLB; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, mma_part<T, st>() + T::kA + 1024 * (kLB * wave + q), 16, (int)boff[q], 0, 0, 0);
+#pragma unroll
+    for (int q = 0; q < kLA; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, mma_part<T, st>() + 1024 * (kLA * wave + q), 16, (int)aoff[q], 0, 0, 0);
+  };
+  // vmcnt(kL (kS - 2)), and lgkmcnt(0): the wave has read the stage before
+  constexpr int kFlight = kL * (kS - 2), kWait = (kFlight & 15) | ((kFlight >> 4) << 14) | (7 << 4);
+  auto kstep = [&](int step, auto S) __attribute__((always_inline)) {
+    constexpr int st = decltype(S)::value;
+    __builtin_amdgcn_s_waitcnt(kWait);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");
+    load(step + kS - 1, std::integral_constant<int, (st + kS - 1) % kS>{});
+    const uint8_t* p = mma_part<T, st>();
+    auto as_v8 = [](const uint4& lo, const uint4& hi) __attribute__((always_inline)) {
+      return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w, (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+    };
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      uint4 fa[kI][2], fb[kJ][2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) fb[j][e] = *reinterpret_cast<const uint4*>(p + (b_at[e] ^ (64 * kk)) + 4096 * j);
+#pragma unroll
+        for (int i = 0; i < kI; ++i) fa[i][e] = *reinterpret_cast<const uint4*>(p + (a_at[e] ^ (64 * kk)) + 4096 * i);
+      }
+#pragma unroll
+      for (int i = 0; i < kI; ++i)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+          if constexpr (kFP8) {
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(as_v8(fb[j][0], fb[j][1]), as_v8(fa[i][0], fa[i][1]),
+                                                                        acc[i][j], 0, 0, 0, 0, 0, 0);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fb[j][e]),
+                                                                  __builtin_bit_cast(v8bf, fa[i][e]), acc[i][j], 0, 0, 0);
+          }
+        }
+    }
+  };
+  auto each = [&](auto self, int step, auto S, auto fn) __attribute__((always_inline)) -> void {
+    constexpr int st = decltype(S)::value;
+    if constexpr (st < kS) {
+      if (!fn(step + st, S)) return;
+      self(self, step, std::integral_constant<int, st + 1>{}, fn);
+    }
+  };
+  using S0 = std::integral_constant<int, 0>;
+  each(each, 0, S0{}, [&](int step, auto S) __attribute__((always_inline)) {
+    if constexpr (decltype(S)::value < kS - 1) load(step, S);
+    return true;
+  });
+  int step = 0;
+  for (; step + kS <= steps; step += kS)
+    each(each, step, S0{}, [&](int t, auto S) __attribute__((always_inline)) {
+      kstep(t, S);
+      return true;
+    });
+  each(each, step, S0{}, [&](int t, auto S) __attribute__((always_inline)) {
+    if (t >= steps) return false;
+    kstep(t, S);
+    return true;
+  });
+  __builtin_amdgcn_s_waitcnt(0);   // no load into the LDS outlives the loop
+  __syncthreads();
+#endif
+}
+
 // A BF16 tile through the LDS, so that it leaves in whole 16-byte chunks of
 // rows.  word(i, j, q) gives the four values of a run, packed; out(row, chunk,
 // bytes) takes chunk `chunk` (8 columns) of row `row` of the tile.  The block
@@ -280,8 +386,8 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
 template <class T, class Word, class Out>
 __device__ __forceinline__ void tile_out_bf16(Word word, Out out) {
   constexpr int kRowBytes = 2 * T::kBN, kChunks = kRowBytes / 16, kMask = (kChunks < 16 ? kChunks : 16) - 1;
-  constexpr int kRows = T::kArrA / kRowBytes;   // rows of an LDS array
-  static_assert(kRows % 32 == 0 && kRows * 4 >= T::kBM && T::kB >= T::kArrA, "the tile fits the arrays");
+  constexpr int kPart = mma_part_bytes<T>(0), kRows = kPart / kRowBytes / 32 * 32;   // rows of an LDS array
+  static_assert(kRows >= 32 && kRows * 4 >= T::kBM && mma_part_bytes<T>(1) >= kPart, "the tile fits the arrays");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
   auto part = [](int q) __attribute__((always_inline)) {
