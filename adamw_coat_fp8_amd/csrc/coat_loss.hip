@@ -36,11 +36,12 @@ namespace {
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 using Large = MmaTile<4, 2, 2, 4>;              // 256 x 256, eight waves of 64 x 128
-using Half = MmaTile<4, 2, 1, 4, Large::kA>;    // 128 x 256, eight waves of 32 x 128
+using Half = MmaTile<2, 4, 2, 2, Large::kA>;    // 128 x 256, eight waves of 64 x 64
 template <int kI>
 using Thin = MmaTile<1, 2, kI, 1, 0, 5>;        // 32 kI x 64, two waves, five stages
 constexpr int kThinCols = 64, kThinStrip = 32;
 
+constexpr int kStrip = 128;       // columns of a partial softmax, but for thin tiles
 constexpr int kGroupM = 4;        // tile rows that are walked together
 constexpr int kUnits = 256;       // compute units of the device the plans are made for
 
@@ -227,6 +228,54 @@ __device__ __forceinline__ void tile_at(uint32_t order, uint32_t m_tiles, uint32
   tm = first + local - tn * rows;
 }
 
+// How M rows are cut into tiles of n_tiles columns: 256 rows each, but 128 for
+// a last row of tiles that holds no more; and the last round of whole tiles in
+// halves, where that ends earlier.  In units of half a tile's time, whole
+// tiles first: keeping `rem` of them in the last round takes 2 units there and
+// leaves room for 2 (units - rem) halves.
+struct TilePlan {
+  uint32_t rows, whole, halves;   // whole rows of tiles; whole tiles; halves behind them: the last row's, then split ones
+  uint32_t last;                  // halves of the last row
+  __host__ __device__ TilePlan(int64_t M, uint32_t n_tiles) {
+    const uint32_t rest = (uint32_t)(M % Large::kBM);
+    rows = (uint32_t)(M / Large::kBM) + (rest > Half::kBM);
+    last = rest > 0 && rest <= Half::kBM ? n_tiles : 0;
+    whole = rows * n_tiles;
+    const uint32_t rem = whole % kUnits;
+    const uint32_t split = rem > 0 && last + 2 * rem <= kUnits ? rem : 0;
+    whole -= split;
+    halves = last + 2 * split;
+  }
+};
+
+// The tile of block b; false: none.
+struct TileAt {
+  int64_t m0;
+  uint32_t tn;
+  bool half;
+};
+
+__device__ __forceinline__ bool tile_of(uint32_t b, const TilePlan& p, uint32_t n_tiles, TileAt& t) {
+  uint32_t tm;
+  if (b < p.whole) {
+    tile_at(xcd_contiguous32(b, p.whole), p.rows, n_tiles, tm, t.tn);
+    t.m0 = (int64_t)tm * Large::kBM;
+    t.half = false;
+    return true;
+  }
+  if (b >= p.whole + p.halves) return false;
+  const uint32_t order = xcd_contiguous32(b - p.whole, p.halves);
+  t.half = true;
+  if (order < p.last) {
+    t.m0 = (int64_t)p.rows * Large::kBM;
+    t.tn = order;
+  } else {
+    tile_at(p.whole + ((order - p.last) >> 1), p.rows, n_tiles, tm, t.tn);
+    t.m0 = (int64_t)tm * Large::kBM + Half::kBM * ((order - p.last) & 1);
+  }
+  return true;
+}
+
 template <class T, bool kFP8, bool kGrad>
 __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t live, const int64_t m0, const int64_t n0) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -278,9 +327,25 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
 #pragma unroll
         for (int r = 0; r < 16; ++r)
           sum[r % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], p.scale2, -top));
-      const float all = pair_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      float all = pair_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
       const bool stored = row < live;
-      if (stored && half == 0) p.part[(n0 / (32 * T::kJ) + wn) * p.strip_step + row * p.row_step] = make_float2(top, all);
+      int strip = wn;
+      if constexpr (32 * T::kJ < kStrip && T::kStages == 2) {
+        // two waves share a strip: the odd one hands its part over
+        static_assert(64 * T::kJ == kStrip, "two waves");
+        float2* shared = reinterpret_cast<float2*>(mma_part<T, 0>()) + 32 * (T::kI * wm + i) + l32 + T::kBM * (wn >> 1);
+        if ((wn & 1) && half == 0) *shared = make_float2(top, all);
+        __syncthreads();
+        if (!(wn & 1)) {
+          const float2 o = *shared;
+          const float m = fmaxf(top, o.x);
+          all = all * __builtin_amdgcn_exp2f(top - m) + o.y * __builtin_amdgcn_exp2f(o.x - m);
+          top = m;
+        }
+        strip = wn & 1 ? -1 : wn >> 1;
+      }
+      if (stored && half == 0 && strip >= 0)
+        p.part[(n0 / (T::kStages == 2 ? kStrip : 32 * T::kJ) + strip) * p.strip_step + row * p.row_step] = make_float2(top, all);
       // the target's logit, where it lies in the lane's columns
       int64_t t = -1;
       if (stored) t = p.target ? (int64_t)p.target[row] : p.targets[row];
@@ -346,25 +411,15 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
   }
 }
 
-// The tiles of `live` rows in order, the last round of them in halves where
-// that fills it; the grid is that of all M rows, and blocks past the last tile
+// The grid is that of all M rows; blocks past the last tile of the live ones
 // end.
 template <bool kFP8, bool kGrad>
 __global__ __launch_bounds__(Large::kThreads) void logit_large_kernel(const LogitParams p) {
   const int64_t live = p.header ? p.header->live : p.M;
-  const uint32_t m_tiles = (uint32_t)((live + Large::kBM - 1) / Large::kBM), n_tiles = (uint32_t)p.n_tiles;
-  const uint32_t tiles = m_tiles * n_tiles, rem = tiles % kUnits;
-  const uint32_t halves = 2 * rem <= kUnits ? rem : 0, whole = tiles - halves, b = blockIdx.x;
-  uint32_t tm, tn;
-  if (b < whole) {
-    tile_at(xcd_contiguous32(b, whole), m_tiles, n_tiles, tm, tn);
-    logit_tile<Large, kFP8, kGrad>(p, live, (int64_t)tm * Large::kBM, (int64_t)tn * Large::kBN);
-  } else if (b < whole + 2 * halves) {
-    const uint32_t order = xcd_contiguous32(b - whole, 2 * halves);
-    tile_at(whole + (order >> 1), m_tiles, n_tiles, tm, tn);
-    const int64_t m0 = (int64_t)tm * Large::kBM + Half::kBM * (order & 1);
-    if (m0 < live) logit_tile<Half, kFP8, kGrad>(p, live, m0, (int64_t)tn * Large::kBN);
-  }
+  TileAt t;
+  if (!tile_of(blockIdx.x, TilePlan(live, (uint32_t)p.n_tiles), (uint32_t)p.n_tiles, t)) return;
+  if (!t.half) logit_tile<Large, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
+  else if (t.m0 < live) logit_tile<Half, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
 }
 
 // At most 32 kI rows.
@@ -461,6 +516,23 @@ __global__ __launch_bounds__(64) void loss_join_few_kernel(const JoinParams p) {
 
 enum Out { kBF16 = 0, kF32 = 1, kF32Add = 2 };
 
+// How a product's contraction is split where its tiles leave compute units
+// empty: into parts of partial sums.  A function of the rows (M, or the live
+// ones) alone, on the device too.
+struct Splits {
+  int32_t most;        // by the steps: eight to a part at least
+  int32_t always;      // partial sums even of one part (joined over pieces)
+  int64_t room;        // rows that the partial sums have room for
+  __host__ __device__ int32_t parts(int64_t rows, uint32_t n_tiles) const {
+    const int64_t tiles = (rows + Large::kBM - 1) / Large::kBM * n_tiles;
+    if (tiles == 0 || tiles > kUnits / 2) return 1;
+    int64_t s = kUnits / tiles;
+    s = s < most ? s : most;
+    s = s < room / rows ? s : room / rows;
+    return (int32_t)(s < 1 ? 1 : s);
+  }
+};
+
 struct ProductParams {
   const uint8_t* a;         // g: rows of lda bytes
   const uint8_t* a_rest;    // its second part, or NULL
@@ -468,11 +540,13 @@ struct ProductParams {
   const Header* header;
   const int32_t* list;      // C's row m goes to row list[m], or NULL
   void* out;                // BF16 or FP32, rows of N values
-  float* partial;           // FP32 sums instead, [split][row][N], or NULL
-  int64_t M, N, partial_rows;
+  float* partial;           // FP32 sums, [split][row][N], or NULL
+  int64_t M, N;
+  Splits splits;
   uint32_t lda, ldb;
   int32_t k_rows;           // contracted rows of b; those of a are padded with zeros to a multiple of 64
-  int32_t splits, mode;     // mode: of out, or of the partial sums
+  int32_t mode;             // of out
+  int32_t add;              // the partial sums are added to
   float scale;              // of out, times the header's d_max
   uint32_t n_tiles;
 };
@@ -480,13 +554,13 @@ struct ProductParams {
 // kGT: C = g^T x (A slow, the contracted rows are the live ones); else g W.
 template <class T, bool kGT>
 __device__ __forceinline__ void product_tile(const ProductParams& p, const int64_t live, const int64_t m0, const int64_t n0,
-                                             const int part) {
+                                             const int part, const int parts) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
   const int64_t M = kGT ? p.M : live;
   const int k_rows = kGT ? (int)live : p.k_rows;
   const int each = (k_rows + 63) / 64, all = p.a_rest ? 2 * each : each;
-  const int first = (int)((int64_t)all * part / p.splits), last = (int)((int64_t)all * (part + 1) / p.splits);
+  const int first = (int)((int64_t)all * part / parts), last = (int)((int64_t)all * (part + 1) / parts);
   uint32_t aoff[T::kLA], boff[T::kLB], blast[T::kLB];
   const int64_t cols = p.N - n0;
   if constexpr (kGT) {
@@ -509,9 +583,11 @@ __device__ __forceinline__ void product_tile(const ProductParams& p, const int64
       [&](int s) { return first + s < each ? a0 + (first + s) * a_step : a1 + (first + s - each) * a_step; }, aoff,
       [&](int s) { return b0 + (first + s < each ? first + s : first + s - each) * b_step; }, boff, blast,
       [&](int s) { return first + s == each - 1 || first + s == 2 * each - 1; });
-  if (p.partial || p.mode != kBF16) {
-    const float scale = p.partial ? 1.0f : p.scale * p.header->d_max;
-    float* out = p.partial ? p.partial + part * p.partial_rows * p.N : (float*)p.out;
+  const bool partial = parts > 1 || p.splits.always;
+  if (partial || p.mode != kBF16) {
+    const float scale = partial ? 1.0f : p.scale * p.header->d_max;
+    const bool add = partial ? p.add : p.mode == kF32Add;
+    float* out = partial ? p.partial + part * M * p.N : (float*)p.out;
 #pragma unroll
     for (int i = 0; i < T::kI; ++i) {
       const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
@@ -525,7 +601,7 @@ __device__ __forceinline__ void product_tile(const ProductParams& p, const int64
           float4* dst = reinterpret_cast<float4*>(out + row * p.N + col);
           float4 v = make_float4(acc[i][j][4 * q] * scale, acc[i][j][4 * q + 1] * scale, acc[i][j][4 * q + 2] * scale,
                                  acc[i][j][4 * q + 3] * scale);
-          if (p.mode == kF32Add) {
+          if (add) {
             const float4 o = *dst;
             v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
           }
@@ -547,26 +623,20 @@ __device__ __forceinline__ void product_tile(const ProductParams& p, const int64
 template <bool kGT>
 __global__ __launch_bounds__(Large::kThreads) void product_kernel(const ProductParams p) {
   const int64_t live = p.header->live, M = kGT ? p.M : live;
-  const uint32_t m_tiles = (uint32_t)((M + Large::kBM - 1) / Large::kBM), tiles = m_tiles * p.n_tiles;
-  const uint32_t b = blockIdx.x;
-  uint32_t tm, tn;
-  if (p.splits > 1) {
-    if (b >= tiles * p.splits) return;
-    const uint32_t order = xcd_contiguous32(b, tiles * p.splits), part = order / tiles;
-    tile_at(order - part * tiles, m_tiles, p.n_tiles, tm, tn);
-    product_tile<Large, kGT>(p, live, (int64_t)tm * Large::kBM, (int64_t)tn * Large::kBN, (int)part);
+  const int parts = p.splits.parts(M, p.n_tiles);
+  TileAt t;
+  if (parts > 1) {
+    const uint32_t m_tiles = (uint32_t)((M + Large::kBM - 1) / Large::kBM), tiles = m_tiles * p.n_tiles;
+    if (blockIdx.x >= tiles * parts) return;
+    const uint32_t order = xcd_contiguous32(blockIdx.x, tiles * parts), part = order / tiles;
+    uint32_t tm;
+    tile_at(order - part * tiles, m_tiles, p.n_tiles, tm, t.tn);
+    product_tile<Large, kGT>(p, live, (int64_t)tm * Large::kBM, (int64_t)t.tn * Large::kBN, (int)part, parts);
     return;
   }
-  const uint32_t rem = tiles % kUnits, halves = 2 * rem <= kUnits ? rem : 0, whole = tiles - halves;
-  if (b < whole) {
-    tile_at(xcd_contiguous32(b, whole), m_tiles, p.n_tiles, tm, tn);
-    product_tile<Large, kGT>(p, live, (int64_t)tm * Large::kBM, (int64_t)tn * Large::kBN, 0);
-  } else if (b < whole + 2 * halves) {
-    const uint32_t order = xcd_contiguous32(b - whole, 2 * halves);
-    tile_at(whole + (order >> 1), m_tiles, p.n_tiles, tm, tn);
-    const int64_t m0 = (int64_t)tm * Large::kBM + Half::kBM * (order & 1);
-    if (m0 < M) product_tile<Half, kGT>(p, live, m0, (int64_t)tn * Large::kBN, 0);
-  }
+  if (!tile_of(blockIdx.x, TilePlan(M, p.n_tiles), p.n_tiles, t)) return;
+  if (!t.half) product_tile<Large, kGT>(p, live, t.m0, (int64_t)t.tn * Large::kBN, 0, 1);
+  else if (t.m0 < M) product_tile<Half, kGT>(p, live, t.m0, (int64_t)t.tn * Large::kBN, 0, 1);
 }
 
 struct FinishParams {
@@ -574,8 +644,10 @@ struct FinishParams {
   const Header* header;
   const int32_t* list;      // rows of out, and the live rows alone; or NULL: M rows
   void* out;
-  int64_t M, N, partial_rows;
-  int32_t splits, mode;
+  int64_t M, N;
+  Splits splits;
+  uint32_t n_tiles;
+  int32_t mode;
   float scale;
 };
 
@@ -584,12 +656,14 @@ __global__ __launch_bounds__(256) void finish_kernel(const FinishParams p) {
   const int64_t rows = p.list ? (int64_t)p.header->live : p.M, quads = p.N / 4;
   const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, row = at / quads, col = 4 * (at - row * quads);
   if (row >= rows) return;
+  const int parts = p.splits.parts(rows, p.n_tiles);
+  if (parts == 1 && !p.splits.always) return;   // the product wrote the result
   const float scale = p.scale * p.header->d_max;
   const float* src = p.partial + row * p.N + col;
   float4 v = *reinterpret_cast<const float4*>(src);
 #pragma unroll 4
-  for (int s = 1; s < p.splits; ++s) {
-    const float4 o = *reinterpret_cast<const float4*>(src + s * p.partial_rows * p.N);
+  for (int s = 1; s < parts; ++s) {
+    const float4 o = *reinterpret_cast<const float4*>(src + s * rows * p.N);
     v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
   }
   v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
@@ -668,13 +742,20 @@ LossSpace loss_space(void* base, int64_t M, int64_t V) {
   return s;
 }
 
-// Splits of a product's contraction where its tiles leave compute units empty,
-// eight steps to a part at least.
-int32_t splits_for(int64_t tiles, int64_t steps) {
-  if (tiles <= 0 || tiles > kUnits / 2) return 1;
-  const int64_t most = steps / 8, want = kUnits / tiles;
-  const int64_t s = want < most ? want : most;
-  return (int32_t)(s < 1 ? 1 : s);
+// Splits of a product of up to `rows` rows and `cols` columns over `steps`.
+// room: rows that the parts of any number of rows take at most.
+Splits splits_for(int64_t rows, int64_t cols, int64_t steps, bool always) {
+  Splits s;
+  const int64_t n_tiles = up(cols, Large::kBN), by_steps = steps / 8, by_tiles = kUnits / n_tiles;
+  s.most = (int32_t)(by_steps < by_tiles ? by_steps : by_tiles);
+  s.always = always;
+  s.room = 0;
+  if (s.most > 1 && up(rows, Large::kBM) * n_tiles <= 2 * kUnits) {
+    const int64_t all = Large::kBM * kUnits / n_tiles;
+    s.room = s.most * rows < all ? s.most * rows : all;
+  }
+  if (always && s.room < rows) s.room = rows;
+  return s;
 }
 
 struct GradSpace {
@@ -686,7 +767,7 @@ struct GradSpace {
   uint16_t *g, *g_rest, *w_bf16;
   float *dx_sum, *dw_sum;
   int64_t pieces, piece, bytes;   // piece: vocabulary rows, a multiple of 256
-  int32_t dx_splits, dw_splits;
+  Splits dx_splits, dw_splits;
 };
 
 struct GradShape {
@@ -700,9 +781,9 @@ GradSpace grad_space_of(void* base, const GradShape& h, int64_t pieces) {
   memset(&s, 0, sizeof(s));
   s.piece = round_up(up(h.V, pieces), 256);
   s.pieces = up(h.V, s.piece);
-  const int64_t rows = round_up(h.M, 64), k_tiles = up(h.K, Large::kBN), p = s.piece;
-  s.dx_splits = h.dx ? splits_for(up(h.M, Large::kBM) * k_tiles, p / 64) : 1;
-  s.dw_splits = h.dw ? splits_for(p / Large::kBM * k_tiles, (h.f32 ? 2 : 1) * rows / 64) : 1;
+  const int64_t rows = round_up(h.M, 64), p = s.piece;
+  s.dx_splits = splits_for(h.M, h.K, p / 64, s.pieces > 1);
+  s.dw_splits = splits_for(p, h.K, (h.f32 ? 2 : 1) * rows / 64, false);
   s.header = c.take<Header>(sizeof(Header));
   s.list = c.take<int32_t>(4 * h.M);
   s.place = c.take<int32_t>(4 * h.M);
@@ -712,8 +793,8 @@ GradSpace grad_space_of(void* base, const GradShape& h, int64_t pieces) {
   s.g = c.take<uint16_t>(2 * rows * p);
   if (h.dw && h.f32) s.g_rest = c.take<uint16_t>(2 * rows * p);
   if (h.fp8 && h.dx) s.w_bf16 = c.take<uint16_t>(2 * p * h.K);
-  if (h.dx && (s.pieces > 1 || s.dx_splits > 1)) s.dx_sum = c.take<float>(4 * s.dx_splits * h.M * h.K);
-  if (h.dw && s.dw_splits > 1) s.dw_sum = c.take<float>(4 * s.dw_splits * p * h.K);
+  if (h.dx && s.dx_splits.room > 0) s.dx_sum = c.take<float>(4 * s.dx_splits.room * h.K);
+  if (h.dw && s.dw_splits.room > 0) s.dw_sum = c.take<float>(4 * s.dw_splits.room * h.K);
   s.bytes = c.used;
   return s;
 }
@@ -780,12 +861,14 @@ hipError_t launch_logits(LogitParams& p, bool fp8, hipStream_t stream) {
 template <bool kGT>
 hipError_t launch_product(ProductParams& p, hipStream_t stream) {
   p.n_tiles = (uint32_t)up(p.N, Large::kBN);
-  const int64_t tiles = up(p.M, Large::kBM) * p.n_tiles;
-  return launch(reinterpret_cast<const void*>(&product_kernel<kGT>), p.splits > 1 ? tiles * p.splits : tiles + kUnits / 2,
-                Large::kThreads, &p, stream);
+  // (parts times tiles are at most kUnits)
+  const int64_t tiles = up(p.M, Large::kBM) * p.n_tiles + kUnits / 2;
+  return launch(reinterpret_cast<const void*>(&product_kernel<kGT>), tiles > kUnits ? tiles : kUnits, Large::kThreads, &p,
+                stream);
 }
 
 hipError_t launch_finish(FinishParams& p, hipStream_t stream) {
+  p.n_tiles = (uint32_t)up(p.N, Large::kBN);
   return launch(reinterpret_cast<const void*>(&finish_kernel), up(p.M * (p.N / 4), 256), 256, &p, stream);
 }
 
@@ -972,13 +1055,14 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.list = s.list;
       p.out = a->dx;
       p.partial = s.dx_sum;
-      p.M = p.partial_rows = M;
+      p.M = M;
       p.N = K;
       p.lda = (uint32_t)(2 * ld);
       p.ldb = (uint32_t)(2 * K);
       p.k_rows = (int32_t)rows;
       p.splits = s.dx_splits;
-      p.mode = s.dx_sum ? (n > 0 ? kF32Add : kF32) : kBF16;
+      p.mode = kBF16;
+      p.add = n > 0;
       p.scale = a->weight_scale * a->logit_scale;
       if (e == hipSuccess) e = launch_product<false>(p, stream);
     }
@@ -994,12 +1078,11 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.out = dst;
       p.partial = s.dw_sum;
       p.M = rows;
-      p.partial_rows = s.piece;
       p.N = K;
       p.lda = (uint32_t)(2 * ld);
       p.ldb = (uint32_t)(2 * K);
       p.splits = s.dw_splits;
-      p.mode = s.dw_sum ? (int)kF32 : out;
+      p.mode = out;
       p.scale = a->x_scale * a->logit_scale;
       e = launch_product<true>(p, stream);
       if (e == hipSuccess && s.dw_sum) {
@@ -1010,7 +1093,6 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
         f.out = dst;
         f.M = rows;
         f.N = K;
-        f.partial_rows = s.piece;
         f.splits = s.dw_splits;
         f.mode = out;
         f.scale = p.scale;
@@ -1025,7 +1107,7 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
     f.header = s.header;
     f.list = s.list;
     f.out = a->dx;
-    f.M = f.partial_rows = M;
+    f.M = M;
     f.N = K;
     f.splits = s.dx_splits;
     f.mode = kBF16;
