@@ -750,7 +750,7 @@ Splits splits_for(int64_t rows, int64_t cols, int64_t steps, bool always) {
   s.most = (int32_t)(by_steps < by_tiles ? by_steps : by_tiles);
   s.always = always;
   s.room = 0;
-  if (s.most > 1 && up(rows, Large::kBM) * n_tiles <= 2 * kUnits) {
+  if (s.most > 1 && up(rows, Large::kBM) * n_tiles <= kUnits) {
     const int64_t all = Large::kBM * kUnits / n_tiles;
     s.room = s.most * rows < all ? s.most * rows : all;
   }

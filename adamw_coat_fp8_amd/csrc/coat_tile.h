@@ -245,8 +245,10 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
       mma1(1, n);
 #pragma unroll
       for (int r = n * kR / kMF; r < (n + 1) * kR / kMF; ++r) read1(0, An, Bn, 0, r);
+      // (two at a time: the sooner they go out, the longer they have)
 #pragma unroll
-      for (int q = n * kL / kMF; q < (n + 1) * kL / kMF; ++q) load1(next, S, q);
+      for (int q = 2 * n; q < 2 * n + 2; ++q)
+        if (q < kL) load1(next, S, q);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
