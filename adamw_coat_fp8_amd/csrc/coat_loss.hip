@@ -352,61 +352,62 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
       const int64_t at = t - col0;
       const bool mine = t >= 0 && t < p.V && at >= 0 && at < 32 * T::kJ && ((at >> 2) & 1) == half;
       if (__any(mine)) {
-        float v = 0.0f;
-#pragma unroll
-        for (int j = 0; j < T::kJ; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (32 * j + 8 * (r / 4) + 4 * half + r % 4 == (int)at) v = acc[i][j][r];
+        const float v = value_at<T>(acc, i, (int)at);
         if (mine) p.at_target[row] = v * p.scale2;
       }
     }
   } else {
     const int64_t padded = (live + 63) / 64 * 64;   // rows of g that the products read
+    RowInfo f[T::kI];
 #pragma unroll
     for (int i = 0; i < T::kI; ++i) {
       const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
-      RowInfo f = {0.0f, 0.0f, 0.0f, -1};
-      if (row < live) f = p.info[row];
-#pragma unroll
-      for (int j = 0; j < T::kJ; ++j)
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          acc[i][j][r] = f.coef * __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], p.scale2, -f.lse2));
-      const int64_t at = (int64_t)f.target - p.v0 - col0;
-      const bool mine = f.target >= 0 && at >= 0 && at < 32 * T::kJ && ((at >> 2) & 1) == half;
-      if (__any(mine)) {
-#pragma unroll
-        for (int j = 0; j < T::kJ; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (mine && 32 * j + 8 * (r / 4) + 4 * half + r % 4 == (int)at) acc[i][j][r] -= f.d;
-      }
-      if (valid < 32 * T::kJ || m0 + 32 * (T::kI * wm + i) + 32 > live) {
-#pragma unroll
-        for (int j = 0; j < T::kJ; ++j)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (row >= live || 32 * j + 8 * (r / 4) + 4 * half + r % 4 >= valid) acc[i][j][r] = 0.0f;
-      }
+      f[i] = row < live ? p.info[row] : RowInfo{0.0f, 0.0f, 0.0f, -1};
     }
-    auto store = [&](uint16_t* g) __attribute__((always_inline)) {
-      return [&, g](int row, int c, uint4 v) __attribute__((always_inline)) {
-        if (m0 + row < padded && n0 + 8 * c < p.ld) *reinterpret_cast<uint4*>(g + (m0 + row) * p.ld + n0 + 8 * c) = v;
-      };
+    auto share = [&](int i, float product) __attribute__((always_inline)) {
+      return f[i].coef * __builtin_amdgcn_exp2f(__builtin_fmaf(product, p.scale2, -f[i].lse2));
     };
-    tile_out_bf16<T>([&](int i, int j, int q) __attribute__((always_inline)) {
-      return make_uint2(bf16_pack2(acc[i][j][4 * q], acc[i][j][4 * q + 1]), bf16_pack2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
-    }, store(p.g));
+    // kRest: what BF16 leaves of the value
+    auto pair = [](float a, float b, auto kRest) __attribute__((always_inline)) {
+      const uint32_t w = bf16_pack2(a, b);
+      if constexpr (!decltype(kRest)::value) return w;
+      return bf16_pack2(a - bf16_lo(w), b - bf16_hi(w));
+    };
+    auto write = [&](uint16_t* g, auto kRest) __attribute__((always_inline)) {
+      tile_out_bf16<T>(
+          [&](int i, int j, int q) __attribute__((always_inline)) {
+            const float v0 = share(i, acc[i][j][4 * q]), v1 = share(i, acc[i][j][4 * q + 1]);
+            const float v2 = share(i, acc[i][j][4 * q + 2]), v3 = share(i, acc[i][j][4 * q + 3]);
+            return make_uint2(pair(v0, v1, kRest), pair(v2, v3, kRest));
+          },
+          // rows and columns past the last are zero
+          [&](int row, int c, uint4 v) __attribute__((always_inline)) {
+            const int64_t m = m0 + row, n = n0 + 8 * c;
+            if (m >= padded || n >= p.ld) return;
+            const int64_t left = m < live ? p.N - n : 0;
+            if (left < 8) {
+              auto keep = [&](int at, uint32_t w) { return left > at + 1 ? w : left > at ? w & 0xFFFFu : 0u; };
+              v = make_uint4(keep(0, v.x), keep(2, v.y), keep(4, v.z), keep(6, v.w));
+            }
+            store_stream16(g + m * p.ld + n, v);
+          },
+          // the target's value, where it lies in the lane's columns
+          [&](int i, auto set) __attribute__((always_inline)) {
+            const int64_t at = (int64_t)f[i].target - p.v0 - col0;
+            const bool mine = f[i].target >= 0 && at >= 0 && at < 32 * T::kJ && ((at >> 2) & 1) == half;
+            if (!__any(mine)) return;
+            const float product = value_at<T>(acc, i, (int)at);
+            if (mine) set((int)at + 32 * T::kJ * wn, pair(share(i, product) - f[i].d, 0.0f, kRest) & 0xFFFFu);
+          });
+    };
+    write(p.g, std::false_type{});
     if (p.g_rest) {
       __syncthreads();
-      auto rest2 = [](float a, float b) __attribute__((always_inline)) {
-        const uint32_t w = bf16_pack2(a, b);
-        return bf16_pack2(a - bf16_lo(w), b - bf16_hi(w));
-      };
-      tile_out_bf16<T>([&](int i, int j, int q) __attribute__((always_inline)) {
-        return make_uint2(rest2(acc[i][j][4 * q], acc[i][j][4 * q + 1]), rest2(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]));
-      }, store(p.g_rest));
+      // (values are formed again: kept since the first pass they would not fit
+      // the registers)
+#pragma unroll
+      for (int i = 0; i < T::kI; ++i) asm volatile("" : "+v"(f[i].lse2));
+      write(p.g_rest, std::true_type{});
     }
   }
 }

@@ -217,6 +217,7 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
                (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
   };
   constexpr int kTiles = kI * kJ, kMF = kFP8 ? kTiles : 2 * kTiles;
+  constexpr int kRF = kMF - kMF / 8;   // MFMAs that reads go out behind
   auto mma1 = [&](int f, int n) __attribute__((always_inline)) {
     const int i = n % kTiles / kJ, j = n % kJ, e = n / kTiles;
     if constexpr (kFP8)
@@ -234,7 +235,8 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
     for (int n = 0; n < kMF; ++n) {
       mma1(0, n);
 #pragma unroll
-      for (int r = n * kR / kMF; r < (n + 1) * kR / kMF; ++r) read1(1, As, Bs, 1, r);
+      for (int r = n * kR / kRF; r < (n + 1) * kR / kRF; ++r)
+        if (r < kR) read1(1, As, Bs, 1, r);
       __builtin_amdgcn_sched_barrier(0);
     }
     const From next = from(step + 2);
@@ -244,7 +246,8 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
     for (int n = 0; n < kMF; ++n) {
       mma1(1, n);
 #pragma unroll
-      for (int r = n * kR / kMF; r < (n + 1) * kR / kMF; ++r) read1(0, An, Bn, 0, r);
+      for (int r = n * kR / kRF; r < (n + 1) * kR / kRF; ++r)
+        if (r < kR) read1(0, An, Bn, 0, r);
       // (two at a time: the sooner they go out, the longer they have)
 #pragma unroll
       for (int q = 2 * n; q < 2 * n + 2; ++q)
@@ -382,11 +385,13 @@ __device__ __forceinline__ void mma_stream(v16f (&acc)[T::kI][T::kJ], int steps,
 // A BF16 tile through the LDS, so that it leaves in whole 16-byte chunks of
 // rows.  word(i, j, q) gives the four values of a run, packed; out(row, chunk,
 // bytes) takes chunk `chunk` (8 columns) of row `row` of the tile.  The block
-// must have met before and meets inside.  Chunks are XORed with row % 16 (or
+// must have met before and meets inside; patch(i, set) may replace single
+// values of the lane's row of tile i before it does, by set(column, bits).
+// Chunks are XORed with row % 16 (or
 // the chunks of a shorter row): 8-byte writes of 32 rows and 16-byte reads
 // meet no bank conflicts.
-template <class T, class Word, class Out>
-__device__ __forceinline__ void tile_out_bf16(Word word, Out out) {
+template <class T, class Word, class Out, class Patch>
+__device__ __forceinline__ void tile_out_bf16(Word word, Out out, Patch patch) {
   constexpr int kRowBytes = 2 * T::kBN, kChunks = kRowBytes / 16, kMask = (kChunks < 16 ? kChunks : 16) - 1;
   constexpr int kPart = mma_part_bytes<T>(0), kRows = kPart / kRowBytes / 32 * 32;   // rows of an LDS array
   static_assert(kRows >= 32 && kRows * 4 >= T::kBM && mma_part_bytes<T>(1) >= kPart, "the tile fits the arrays");
@@ -403,8 +408,13 @@ __device__ __forceinline__ void tile_out_bf16(Word word, Out out) {
 #pragma unroll
     for (int j = 0; j < T::kJ; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
+      for (int q = 0; q < 4; ++q) {
         *reinterpret_cast<uint2*>(tile + at(row, 4 * (T::kJ * wn + j) + q) + 8 * half) = word(i, j, q);
+        if (q % 2) __builtin_amdgcn_sched_barrier(0);   // (or every word is begun before one is stored)
+      }
+    patch(i, [&](int col, uint32_t bits) __attribute__((always_inline)) {
+      *reinterpret_cast<uint16_t*>(tile + at(row, col >> 3) + 2 * (col & 7)) = (uint16_t)bits;
+    });
   }
   __syncthreads();
 #pragma unroll
@@ -412,6 +422,43 @@ __device__ __forceinline__ void tile_out_bf16(Word word, Out out) {
     const int task = k * T::kThreads + threadIdx.x, row = task / kChunks, c = task % kChunks;
     out(row, c, *reinterpret_cast<const uint4*>(part(row / kRows) + at(row, c)));
   }
+}
+
+// The value at column `col` (of the wave's 32 kJ, in the lane's half) of the
+// lane's row of tile i: a tree of selections by the column's bits, each a
+// mask.  (Of conditions the compiler makes searches through whole vectors.)
+template <class T>
+__device__ __forceinline__ float value_at(const v16f (&acc)[T::kI][T::kJ], int i, int col) {
+  static_assert(T::kJ == 1 || T::kJ == 2 || T::kJ == 4, "a power of two");
+  uint32_t mask[6];
+  constexpr int kBit[6] = {0, 1, 3, 4, 5, 6};
+#pragma unroll
+  for (int b = 0; b < 6; ++b) {
+    mask[b] = 0u - (uint32_t)((col >> kBit[b]) & 1);
+    asm volatile("" : "+v"(mask[b]));
+  }
+  auto pick = [&](int b, uint32_t zero, uint32_t one) __attribute__((always_inline)) {
+    return (one & mask[b]) | (zero & ~mask[b]);
+  };
+  uint32_t of_j[T::kJ];
+#pragma unroll
+  for (int j = 0; j < T::kJ; ++j) {
+    uint32_t of_q[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      auto bits = [&](int e) __attribute__((always_inline)) { return __float_as_uint(acc[i][j][4 * q + e]); };
+      of_q[q] = pick(1, pick(0, bits(0), bits(1)), pick(0, bits(2), bits(3)));
+    }
+    of_j[j] = pick(3, pick(2, of_q[0], of_q[1]), pick(2, of_q[2], of_q[3]));
+  }
+  if constexpr (T::kJ == 4) return __uint_as_float(pick(5, pick(4, of_j[0], of_j[1]), pick(4, of_j[2], of_j[3])));
+  if constexpr (T::kJ == 2) return __uint_as_float(pick(4, of_j[0], of_j[1]));
+  return __uint_as_float(of_j[0]);
+}
+
+template <class T, class Word, class Out>
+__device__ __forceinline__ void tile_out_bf16(Word word, Out out) {
+  tile_out_bf16<T>(word, out, [](int, auto) {});
 }
 
 // xcd_contiguous for 32-bit indexes.
