@@ -40,6 +40,9 @@ using Half = MmaTile<2, 4, 2, 2, Large::kA>;    // 128 x 256, eight waves of 64 
 template <int kI>
 using Thin = MmaTile<1, 2, kI, 1, 0, 5>;        // 32 kI x 64, two waves, five stages
 constexpr int kThinCols = 64, kThinStrip = 32;
+using Small = MmaTile<2, 2, 2, 2>;              // 128 x 128, four waves of 64 x 64
+using ThinDx = MmaTile<1, 4, 4, 1>;             // 128 x 128, four waves of 128 x 32
+constexpr int64_t kThinRows = 64, kFewRows = 128, kSmallSteps = 8;
 
 constexpr int kStrip = 128;       // columns of a partial softmax, but for thin tiles
 constexpr int kGroupM = 4;        // tile rows that are walked together
@@ -82,6 +85,16 @@ struct PrepParams {
   int64_t M, V;
   float z;
 };
+
+__device__ __forceinline__ RowInfo row_info(const PrepParams& p, int64_t r, float d_max) {
+  const float lse = p.lse[r];
+  RowInfo f;
+  f.lse2 = lse * kLog2e;
+  f.d = p.d_loss[r] / d_max;
+  f.coef = f.d * __builtin_fmaf(2.0f * p.z, lse, 1.0f);
+  f.target = (int32_t)p.targets[r];
+  return f;
+}
 
 // One block: a running count over 8192 rows at a time, in order.
 __global__ __launch_bounds__(1024) void prep_kernel(const PrepParams p) {
@@ -140,13 +153,7 @@ __global__ __launch_bounds__(1024) void prep_kernel(const PrepParams p) {
   for (int64_t r = t; r < p.M; r += 1024) {
     const int32_t at = p.place[r];
     if (at < 0) continue;
-    RowInfo f;
-    const float lse = p.lse[r];
-    f.lse2 = lse * kLog2e;
-    f.d = p.d_loss[r] / d_max;
-    f.coef = f.d * __builtin_fmaf(2.0f * p.z, lse, 1.0f);
-    f.target = (int32_t)p.targets[r];
-    p.info[at] = f;
+    p.info[at] = row_info(p, r, d_max);
   }
 }
 
@@ -166,11 +173,10 @@ __device__ __forceinline__ uint4 bf16_of_codes(uint2 c) {
   return pack8(f);
 }
 
-// Row blockIdx.x into its place in the list, codes as BF16 (exact) and as
+// Row r of x into its place `at` in the list, codes as BF16 (exact) and as
 // they are.
-__global__ __launch_bounds__(256) void gather_kernel(const GatherParams p) {
-  const int64_t r = blockIdx.x, chunks = p.K / 8;
-  const int32_t at = p.place[r];
+__device__ __forceinline__ void gather_row(const GatherParams& p, int64_t r, int at) {
+  const int64_t chunks = p.K / 8;
   if (at < 0) {
     if (p.dx)
       for (int64_t c = threadIdx.x; c < chunks; c += 256)
@@ -186,6 +192,33 @@ __global__ __launch_bounds__(256) void gather_kernel(const GatherParams p) {
       *reinterpret_cast<uint4*>(p.x_bf16 + at * p.K + 8 * c) = load_stream16(p.x + 2 * (r * p.K + 8 * c));
     }
   }
+}
+
+__global__ __launch_bounds__(256) void gather_kernel(const GatherParams p) {
+  gather_row(p, blockIdx.x, p.place[blockIdx.x]);
+}
+
+// Both for at most 64 rows, a block each.
+__global__ __launch_bounds__(256) void prep_few_kernel(const PrepParams p, const GatherParams g) {
+  const int64_t r = blockIdx.x;
+  const int lane = threadIdx.x & 63;
+  const int64_t target = lane < p.M ? p.targets[lane] : -1;
+  const bool live = target >= 0 && target < p.V;
+  const uint64_t lives = __ballot(live);
+  float top = live ? fabsf(p.d_loss[lane]) : 0.0f;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+  const float d_max = top > 0.0f && top <= FLT_MAX ? top : 1.0f;
+  if (r == 0 && threadIdx.x == 0) {
+    p.header->live = __popcll(lives);
+    p.header->d_max = d_max;
+  }
+  const int at = (lives >> r) & 1 ? __popcll(lives & (((uint64_t)1 << r) - 1)) : -1;
+  if (at >= 0 && threadIdx.x == 0) {
+    p.list[at] = (int32_t)r;
+    p.info[at] = row_info(p, r, d_max);
+  }
+  gather_row(g, r, at);
 }
 
 // E4M3 codes as BF16, exactly; eight a thread.
@@ -423,6 +456,14 @@ __global__ __launch_bounds__(Large::kThreads) void logit_large_kernel(const Logi
   else if (t.m0 < live) logit_tile<Half, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
 }
 
+// At most 128 rows.
+template <bool kFP8, bool kGrad>
+__global__ __launch_bounds__(Small::kThreads) void logit_small_kernel(const LogitParams p) {
+  const int64_t live = p.header ? p.header->live : p.M;
+  if (live == 0) return;
+  logit_tile<Small, kFP8, kGrad>(p, live, 0, (int64_t)xcd_contiguous32(blockIdx.x, gridDim.x) * Small::kBN);
+}
+
 // At most 32 kI rows.
 template <bool kFP8, bool kGrad, int kI>
 __global__ __launch_bounds__(128) void logit_thin_kernel(const LogitParams p) {
@@ -524,10 +565,11 @@ struct Splits {
   int32_t most;        // by the steps: eight to a part at least
   int32_t always;      // partial sums even of one part (joined over pieces)
   int64_t room;        // rows that the partial sums have room for
-  __host__ __device__ int32_t parts(int64_t rows, uint32_t n_tiles) const {
-    const int64_t tiles = (rows + Large::kBM - 1) / Large::kBM * n_tiles;
-    if (tiles == 0 || tiles > kUnits / 2) return 1;
-    int64_t s = kUnits / tiles;
+  int32_t tile_rows, n_tiles, blocks;   // of the tiles; blocks that fill the device
+  __host__ __device__ int32_t parts(int64_t rows) const {
+    const int64_t tiles = (rows + tile_rows - 1) / tile_rows * n_tiles;
+    if (tiles == 0 || tiles > blocks / 2) return 1;
+    int64_t s = blocks / tiles;
     s = s < most ? s : most;
     s = s < room / rows ? s : room / rows;
     return (int32_t)(s < 1 ? 1 : s);
@@ -624,7 +666,7 @@ __device__ __forceinline__ void product_tile(const ProductParams& p, const int64
 template <bool kGT>
 __global__ __launch_bounds__(Large::kThreads) void product_kernel(const ProductParams p) {
   const int64_t live = p.header->live, M = kGT ? p.M : live;
-  const int parts = p.splits.parts(M, p.n_tiles);
+  const int parts = p.splits.parts(M);
   TileAt t;
   if (parts > 1) {
     const uint32_t m_tiles = (uint32_t)((M + Large::kBM - 1) / Large::kBM), tiles = m_tiles * p.n_tiles;
@@ -640,6 +682,68 @@ __global__ __launch_bounds__(Large::kThreads) void product_kernel(const ProductP
   else if (t.m0 < M) product_tile<Half, kGT>(p, live, t.m0, (int64_t)t.tn * Large::kBN, 0, 1);
 }
 
+// g^T x with few steps to a tile: small tiles, two blocks to a compute unit,
+// so that one's loads and stores run beside the other's.
+__global__ __launch_bounds__(Small::kThreads) void product_small_kernel(const ProductParams p) {
+  const uint32_t n_tiles = (uint32_t)((p.N + Small::kBN - 1) / Small::kBN), m_tiles = (uint32_t)((p.M + Small::kBM - 1) / Small::kBM);
+  uint32_t tm, tn;
+  tile_at(xcd_contiguous32(blockIdx.x, m_tiles * n_tiles), m_tiles, n_tiles, tm, tn);
+  product_tile<Small, true>(p, p.header->live, (int64_t)tm * Small::kBM, (int64_t)tn * Small::kBN, 0, 1);
+}
+
+// g W for at most 64 rows: g's two parts are rows 0 to 63 and 64 to 127 of a
+// tile, and are added where they meet, in the registers.
+__global__ __launch_bounds__(ThinDx::kThreads) void product_thin_kernel(const ProductParams p) {
+  using T = ThinDx;
+  const int64_t live = p.header->live;
+  const int parts = p.splits.parts(live);
+  const uint32_t blocks = (uint32_t)(p.splits.n_tiles * parts);
+  if (live == 0 || blockIdx.x >= blocks) return;
+  const uint32_t order = xcd_contiguous32(blockIdx.x, blocks), part = order / p.splits.n_tiles;
+  const int64_t n0 = (int64_t)(order - part * p.splits.n_tiles) * T::kBN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = lane >> 5, l32 = lane & 31;
+  const int all = (p.k_rows + 63) / 64;
+  const int first = (int)((int64_t)all * part / parts), last = (int)((int64_t)all * (part + 1) / parts);
+  uint32_t aoff[T::kLA], boff[T::kLB], blast[T::kLB];
+  minor_offsets(wave, lane, [&](int r) __attribute__((always_inline)) { return (uint32_t)r * p.lda; }, aoff);
+  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, p.N - n0, 64, boff);
+  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, p.N - n0, p.k_rows - 64 * (all - 1), blast);
+  v16f acc[T::kI][T::kJ];
+  mma_zero<T>(acc);
+  const uint8_t* b0 = p.b + 2 * n0;
+  const int64_t b_step = 64 * (int64_t)p.ldb;
+  mma_run<T, false, false, true>(acc, last - first, [&](int s) { return p.a + 128 * (int64_t)(first + s); }, aoff,
+                                 [&](int s) { return b0 + (first + s) * b_step; }, boff, blast,
+                                 [&](int s) { return first + s == all - 1; });
+  const bool partial = parts > 1 || p.splits.always;
+  const float scale = p.scale * p.header->d_max;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t row = 32 * i + l32;
+    if (row >= live) continue;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t col = n0 + 32 * wave + 8 * q + 4 * half;
+      if (col >= p.N) continue;
+      float4 v;
+      v.x = acc[i][0][4 * q] + acc[i + 2][0][4 * q], v.y = acc[i][0][4 * q + 1] + acc[i + 2][0][4 * q + 1];
+      v.z = acc[i][0][4 * q + 2] + acc[i + 2][0][4 * q + 2], v.w = acc[i][0][4 * q + 3] + acc[i + 2][0][4 * q + 3];
+      if (partial) {
+        float4* dst = reinterpret_cast<float4*>(p.partial + (part * live + row) * p.N + col);
+        if (p.add) {
+          const float4 o = *dst;
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+        *dst = v;
+      } else {
+        *reinterpret_cast<uint2*>((uint16_t*)p.out + (int64_t)p.list[row] * p.N + col) =
+            make_uint2(bf16_pack2(v.x * scale, v.y * scale), bf16_pack2(v.z * scale, v.w * scale));
+      }
+    }
+  }
+}
+
 struct FinishParams {
   const float* partial;     // [split][row][N]
   const Header* header;
@@ -647,26 +751,41 @@ struct FinishParams {
   void* out;
   int64_t M, N;
   Splits splits;
-  uint32_t n_tiles;
   int32_t mode;
   float scale;
 };
 
-// Sums of the splits in order, scaled; four columns a thread.
+// Sums of the splits, scaled; four columns a thread, and with kBy > 1 every
+// kBy-th split a thread, joined in a fixed order.
+template <int kBy>
 __global__ __launch_bounds__(256) void finish_kernel(const FinishParams p) {
+  __shared__ float4 part[kBy][256 / kBy];
   const int64_t rows = p.list ? (int64_t)p.header->live : p.M, quads = p.N / 4;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, row = at / quads, col = 4 * (at - row * quads);
-  if (row >= rows) return;
-  const int parts = p.splits.parts(rows, p.n_tiles);
-  if (parts == 1 && !p.splits.always) return;   // the product wrote the result
-  const float scale = p.scale * p.header->d_max;
-  const float* src = p.partial + row * p.N + col;
-  float4 v = *reinterpret_cast<const float4*>(src);
-#pragma unroll 4
-  for (int s = 1; s < parts; ++s) {
-    const float4 o = *reinterpret_cast<const float4*>(src + s * rows * p.N);
-    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  const int parts = rows > 0 ? p.splits.parts(rows) : 1;
+  if (rows == 0 || (parts == 1 && !p.splits.always)) return;   // the product wrote the result
+  const int t = threadIdx.x % (256 / kBy), by = threadIdx.x / (256 / kBy);
+  const int64_t at = (int64_t)blockIdx.x * (256 / kBy) + t, row = at / quads, col = 4 * (at - row * quads);
+  float4 v = make_float4(0, 0, 0, 0);
+  if (row < rows) {
+    const float* src = p.partial + row * p.N + col;
+#pragma unroll 8
+    for (int s = by; s < parts; s += kBy) {
+      const float4 o = *reinterpret_cast<const float4*>(src + s * rows * p.N);
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
   }
+  if constexpr (kBy > 1) {
+    part[by][t] = v;
+    __syncthreads();
+    if (by > 0) return;
+#pragma unroll
+    for (int s = 1; s < kBy; ++s) {
+      const float4 o = part[s][t];
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+  }
+  if (row >= rows) return;
+  const float scale = p.scale * p.header->d_max;
   v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
   const int64_t to = (p.list ? (int64_t)p.list[row] : row) * p.N + col;
   if (p.mode == kBF16) {
@@ -690,8 +809,6 @@ __global__ __launch_bounds__(256) void zero_kernel(uint8_t* p, int64_t bytes) {
 // ------------------------------------------------------------------ host
 
 constexpr int64_t kMaxRows = 1 << 23, kMaxVocab = 1 << 22, kMaxCols = 1 << 16;   // (a launch has less than 2^32 threads)
-constexpr int64_t kThinRows = 64;
-
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return up(a, b) * b; }
 
@@ -727,32 +844,36 @@ LossSpace loss_space(void* base, int64_t M, int64_t V) {
   Cutter c{(uint8_t*)base};
   LossSpace s;
   memset(&s, 0, sizeof(s));
-  const bool thin = M <= kThinRows;
+  const bool thin = M <= kThinRows, few = M <= kFewRows;
   s.at_target = c.take<float>(4 * M);
-  if (!thin) {
+  if (!few) {
     s.header = c.take<Header>(sizeof(Header));
     s.list = c.take<int32_t>(4 * M);
     s.place = c.take<int32_t>(4 * M);
     s.target = c.take<int32_t>(4 * M);
   }
-  s.strips = (int32_t)(thin ? up(V, kThinCols) * (kThinCols / kThinStrip) : up(V, Large::kBN) * Large::kWN);
-  s.row_step = thin ? s.strips : 1;
-  s.strip_step = thin ? 1 : round_up(M, 16);
-  s.part = c.take<float2>(8 * (thin ? M : s.strip_step) * s.strips);
+  s.strips = (int32_t)(thin ? up(V, kThinCols) * (kThinCols / kThinStrip)
+                      : few ? up(V, kStrip) : up(V, Large::kBN) * (Large::kBN / kStrip));
+  s.row_step = few ? s.strips : 1;
+  s.strip_step = few ? 1 : round_up(M, 16);
+  s.part = c.take<float2>(8 * (few ? M : s.strip_step) * s.strips);
   s.bytes = c.used;
   return s;
 }
 
 // Splits of a product of up to `rows` rows and `cols` columns over `steps`.
 // room: rows that the parts of any number of rows take at most.
-Splits splits_for(int64_t rows, int64_t cols, int64_t steps, bool always) {
+Splits splits_for(int64_t rows, int64_t cols, int64_t steps, bool always, bool thin) {
   Splits s;
-  const int64_t n_tiles = up(cols, Large::kBN), by_steps = steps / 8, by_tiles = kUnits / n_tiles;
+  s.tile_rows = thin ? (int32_t)kThinRows : Large::kBM;
+  s.n_tiles = (int32_t)up(cols, thin ? ThinDx::kBN : Large::kBN);
+  s.blocks = (int32_t)(thin ? 2 * kUnits : kUnits);
+  const int64_t by_steps = steps / 8, by_tiles = s.blocks / s.n_tiles;
   s.most = (int32_t)(by_steps < by_tiles ? by_steps : by_tiles);
   s.always = always;
   s.room = 0;
-  if (s.most > 1 && up(rows, Large::kBM) * n_tiles <= kUnits) {
-    const int64_t all = Large::kBM * kUnits / n_tiles;
+  if (s.most > 1 && up(rows, s.tile_rows) * s.n_tiles <= s.blocks) {
+    const int64_t all = (int64_t)s.tile_rows * s.blocks / s.n_tiles;
     s.room = s.most * rows < all ? s.most * rows : all;
   }
   if (always && s.room < rows) s.room = rows;
@@ -765,7 +886,7 @@ struct GradSpace {
   RowInfo* info;
   uint16_t* x_bf16;
   uint8_t* x_codes;
-  uint16_t *g, *g_rest, *w_bf16;
+  uint16_t *g, *w_bf16;
   float *dx_sum, *dw_sum;
   int64_t pieces, piece, bytes;   // piece: vocabulary rows, a multiple of 256
   Splits dx_splits, dw_splits;
@@ -783,16 +904,16 @@ GradSpace grad_space_of(void* base, const GradShape& h, int64_t pieces) {
   s.piece = round_up(up(h.V, pieces), 256);
   s.pieces = up(h.V, s.piece);
   const int64_t rows = round_up(h.M, 64), p = s.piece;
-  s.dx_splits = splits_for(h.M, h.K, p / 64, s.pieces > 1);
-  s.dw_splits = splits_for(p, h.K, (h.f32 ? 2 : 1) * rows / 64, false);
+  const bool thin = h.M <= kThinRows, two = thin || h.f32;   // two: g in two parts
+  s.dx_splits = splits_for(h.M, h.K, p / 64, s.pieces > 1, thin);
+  s.dw_splits = splits_for(p, h.K, (two ? 2 : 1) * rows / 64, false, false);
   s.header = c.take<Header>(sizeof(Header));
   s.list = c.take<int32_t>(4 * h.M);
   s.place = c.take<int32_t>(4 * h.M);
   s.info = c.take<RowInfo>(sizeof(RowInfo) * h.M);
   if (!h.fp8 || h.dw) s.x_bf16 = c.take<uint16_t>(2 * h.M * h.K);
   if (h.fp8) s.x_codes = c.take<uint8_t>(h.M * h.K);
-  s.g = c.take<uint16_t>(2 * rows * p);
-  if (h.dw && h.f32) s.g_rest = c.take<uint16_t>(2 * rows * p);
+  s.g = c.take<uint16_t>((two ? 4 : 2) * rows * p);
   if (h.fp8 && h.dx) s.w_bf16 = c.take<uint16_t>(2 * p * h.K);
   if (h.dx && s.dx_splits.room > 0) s.dx_sum = c.take<float>(4 * s.dx_splits.room * h.K);
   if (h.dw && s.dw_splits.room > 0) s.dw_sum = c.take<float>(4 * s.dw_splits.room * h.K);
@@ -853,24 +974,36 @@ hipError_t launch_logits(LogitParams& p, bool fp8, hipStream_t stream) {
                          reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad, 2>)};
     return launch(fns[2 * fp8 + (p.M > 32)], up(p.N, kThinCols), 128, &p, stream);
   }
+  if (p.M <= kFewRows) {
+    const void* fn = fp8 ? reinterpret_cast<const void*>(&logit_small_kernel<true, kGrad>)
+                         : reinterpret_cast<const void*>(&logit_small_kernel<false, kGrad>);
+    return launch(fn, up(p.N, Small::kBN), Small::kThreads, &p, stream);
+  }
   const void* fn = fp8 ? reinterpret_cast<const void*>(&logit_large_kernel<true, kGrad>)
                        : reinterpret_cast<const void*>(&logit_large_kernel<false, kGrad>);
   p.n_tiles = (int32_t)up(p.N, Large::kBN);
   return launch(fn, up(p.M, Large::kBM) * p.n_tiles + kUnits / 2, Large::kThreads, &p, stream);
 }
 
-template <bool kGT>
-hipError_t launch_product(ProductParams& p, hipStream_t stream) {
+hipError_t launch_product(ProductParams& p, bool gt, int64_t rows, hipStream_t stream) {
+  if (!gt && rows <= kThinRows)
+    return launch(reinterpret_cast<const void*>(&product_thin_kernel),
+                  (int64_t)p.splits.n_tiles * (p.splits.most > 1 ? p.splits.most : 1), ThinDx::kThreads, &p, stream);
+  if (gt && p.splits.room == 0 && up(rows, 64) * (p.a_rest ? 2 : 1) <= kSmallSteps)
+    return launch(reinterpret_cast<const void*>(&product_small_kernel), up(p.M, Small::kBM) * up(p.N, Small::kBN),
+                  Small::kThreads, &p, stream);
   p.n_tiles = (uint32_t)up(p.N, Large::kBN);
   // (parts times tiles are at most kUnits)
   const int64_t tiles = up(p.M, Large::kBM) * p.n_tiles + kUnits / 2;
-  return launch(reinterpret_cast<const void*>(&product_kernel<kGT>), tiles > kUnits ? tiles : kUnits, Large::kThreads, &p,
-                stream);
+  const void* fn = gt ? reinterpret_cast<const void*>(&product_kernel<true>) : reinterpret_cast<const void*>(&product_kernel<false>);
+  return launch(fn, tiles > kUnits ? tiles : kUnits, Large::kThreads, &p, stream);
 }
 
-hipError_t launch_finish(FinishParams& p, hipStream_t stream) {
-  p.n_tiles = (uint32_t)up(p.N, Large::kBN);
-  return launch(reinterpret_cast<const void*>(&finish_kernel), up(p.M * (p.N / 4), 256), 256, &p, stream);
+// rows: at most.
+hipError_t launch_finish(FinishParams& p, int64_t rows, hipStream_t stream) {
+  if (rows <= kThinRows)
+    return launch(reinterpret_cast<const void*>(&finish_kernel<8>), up(rows * (p.N / 4), 32), 256, &p, stream);
+  return launch(reinterpret_cast<const void*>(&finish_kernel<1>), up(rows * (p.N / 4), 256), 256, &p, stream);
 }
 
 }  // namespace
@@ -1005,20 +1138,25 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
   q.M = M;
   q.V = V;
   q.z = a->z_loss;
-  hipError_t e = launch(reinterpret_cast<const void*>(&prep_kernel), 1, 1024, &q, stream);
-  if (e == hipSuccess) {
-    GatherParams g;
-    memset(&g, 0, sizeof(g));
-    g.x = x;
-    g.place = s.place;
-    g.x_bf16 = s.x_bf16;
-    g.x_codes = s.x_codes;
-    g.dx = a->dx;
-    g.K = K;
-    g.fp8 = fp8;
-    e = launch(reinterpret_cast<const void*>(&gather_kernel), M, 256, &g, stream);
+  GatherParams g;
+  memset(&g, 0, sizeof(g));
+  g.x = x;
+  g.place = s.place;
+  g.x_bf16 = s.x_bf16;
+  g.x_codes = s.x_codes;
+  g.dx = a->dx;
+  g.K = K;
+  g.fp8 = fp8;
+  hipError_t e;
+  if (M <= kThinRows) {
+    void* args[] = {&q, &g};
+    e = hipLaunchKernel(reinterpret_cast<const void*>(&prep_few_kernel), dim3((unsigned)M), dim3(256), args, 0, stream);
+  } else {
+    e = launch(reinterpret_cast<const void*>(&prep_kernel), 1, 1024, &q, stream);
+    if (e == hipSuccess) e = launch(reinterpret_cast<const void*>(&gather_kernel), M, 256, &g, stream);
   }
   const float scale = a->x_scale * a->weight_scale * a->logit_scale;
+  const bool thin = M <= kThinRows, two = thin || h.f32;
   for (int64_t n = 0; n < s.pieces && e == hipSuccess; ++n) {
     const int64_t v0 = n * s.piece, rows = V - v0 < s.piece ? V - v0 : s.piece, ld = round_up(rows, 64);
     const uint8_t* wp = w + v0 * K * (fp8 ? 1 : 2);
@@ -1037,7 +1175,7 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.ld = ld;
       p.info = s.info;
       p.g = s.g;
-      p.g_rest = s.g_rest;
+      p.g_rest = two ? s.g + round_up(M, 64) * ld : nullptr;
       p.v0 = (int32_t)v0;
       e = launch_logits<true>(p, fp8, stream);
     }
@@ -1065,7 +1203,7 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.mode = kBF16;
       p.add = n > 0;
       p.scale = a->weight_scale * a->logit_scale;
-      if (e == hipSuccess) e = launch_product<false>(p, stream);
+      if (e == hipSuccess) e = launch_product(p, false, M, stream);
     }
     if (e == hipSuccess && dw) {
       const int out = a->dw_bf16 ? kBF16 : a->accumulate ? kF32Add : kF32;
@@ -1073,7 +1211,7 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       ProductParams p;
       memset(&p, 0, sizeof(p));
       p.a = (const uint8_t*)s.g;
-      p.a_rest = (const uint8_t*)s.g_rest;
+      p.a_rest = two ? (const uint8_t*)(s.g + round_up(M, 64) * ld) : nullptr;
       p.b = (const uint8_t*)s.x_bf16;
       p.header = s.header;
       p.out = dst;
@@ -1085,7 +1223,7 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.splits = s.dw_splits;
       p.mode = out;
       p.scale = a->x_scale * a->logit_scale;
-      e = launch_product<true>(p, stream);
+      e = launch_product(p, true, M, stream);
       if (e == hipSuccess && s.dw_sum) {
         FinishParams f;
         memset(&f, 0, sizeof(f));
@@ -1097,7 +1235,7 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
         f.splits = s.dw_splits;
         f.mode = out;
         f.scale = p.scale;
-        e = launch_finish(f, stream);
+        e = launch_finish(f, rows, stream);
       }
     }
   }
@@ -1113,7 +1251,7 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
     f.splits = s.dx_splits;
     f.mode = kBF16;
     f.scale = a->weight_scale * a->logit_scale;
-    e = launch_finish(f, stream);
+    e = launch_finish(f, M, stream);
   }
   return e == hipSuccess ? COAT_OK : hip_fail(e);
 }

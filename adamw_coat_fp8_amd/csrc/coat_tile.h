@@ -265,8 +265,11 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
     const From f0 = from(0), f1 = from(1);
 #pragma unroll
     for (int q = 0; q < kL; ++q) load1(f0, S0{}, q);
+    if (steps == 1) __builtin_amdgcn_s_waitcnt(7 << 4 | 15 << 8);   // vmcnt(0)
+    else {
 #pragma unroll
-    for (int q = 0; q < kL; ++q) load1(f1, S1{}, q);
+      for (int q = 0; q < kL; ++q) load1(f1, S1{}, q);
+    }
   }
   __builtin_amdgcn_s_waitcnt(kStage1InFlight);
   __builtin_amdgcn_s_barrier();

@@ -1,0 +1,1121 @@
+// coat_loss.hip -- gfx950 softmax cross entropy from hidden states and the
+// output projection's weights, with its gradients, and its C ABI.
+
+#include <hip/hip_runtime.h>
+
+#include <float.h>
+#include <math.h>
+#include <stdint.h>
+#include <string.h>
+
+#include "coat_tile.h"
+
+using namespace coat;
+
+namespace {
+
+// With l = c x W^T (never stored) a row's loss is
+//   lse - l[t] + z lse^2,  lse = log sum over v of exp(l[v]),
+// and the gradient of l is
+//   g[v] = d ((1 + 2 z lse) exp(l[v] - lse) - [v = t]),  dx = c g W,  dW = c g^T x.
+//
+// Forward: one product whose tiles end in a maximum and a sum of exponentials
+// for each row and strip of columns (in powers of two), joined by a second
+// kernel.  Backward, for one piece of the vocabulary after the other: the
+// piece's logits again, whose tiles end in g as BF16; then g W and g^T x.
+//
+// Rows without a target take no part: the rows that have one are listed first
+// (prep_kernel), the products run over those alone, and the number of them
+// stays on the device, where blocks without work end at once.
+//
+// g is stored divided by the largest |d| of the call, which multiplies the
+// products' FP32 results: with one d for all rows, a mean's, the target's
+// value 1 - p of an unlikely target then lies near 1, where BF16 is exact, and
+// is not rounded alike in every row.
+
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
+using Large = MmaTile<2, 2, 4, 4>;              // 256 x 256, eight waves of 64 x 128
+using Half = MmaTile<2, 2, 2, 4, Large::kA>;    // 128 x 256, eight waves of 64 x 64
+template <int kI>
+using Thin = MmaTile<1, 2, kI, 1, 0, 5>;        // 32 kI x 64, two waves, five stages
+constexpr int kThinCols = 64, kThinStrip = 32;
+
+constexpr int kStrip = 128;       // columns of a partial softmax, but for thin tiles
+constexpr int kGroupM = 4;        // tile rows that are walked together
+constexpr int kUnits = 256;       // compute units of the device the plans are made for
+
+// What the backward pass needs of a row: log2(e) lse, the factor of
+// exp(l - lse), what the target's value is lowered by, the target.
+struct RowInfo {
+  float lse2, coef, d;
+  int32_t target;
+};
+
+struct Header {
+  int32_t live;   // rows that have a target
+  float d_max;    // what g was divided by
+  int32_t pad[14];
+};
+
+__device__ __forceinline__ float pair_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float pair_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ------------------------------------------------------ rows with a target
+
+struct PrepParams {
+  const int64_t* targets;
+  const float* d_loss;   // or NULL: no RowInfo
+  const float* lse;
+  Header* header;
+  int32_t* list;         // row of each listed one
+  int32_t* place;        // of each row in the list, or -1
+  int32_t* target;       // of each listed row, or NULL
+  RowInfo* info;         // of each listed row, or NULL
+  int64_t M, V;
+  float z;
+};
+
+// One block: a running count over 8192 rows at a time, in order.
+__global__ __launch_bounds__(1024) void prep_kernel(const PrepParams p) {
+  __shared__ int32_t wave_count[16];
+  __shared__ float wave_max[16];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  constexpr int kEach = 8;
+  int32_t base = 0;
+  float top = 0.0f;
+  for (int64_t first = 0; first < p.M; first += 1024 * kEach) {
+    const int64_t r0 = first + (int64_t)t * kEach;
+    int64_t target[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) target[e] = r0 + e < p.M ? p.targets[r0 + e] : -1;
+    int32_t mine = 0;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const bool live = target[e] >= 0 && target[e] < p.V;
+      mine += live;
+      if (live && p.d_loss) top = fmaxf(top, fabsf(p.d_loss[r0 + e]));
+    }
+    int32_t upto = mine;   // of the wave's lanes up to this one
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) {
+      const int32_t o = __shfl_up(upto, s);
+      if (lane >= s) upto += o;
+    }
+    if (lane == 63) wave_count[wave] = upto;
+    __syncthreads();
+    int32_t at = base + upto - mine;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) at += wave_count[w];
+      base += wave_count[w];
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      if (r0 + e >= p.M) continue;
+      const bool live = target[e] >= 0 && target[e] < p.V;
+      p.place[r0 + e] = live ? at : -1;
+      if (!live) continue;
+      p.list[at] = (int32_t)(r0 + e);
+      if (p.target) p.target[at] = (int32_t)target[e];
+      ++at;
+    }
+    __syncthreads();   // wave_count is read
+  }
+  if (t == 0) p.header->live = base;
+  if (!p.d_loss) return;
+#pragma unroll
+  for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+  if (lane == 0) wave_max[wave] = top;
+  __syncthreads();
+  for (int w = 0; w < 16; ++w) top = fmaxf(top, wave_max[w]);
+  const float d_max = top > 0.0f && top <= FLT_MAX ? top : 1.0f;
+  if (t == 0) p.header->d_max = d_max;
+  for (int64_t r = t; r < p.M; r += 1024) {
+    const int32_t at = p.place[r];
+    if (at < 0) continue;
+    RowInfo f;
+    const float lse = p.lse[r];
+    f.lse2 = lse * kLog2e;
+    f.d = p.d_loss[r] / d_max;
+    f.coef = f.d * __builtin_fmaf(2.0f * p.z, lse, 1.0f);
+    f.target = (int32_t)p.targets[r];
+    p.info[at] = f;
+  }
+}
+
+struct GatherParams {
+  const uint8_t* x;          // M x K BF16, or codes
+  const int32_t* place;
+  uint16_t* x_bf16;          // listed rows (written), or NULL
+  uint8_t* x_codes;          // or NULL
+  uint16_t* dx;              // zeros for rows without a target, or NULL
+  int64_t K;
+  int32_t fp8;
+};
+
+__device__ __forceinline__ uint4 bf16_of_codes(uint2 c) {
+  float f[8];
+  e4m3_values8(c, f);
+  return pack8(f);
+}
+
+// Row blockIdx.x into its place in the list, codes as BF16 (exact) and as
+// they are.
+__global__ __launch_bounds__(256) void gather_kernel(const GatherParams p) {
+  const int64_t r = blockIdx.x, chunks = p.K / 8;
+  const int32_t at = p.place[r];
+  if (at < 0) {
+    if (p.dx)
+      for (int64_t c = threadIdx.x; c < chunks; c += 256)
+        *reinterpret_cast<uint4*>(p.dx + r * p.K + 8 * c) = make_uint4(0, 0, 0, 0);
+    return;
+  }
+  for (int64_t c = threadIdx.x; c < chunks; c += 256) {
+    if (p.fp8) {
+      const uint2 v = load_stream8(p.x + r * p.K + 8 * c);
+      if (p.x_codes) *reinterpret_cast<uint2*>(p.x_codes + at * p.K + 8 * c) = v;
+      if (p.x_bf16) *reinterpret_cast<uint4*>(p.x_bf16 + at * p.K + 8 * c) = bf16_of_codes(v);
+    } else {
+      *reinterpret_cast<uint4*>(p.x_bf16 + at * p.K + 8 * c) = load_stream16(p.x + 2 * (r * p.K + 8 * c));
+    }
+  }
+}
+
+// E4M3 codes as BF16, exactly; eight a thread.
+__global__ __launch_bounds__(256) void expand_kernel(const uint8_t* codes, int64_t chunks, uint16_t* out) {
+  const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (c < chunks) *reinterpret_cast<uint4*>(out + 8 * c) = bf16_of_codes(load_stream8(codes + 8 * c));
+}
+
+// ---------------------------------------------------------------- logits
+
+struct LogitParams {
+  const uint8_t* x;         // rows of `stride` bytes; listed ones of them with list
+  const uint8_t* w;         // the piece's weights, N rows of `stride` bytes
+  const int32_t* list;      // or NULL: row m is row m
+  const Header* header;     // or NULL: M rows
+  int64_t M, N, V;
+  uint32_t stride;
+  int32_t steps, n_tiles;
+  float scale2;             // log2(e) times what a product is multiplied by
+  // loss
+  float2* part;             // largest logit and sum of exponentials of each strip and row
+  int64_t strip_step, row_step;
+  float* at_target;         // the target's logit of each row
+  const int32_t* target;    // of listed rows, or NULL
+  const int64_t* targets;
+  // gradient
+  const RowInfo* info;
+  uint16_t* g;              // rows of ld values
+  uint16_t* g_rest;         // what BF16 left of g, or NULL
+  int64_t ld;
+  int32_t v0;               // first vocabulary row of the piece
+};
+
+// Tile order: groups of kGroupM tile rows, column by column inside a group.
+__device__ __forceinline__ void tile_at(uint32_t order, uint32_t m_tiles, uint32_t n_tiles, uint32_t& tm, uint32_t& tn) {
+  const uint32_t group = order / (kGroupM * n_tiles), first = group * kGroupM;
+  const uint32_t rows = m_tiles - first < kGroupM ? m_tiles - first : kGroupM;
+  const uint32_t local = order - group * kGroupM * n_tiles;
+  tn = local / rows;
+  tm = first + local - tn * rows;
+}
+
+// How M rows are cut into tiles of n_tiles columns: 256 rows each, but 128 for
+// a last row of tiles that holds no more; and the last round of whole tiles in
+// halves, where that ends earlier.  In units of half a tile's time, whole
+// tiles first: keeping `rem` of them in the last round takes 2 units there and
+// leaves room for 2 (units - rem) halves.
+struct TilePlan {
+  uint32_t rows, whole, halves;   // whole rows of tiles; whole tiles; halves behind them: the last row's, then split ones
+  uint32_t last;                  // halves of the last row
+  __host__ __device__ TilePlan(int64_t M, uint32_t n_tiles) {
+    const uint32_t rest = (uint32_t)(M % Large::kBM);
+    rows = (uint32_t)(M / Large::kBM) + (rest > Half::kBM);
+    last = rest > 0 && rest <= Half::kBM ? n_tiles : 0;
+    whole = rows * n_tiles;
+    const uint32_t rem = whole % kUnits;
+    const uint32_t split = rem > 0 && last + 2 * rem <= kUnits ? rem : 0;
+    whole -= split;
+    halves = last + 2 * split;
+  }
+};
+
+// The tile of block b; false: none.
+struct TileAt {
+  int64_t m0;
+  uint32_t tn;
+  bool half;
+};
+
+__device__ __forceinline__ bool tile_of(uint32_t b, const TilePlan& p, uint32_t n_tiles, TileAt& t) {
+  uint32_t tm;
+  if (b < p.whole) {
+    tile_at(xcd_contiguous32(b, p.whole), p.rows, n_tiles, tm, t.tn);
+    t.m0 = (int64_t)tm * Large::kBM;
+    t.half = false;
+    return true;
+  }
+  if (b >= p.whole + p.halves) return false;
+  const uint32_t order = xcd_contiguous32(b - p.whole, p.halves);
+  t.half = true;
+  if (order < p.last) {
+    t.m0 = (int64_t)p.rows * Large::kBM;
+    t.tn = order;
+  } else {
+    tile_at(p.whole + ((order - p.last) >> 1), p.rows, n_tiles, tm, t.tn);
+    t.m0 = (int64_t)tm * Large::kBM + Half::kBM * ((order - p.last) & 1);
+  }
+  return true;
+}
+
+template <class T, bool kFP8, bool kGrad>
+__device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t live, const int64_t m0, const int64_t n0) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
+  // rows and columns past the last re-load it
+  uint32_t aoff[T::kLA], boff[T::kLB];
+  const uint8_t* a0 = p.list ? p.x : p.x + m0 * p.stride;
+  const uint8_t* b0 = p.w + n0 * p.stride;
+  minor_offsets(wave, lane, [&](int r) __attribute__((always_inline)) {
+    const int64_t m = m0 + r < live ? m0 + r : live - 1;
+    return p.list ? (uint32_t)p.list[m] * p.stride : (uint32_t)(m - m0) * p.stride;
+  }, aoff);
+  minor_offsets(wave, lane, [&](int r) __attribute__((always_inline)) {
+    return (uint32_t)(n0 + r < p.N ? r : (int)(p.N - 1 - n0)) * p.stride;
+  }, boff);
+  v16f acc[T::kI][T::kJ];
+  mma_zero<T>(acc);
+  if constexpr (T::kStages > 2)
+    mma_stream<T, kFP8>(acc, p.steps, a0, aoff, b0, boff);
+  else
+    mma_run<T, kFP8, false, false>(acc, p.steps, [&](int s) { return a0 + 128 * (int64_t)s; }, aoff,
+                                   [&](int s) { return b0 + 128 * (int64_t)s; }, boff, boff, [](int) { return false; });
+
+  const int64_t col0 = n0 + 32 * T::kJ * wn;          // the wave's first column
+  const int64_t valid = p.N - col0;                    // of its columns
+  if constexpr (!kGrad) {
+    if (valid < 32 * T::kJ) {
+#pragma unroll
+      for (int i = 0; i < T::kI; ++i)
+#pragma unroll
+        for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (32 * j + 8 * (r / 4) + 4 * half + r % 4 >= valid) acc[i][j][r] = -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < T::kI; ++i) {
+      const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
+      // (a NaN is left to the sum)
+      float top = -FLT_MAX;
+#pragma unroll
+      for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) top = fmaxf(fmaxf(top, acc[i][j][r]), acc[i][j][r + 1]);
+      top = fmaxf(pair_max(top) * p.scale2, -FLT_MAX);
+      float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          sum[r % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], p.scale2, -top));
+      float all = pair_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      const bool stored = row < live;
+      int strip = wn;
+      if constexpr (32 * T::kJ < kStrip && T::kStages == 2) {
+        // two waves share a strip: the odd one hands its part over
+        static_assert(64 * T::kJ == kStrip, "two waves");
+        float2* shared = reinterpret_cast<float2*>(mma_part<T, 0>()) + 32 * (T::kI * wm + i) + l32 + T::kBM * (wn >> 1);
+        if ((wn & 1) && half == 0) *shared = make_float2(top, all);
+        __syncthreads();
+        if (!(wn & 1)) {
+          const float2 o = *shared;
+          const float m = fmaxf(top, o.x);
+          all = all * __builtin_amdgcn_exp2f(top - m) + o.y * __builtin_amdgcn_exp2f(o.x - m);
+          top = m;
+        }
+        strip = wn & 1 ? -1 : wn >> 1;
+      }
+      if (stored && half == 0 && strip >= 0)
+        p.part[(n0 / (T::kStages == 2 ? kStrip : 32 * T::kJ) + strip) * p.strip_step + row * p.row_step] = make_float2(top, all);
+      // the target's logit, where it lies in the lane's columns
+      int64_t t = -1;
+      if (stored) t = p.target ? (int64_t)p.target[row] : p.targets[row];
+      const int64_t at = t - col0;
+      const bool mine = t >= 0 && t < p.V && at >= 0 && at < 32 * T::kJ && ((at >> 2) & 1) == half;
+      if (__any(mine)) {
+        const float v = value_at<T>(acc, i, (int)at);
+        if (mine) p.at_target[row] = v * p.scale2;
+      }
+    }
+  } else {
+    const int64_t padded = (live + 63) / 64 * 64;   // rows of g that the products read
+    RowInfo f[T::kI];
+#pragma unroll
+    for (int i = 0; i < T::kI; ++i) {
+      const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
+      f[i] = row < live ? p.info[row] : RowInfo{0.0f, 0.0f, 0.0f, -1};
+    }
+    auto share = [&](int i, float product) __attribute__((always_inline)) {
+      return f[i].coef * __builtin_amdgcn_exp2f(__builtin_fmaf(product, p.scale2, -f[i].lse2));
+    };
+    // kRest: what BF16 leaves of the value
+    auto pair = [](float a, float b, auto kRest) __attribute__((always_inline)) {
+      const uint32_t w = bf16_pack2(a, b);
+      if constexpr (!decltype(kRest)::value) return w;
+      return bf16_pack2(a - bf16_lo(w), b - bf16_hi(w));
+    };
+    auto write = [&](uint16_t* g, auto kRest) __attribute__((always_inline)) {
+      tile_out_bf16<T>(
+          [&](int i, int j, int q) __attribute__((always_inline)) {
+            const float v0 = share(i, acc[i][j][4 * q]), v1 = share(i, acc[i][j][4 * q + 1]);
+            const float v2 = share(i, acc[i][j][4 * q + 2]), v3 = share(i, acc[i][j][4 * q + 3]);
+            return make_uint2(pair(v0, v1, kRest), pair(v2, v3, kRest));
+          },
+          // rows and columns past the last are zero
+          [&](int row, int c, uint4 v) __attribute__((always_inline)) {
+            const int64_t m = m0 + row, n = n0 + 8 * c;
+            if (m >= padded || n >= p.ld) return;
+            const int64_t left = m < live ? p.N - n : 0;
+            if (left < 8) {
+              auto keep = [&](int at, uint32_t w) { return left > at + 1 ? w : left > at ? w & 0xFFFFu : 0u; };
+              v = make_uint4(keep(0, v.x), keep(2, v.y), keep(4, v.z), keep(6, v.w));
+            }
+            store_stream16(g + m * p.ld + n, v);
+          },
+          // the target's value, where it lies in the lane's columns
+          [&](int i, auto set) __attribute__((always_inline)) {
+            const int64_t at = (int64_t)f[i].target - p.v0 - col0;
+            const bool mine = f[i].target >= 0 && at >= 0 && at < 32 * T::kJ && ((at >> 2) & 1) == half;
+            if (!__any(mine)) return;
+            const float product = value_at<T>(acc, i, (int)at);
+            if (mine) set((int)at + 32 * T::kJ * wn, pair(share(i, product) - f[i].d, 0.0f, kRest) & 0xFFFFu);
+          });
+    };
+    write(p.g, std::false_type{});
+    if (p.g_rest) {
+      __syncthreads();
+      // (values are formed again: kept since the first pass they would not fit
+      // the registers)
+#pragma unroll
+      for (int i = 0; i < T::kI; ++i) asm volatile("" : "+v"(f[i].lse2));
+      write(p.g_rest, std::true_type{});
+    }
+  }
+}
+
+// The grid is that of all M rows; blocks past the last tile of the live ones
+// end.
+template <bool kFP8, bool kGrad>
+__global__ __launch_bounds__(Large::kThreads) void logit_large_kernel(const LogitParams p) {
+  const int64_t live = p.header ? p.header->live : p.M;
+  TileAt t;
+  if (!tile_of(blockIdx.x, TilePlan(live, (uint32_t)p.n_tiles), (uint32_t)p.n_tiles, t)) return;
+  if (!t.half) logit_tile<Large, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
+  else if (t.m0 < live) logit_tile<Half, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
+}
+
+// At most 32 kI rows.
+template <bool kFP8, bool kGrad, int kI>
+__global__ __launch_bounds__(128) void logit_thin_kernel(const LogitParams p) {
+  const int64_t live = p.header ? p.header->live : p.M;
+  if (live == 0) return;
+  logit_tile<Thin<kI>, kFP8, kGrad>(p, live, 0, (int64_t)xcd_contiguous32(blockIdx.x, gridDim.x) * kThinCols);
+}
+
+struct JoinParams {
+  const float2* part;
+  int64_t strip_step, row_step;
+  const float* at_target;
+  const int32_t* place;     // of each row in the list, or NULL
+  const int64_t* targets;
+  float* loss;
+  float* lse;               // or NULL
+  int64_t M, V;
+  int32_t strips;
+  float z;
+};
+
+// Joins strips g, g + kBy, .. of a row, eight loads in flight.
+template <int kBy>
+__device__ __forceinline__ float2 join_strips(const JoinParams& p, int64_t at, int g) {
+  const float2* part = p.part + at * p.row_step;
+  float top = -FLT_MAX, sum = 0.0f;
+  for (int s = g; s < p.strips; s += 8 * kBy) {
+    float2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = s + i * kBy < p.strips ? part[(s + i * kBy) * p.strip_step] : make_float2(-FLT_MAX, 0.0f);
+    float m = top;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, v[i].x);
+    sum *= __builtin_amdgcn_exp2f(top - m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += v[i].y * __builtin_amdgcn_exp2f(v[i].x - m);
+    top = m;
+  }
+  return make_float2(top, sum);
+}
+
+__device__ __forceinline__ void store_loss(const JoinParams& p, int64_t row, int64_t at, float top, float sum) {
+  float loss = 0.0f, lse = 0.0f;
+  if (at >= 0) {
+    const float log2s = __builtin_amdgcn_logf(sum);
+    lse = kLn2 * (top + log2s);
+    loss = kLn2 * ((top - p.at_target[at]) + log2s) + p.z * lse * lse;
+  }
+  p.loss[row] = loss;
+  if (p.lse) p.lse[row] = lse;
+}
+
+__device__ __forceinline__ int64_t place_of(const JoinParams& p, int64_t row) {
+  const int64_t target = p.targets[row];
+  if (target < 0 || target >= p.V) return -1;
+  return p.place ? p.place[row] : row;
+}
+
+// 16 rows, 16 threads each.
+__global__ __launch_bounds__(256) void loss_join_kernel(const JoinParams p) {
+  __shared__ float2 part[16][17];
+  const int t = threadIdx.x, r16 = t & 15, g = t >> 4;
+  const int64_t row = (int64_t)blockIdx.x * 16 + r16;
+  const int64_t at = row < p.M ? place_of(p, row) : -1;
+  part[r16][g] = at >= 0 ? join_strips<16>(p, at, g) : make_float2(-FLT_MAX, 0.0f);
+  __syncthreads();
+  if (t >= 16 || row >= p.M) return;
+  float top = -FLT_MAX, sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, part[r16][i].x);
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sum += part[r16][i].y * __builtin_amdgcn_exp2f(part[r16][i].x - top);
+  store_loss(p, row, at, top, sum);
+}
+
+// Few rows: a wave each.
+__global__ __launch_bounds__(64) void loss_join_few_kernel(const JoinParams p) {
+  const int64_t row = blockIdx.x, at = place_of(p, row);
+  float top = -FLT_MAX, sum = 0.0f;
+  if (at >= 0) {
+    const float2 v = join_strips<64>(p, at, threadIdx.x);
+    top = v.x;
+#pragma unroll
+    for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
+    sum = lanes_sum<64>(v.y * __builtin_amdgcn_exp2f(v.x - top));
+  }
+  if (threadIdx.x == 0) store_loss(p, row, at, top, sum);
+}
+
+// -------------------------------------------------- products with g
+
+enum Out { kBF16 = 0, kF32 = 1, kF32Add = 2 };
+
+// How a product's contraction is split where its tiles leave compute units
+// empty: into parts of partial sums.  A function of the rows (M, or the live
+// ones) alone, on the device too.
+struct Splits {
+  int32_t most;        // by the steps: eight to a part at least
+  int32_t always;      // partial sums even of one part (joined over pieces)
+  int64_t room;        // rows that the partial sums have room for
+  __host__ __device__ int32_t parts(int64_t rows, uint32_t n_tiles) const {
+    const int64_t tiles = (rows + Large::kBM - 1) / Large::kBM * n_tiles;
+    if (tiles == 0 || tiles > kUnits / 2) return 1;
+    int64_t s = kUnits / tiles;
+    s = s < most ? s : most;
+    s = s < room / rows ? s : room / rows;
+    return (int32_t)(s < 1 ? 1 : s);
+  }
+};
+
+struct ProductParams {
+  const uint8_t* a;         // g: rows of lda bytes
+  const uint8_t* a_rest;    // its second part, or NULL
+  const uint8_t* b;         // k rows of ldb bytes
+  const Header* header;
+  const int32_t* list;      // C's row m goes to row list[m], or NULL
+  void* out;                // BF16 or FP32, rows of N values
+  float* partial;           // FP32 sums, [split][row][N], or NULL
+  int64_t M, N;
+  Splits splits;
+  uint32_t lda, ldb;
+  int32_t k_rows;           // contracted rows of b; those of a are padded with zeros to a multiple of 64
+  int32_t mode;             // of out
+  int32_t add;              // the partial sums are added to
+  float scale;              // of out, times the header's d_max
+  uint32_t n_tiles;
+};
+
+// kGT: C = g^T x (A slow, the contracted rows are the live ones); else g W.
+template <class T, bool kGT>
+__device__ __forceinline__ void product_tile(const ProductParams& p, const int64_t live, const int64_t m0, const int64_t n0,
+                                             const int part, const int parts) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
+  const int64_t M = kGT ? p.M : live;
+  const int k_rows = kGT ? (int)live : p.k_rows;
+  const int each = (k_rows + 63) / 64, all = p.a_rest ? 2 * each : each;
+  const int first = (int)((int64_t)all * part / parts), last = (int)((int64_t)all * (part + 1) / parts);
+  uint32_t aoff[T::kLA], boff[T::kLB], blast[T::kLB];
+  const int64_t cols = p.N - n0;
+  if constexpr (kGT) {
+    slow_offsets<T::kLA, T::kBM>(wave, lane, p.lda, p.lda / 2 - m0, 64, aoff);
+  } else {
+    minor_offsets(wave, lane, [&](int r) __attribute__((always_inline)) {
+      return (uint32_t)(m0 + r < M ? r : (int)(M - 1 - m0)) * p.lda;
+    }, aoff);
+  }
+  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, cols, 64, boff);
+  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, cols, k_rows - 64 * (each - 1), blast);
+  v16f acc[T::kI][T::kJ];
+  mma_zero<T>(acc);
+  const uint8_t* a0 = kGT ? p.a + 2 * m0 : p.a + m0 * p.lda;
+  const uint8_t* a1 = kGT ? p.a_rest + 2 * m0 : p.a_rest + m0 * p.lda;
+  const uint8_t* b0 = p.b + 2 * n0;
+  const int64_t a_step = kGT ? 64 * (int64_t)p.lda : 128, b_step = 64 * (int64_t)p.ldb;
+  mma_run<T, false, kGT, true>(
+      acc, last - first,
+      [&](int s) { return first + s < each ? a0 + (first + s) * a_step : a1 + (first + s - each) * a_step; }, aoff,
+      [&](int s) { return b0 + (first + s < each ? first + s : first + s - each) * b_step; }, boff, blast,
+      [&](int s) { return first + s == each - 1 || first + s == 2 * each - 1; });
+  const bool partial = parts > 1 || p.splits.always;
+  if (partial || p.mode != kBF16) {
+    const float scale = partial ? 1.0f : p.scale * p.header->d_max;
+    const bool add = partial ? p.add : p.mode == kF32Add;
+    float* out = partial ? p.partial + part * M * p.N : (float*)p.out;
+#pragma unroll
+    for (int i = 0; i < T::kI; ++i) {
+      const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
+      if (row >= M) continue;
+#pragma unroll
+      for (int j = 0; j < T::kJ; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t col = n0 + 32 * (T::kJ * wn + j) + 8 * q + 4 * half;
+          if (col >= p.N) continue;
+          float4* dst = reinterpret_cast<float4*>(out + row * p.N + col);
+          float4 v = make_float4(acc[i][j][4 * q] * scale, acc[i][j][4 * q + 1] * scale, acc[i][j][4 * q + 2] * scale,
+                                 acc[i][j][4 * q + 3] * scale);
+          if (add) {
+            const float4 o = *dst;
+            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+          }
+          *dst = v;
+        }
+    }
+    return;
+  }
+  const float scale = p.scale * p.header->d_max;
+  tile_out_bf16<T>([&](int i, int j, int q) __attribute__((always_inline)) {
+    return make_uint2(bf16_pack2(acc[i][j][4 * q] * scale, acc[i][j][4 * q + 1] * scale),
+                      bf16_pack2(acc[i][j][4 * q + 2] * scale, acc[i][j][4 * q + 3] * scale));
+  }, [&](int row, int c, uint4 v) __attribute__((always_inline)) {
+    const int64_t m = m0 + row, n = n0 + 8 * c;
+    if (m < M && n < p.N) store_stream16((uint16_t*)p.out + (p.list ? (int64_t)p.list[m] : m) * p.N + n, v);
+  });
+}
+
+template <bool kGT>
+__global__ __launch_bounds__(Large::kThreads) void product_kernel(const ProductParams p) {
+  const int64_t live = p.header->live, M = kGT ? p.M : live;
+  const int parts = p.splits.parts(M, p.n_tiles);
+  TileAt t;
+  if (parts > 1) {
+    const uint32_t m_tiles = (uint32_t)((M + Large::kBM - 1) / Large::kBM), tiles = m_tiles * p.n_tiles;
+    if (blockIdx.x >= tiles * parts) return;
+    const uint32_t order = xcd_contiguous32(blockIdx.x, tiles * parts), part = order / tiles;
+    uint32_t tm;
+    tile_at(order - part * tiles, m_tiles, p.n_tiles, tm, t.tn);
+    product_tile<Large, kGT>(p, live, (int64_t)tm * Large::kBM, (int64_t)t.tn * Large::kBN, (int)part, parts);
+    return;
+  }
+  if (!tile_of(blockIdx.x, TilePlan(M, p.n_tiles), p.n_tiles, t)) return;
+  if (!t.half) product_tile<Large, kGT>(p, live, t.m0, (int64_t)t.tn * Large::kBN, 0, 1);
+  else if (t.m0 < M) product_tile<Half, kGT>(p, live, t.m0, (int64_t)t.tn * Large::kBN, 0, 1);
+}
+
+struct FinishParams {
+  const float* partial;     // [split][row][N]
+  const Header* header;
+  const int32_t* list;      // rows of out, and the live rows alone; or NULL: M rows
+  void* out;
+  int64_t M, N;
+  Splits splits;
+  uint32_t n_tiles;
+  int32_t mode;
+  float scale;
+};
+
+// Sums of the splits in order, scaled; four columns a thread.
+__global__ __launch_bounds__(256) void finish_kernel(const FinishParams p) {
+  const int64_t rows = p.list ? (int64_t)p.header->live : p.M, quads = p.N / 4;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x, row = at / quads, col = 4 * (at - row * quads);
+  if (row >= rows) return;
+  const int parts = p.splits.parts(rows, p.n_tiles);
+  if (parts == 1 && !p.splits.always) return;   // the product wrote the result
+  const float scale = p.scale * p.header->d_max;
+  const float* src = p.partial + row * p.N + col;
+  float4 v = *reinterpret_cast<const float4*>(src);
+#pragma unroll 4
+  for (int s = 1; s < parts; ++s) {
+    const float4 o = *reinterpret_cast<const float4*>(src + s * rows * p.N);
+    v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+  }
+  v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+  const int64_t to = (p.list ? (int64_t)p.list[row] : row) * p.N + col;
+  if (p.mode == kBF16) {
+    *reinterpret_cast<uint2*>((uint16_t*)p.out + to) = make_uint2(bf16_pack2(v.x, v.y), bf16_pack2(v.z, v.w));
+  } else {
+    float4* dst = reinterpret_cast<float4*>((float*)p.out + to);
+    if (p.mode == kF32Add) {
+      const float4 o = *dst;
+      v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    }
+    *dst = v;
+  }
+}
+
+// No rows: a gradient of zeros.
+__global__ __launch_bounds__(256) void zero_kernel(uint8_t* p, int64_t bytes) {
+  for (int64_t at = 16 * ((int64_t)blockIdx.x * 256 + threadIdx.x); at < bytes; at += 4096 * (int64_t)gridDim.x)
+    *reinterpret_cast<uint4*>(p + at) = make_uint4(0, 0, 0, 0);
+}
+
+// ------------------------------------------------------------------ host
+
+constexpr int64_t kMaxRows = 1 << 23, kMaxVocab = 1 << 22, kMaxCols = 1 << 16;   // (a launch has less than 2^32 threads)
+constexpr int64_t kThinRows = 64;
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return up(a, b) * b; }
+
+// Cuts a workspace into arrays at multiples of 256 bytes; without a base it
+// counts them.
+struct Cutter {
+  uint8_t* base;
+  int64_t used = 0;
+  template <class P>
+  P* take(int64_t bytes) {
+    P* p = base ? reinterpret_cast<P*>(base + used) : nullptr;
+    used += round_up(bytes, 256);
+    return p;
+  }
+};
+
+struct LossSpace {
+  Header* header;
+  int32_t *list, *place, *target;
+  float* at_target;
+  float2* part;
+  int64_t strip_step, row_step, bytes;
+  int32_t strips;
+};
+
+// Rows of x that the forward pass takes at a time: offsets into them have 32 bits.
+int64_t loss_rows(int64_t M, int64_t K) {
+  const int64_t most = ((int64_t)0xFFFFFFFF / (2 * K)) / 256 * 256;
+  return M < most ? M : most;
+}
+
+LossSpace loss_space(void* base, int64_t M, int64_t V) {
+  Cutter c{(uint8_t*)base};
+  LossSpace s;
+  memset(&s, 0, sizeof(s));
+  const bool thin = M <= kThinRows;
+  s.at_target = c.take<float>(4 * M);
+  if (!thin) {
+    s.header = c.take<Header>(sizeof(Header));
+    s.list = c.take<int32_t>(4 * M);
+    s.place = c.take<int32_t>(4 * M);
+    s.target = c.take<int32_t>(4 * M);
+  }
+  s.strips = (int32_t)(thin ? up(V, kThinCols) * (kThinCols / kThinStrip) : up(V, Large::kBN) * Large::kWN);
+  s.row_step = thin ? s.strips : 1;
+  s.strip_step = thin ? 1 : round_up(M, 16);
+  s.part = c.take<float2>(8 * (thin ? M : s.strip_step) * s.strips);
+  s.bytes = c.used;
+  return s;
+}
+
+// Splits of a product of up to `rows` rows and `cols` columns over `steps`.
+// room: rows that the parts of any number of rows take at most.
+Splits splits_for(int64_t rows, int64_t cols, int64_t steps, bool always) {
+  Splits s;
+  const int64_t n_tiles = up(cols, Large::kBN), by_steps = steps / 8, by_tiles = kUnits / n_tiles;
+  s.most = (int32_t)(by_steps < by_tiles ? by_steps : by_tiles);
+  s.always = always;
+  s.room = 0;
+  if (s.most > 1 && up(rows, Large::kBM) * n_tiles <= kUnits) {
+    const int64_t all = Large::kBM * kUnits / n_tiles;
+    s.room = s.most * rows < all ? s.most * rows : all;
+  }
+  if (always && s.room < rows) s.room = rows;
+  return s;
+}
+
+struct GradSpace {
+  Header* header;
+  int32_t *list, *place;
+  RowInfo* info;
+  uint16_t* x_bf16;
+  uint8_t* x_codes;
+  uint16_t *g, *g_rest, *w_bf16;
+  float *dx_sum, *dw_sum;
+  int64_t pieces, piece, bytes;   // piece: vocabulary rows, a multiple of 256
+  Splits dx_splits, dw_splits;
+};
+
+struct GradShape {
+  int64_t M, V, K;
+  bool fp8, dx, dw, f32;
+};
+
+GradSpace grad_space_of(void* base, const GradShape& h, int64_t pieces) {
+  Cutter c{(uint8_t*)base};
+  GradSpace s;
+  memset(&s, 0, sizeof(s));
+  s.piece = round_up(up(h.V, pieces), 256);
+  s.pieces = up(h.V, s.piece);
+  const int64_t rows = round_up(h.M, 64), p = s.piece;
+  s.dx_splits = splits_for(h.M, h.K, p / 64, s.pieces > 1);
+  s.dw_splits = splits_for(p, h.K, (h.f32 ? 2 : 1) * rows / 64, false);
+  s.header = c.take<Header>(sizeof(Header));
+  s.list = c.take<int32_t>(4 * h.M);
+  s.place = c.take<int32_t>(4 * h.M);
+  s.info = c.take<RowInfo>(sizeof(RowInfo) * h.M);
+  if (!h.fp8 || h.dw) s.x_bf16 = c.take<uint16_t>(2 * h.M * h.K);
+  if (h.fp8) s.x_codes = c.take<uint8_t>(h.M * h.K);
+  s.g = c.take<uint16_t>(2 * rows * p);
+  if (h.dw && h.f32) s.g_rest = c.take<uint16_t>(2 * rows * p);
+  if (h.fp8 && h.dx) s.w_bf16 = c.take<uint16_t>(2 * p * h.K);
+  if (h.dx && s.dx_splits.room > 0) s.dx_sum = c.take<float>(4 * s.dx_splits.room * h.K);
+  if (h.dw && s.dw_splits.room > 0) s.dw_sum = c.take<float>(4 * s.dw_splits.room * h.K);
+  s.bytes = c.used;
+  return s;
+}
+
+// The space of as few pieces as `bytes` hold; pieces 0 if none fit.
+GradSpace grad_space(void* base, int64_t bytes, const GradShape& h) {
+  const int64_t most = up(h.V, 256);
+  GradSpace s;
+  for (int64_t n = 1; n <= most; ++n) {
+    s = grad_space_of(base, h, n);
+    if (s.bytes <= bytes) return s;
+    n = s.pieces > n ? s.pieces : n;
+  }
+  s.pieces = 0;
+  return s;
+}
+
+bool loss_sizes_ok(int64_t M, int64_t V, int64_t K, bool fp8) {
+  return M >= 0 && M <= kMaxRows && V >= 0 && V <= kMaxVocab && K >= 0 && K <= kMaxCols && K % (fp8 ? 128 : 64) == 0 &&
+         M * K <= (int64_t)1 << 33 && V * K <= (int64_t)1 << 34 && up(M, Large::kBM) * up(V, Large::kBN) <= (int64_t)1 << 22;
+}
+
+bool scale_ok(float s) { return s >= FLT_MIN && s <= FLT_MAX; }
+
+// What the forward and the backward call check alike.
+template <class Args>
+coat_status_t check_common(const Args* a, bool& fp8) {
+  fp8 = a->x_codes || a->weight_codes;
+  if (!loss_sizes_ok(a->rows, a->vocab, a->cols, fp8)) return COAT_ERR_INVALID_VALUE;
+  if (fp8 && (a->x || a->weight)) return COAT_ERR_INVALID_VALUE;
+  if (!scale_ok(a->x_scale) || !scale_ok(a->weight_scale) || !scale_ok(a->logit_scale) ||
+      !scale_ok(a->x_scale * a->weight_scale * a->logit_scale) || !(fabsf(a->z_loss) <= FLT_MAX))
+    return COAT_ERR_INVALID_VALUE;
+  return COAT_OK;
+}
+
+template <class Args>
+bool operands_missing(const Args* a, bool fp8) {
+  return fp8 ? !a->x_codes || !a->weight_codes : !a->x || !a->weight;
+}
+
+hipError_t launch(const void* fn, int64_t blocks, int threads, void* params, hipStream_t stream) {
+  void* args[] = {params};
+  return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3((unsigned)threads), args, 0, stream);
+}
+
+template <bool kGrad>
+hipError_t launch_logits(LogitParams& p, bool fp8, hipStream_t stream) {
+  if (p.M <= kThinRows) {
+    // (g has 64 rows for the products at least)
+    constexpr int kLeast = kGrad ? 2 : 1;
+    const void* fns[] = {reinterpret_cast<const void*>(&logit_thin_kernel<false, kGrad, kLeast>),
+                         reinterpret_cast<const void*>(&logit_thin_kernel<false, kGrad, 2>),
+                         reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad, kLeast>),
+                         reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad, 2>)};
+    return launch(fns[2 * fp8 + (p.M > 32)], up(p.N, kThinCols), 128, &p, stream);
+  }
+  const void* fn = fp8 ? reinterpret_cast<const void*>(&logit_large_kernel<true, kGrad>)
+                       : reinterpret_cast<const void*>(&logit_large_kernel<false, kGrad>);
+  p.n_tiles = (int32_t)up(p.N, Large::kBN);
+  return launch(fn, up(p.M, Large::kBM) * p.n_tiles + kUnits / 2, Large::kThreads, &p, stream);
+}
+
+template <bool kGT>
+hipError_t launch_product(ProductParams& p, hipStream_t stream) {
+  p.n_tiles = (uint32_t)up(p.N, Large::kBN);
+  // (parts times tiles are at most kUnits)
+  const int64_t tiles = up(p.M, Large::kBM) * p.n_tiles + kUnits / 2;
+  return launch(reinterpret_cast<const void*>(&product_kernel<kGT>), tiles > kUnits ? tiles : kUnits, Large::kThreads, &p,
+                stream);
+}
+
+hipError_t launch_finish(FinishParams& p, hipStream_t stream) {
+  p.n_tiles = (uint32_t)up(p.N, Large::kBN);
+  return launch(reinterpret_cast<const void*>(&finish_kernel), up(p.M * (p.N / 4), 256), 256, &p, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t coat_fp8_cross_entropy_workspace(int64_t rows, int64_t vocab, int64_t cols) {
+  if (!loss_sizes_ok(rows, vocab, cols, false)) return -1;
+  return rows == 0 || vocab == 0 || cols == 0 ? 0 : loss_space(nullptr, loss_rows(rows, cols), vocab).bytes;
+}
+
+coat_status_t coat_fp8_cross_entropy(const coat_cross_entropy_args_t* a, hipStream_t stream) {
+  if (!a) return COAT_ERR_NULL_POINTER;
+  bool fp8;
+  const coat_status_t st = check_common(a, fp8);
+  if (st != COAT_OK) return st;
+  const int64_t M = a->rows, V = a->vocab, K = a->cols;
+  if (M == 0) return COAT_OK;
+  if (V == 0 || K == 0) return COAT_ERR_INVALID_VALUE;
+  if (operands_missing(a, fp8) || !a->targets || !a->loss || !a->workspace) return COAT_ERR_NULL_POINTER;
+  const uint8_t* x = fp8 ? a->x_codes : (const uint8_t*)a->x;
+  const uint8_t* w = fp8 ? a->weight_codes : (const uint8_t*)a->weight;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a->targets, 8) || !aligned(a->loss, 4) || !aligned(a->lse, 4) ||
+      !aligned(a->workspace, 16))
+    return COAT_ERR_MISALIGNED;
+  const int64_t each = loss_rows(M, K);
+  if (a->workspace_bytes < loss_space(nullptr, each, V).bytes) return COAT_ERR_INVALID_VALUE;
+  hipError_t e = hipSuccess;
+  for (int64_t m0 = 0; m0 < M && e == hipSuccess; m0 += each) {
+    const int64_t rows = M - m0 < each ? M - m0 : each;
+    const LossSpace s = loss_space(a->workspace, rows, V);
+    LogitParams p;
+    memset(&p, 0, sizeof(p));
+    p.stride = (uint32_t)(fp8 ? K : 2 * K);
+    p.x = x + m0 * p.stride;
+    p.w = w;
+    p.M = rows;
+    p.N = p.V = V;
+    p.steps = (int32_t)(p.stride / 128);
+    p.scale2 = a->x_scale * a->weight_scale * a->logit_scale * kLog2e;
+    p.part = s.part;
+    p.at_target = s.at_target;
+    p.targets = a->targets + m0;
+    p.target = s.target;
+    p.list = s.list;
+    p.header = s.header;
+    p.strip_step = s.strip_step;
+    p.row_step = s.row_step;
+    if (s.list) {
+      PrepParams q;
+      memset(&q, 0, sizeof(q));
+      q.targets = p.targets;
+      q.header = s.header;
+      q.list = s.list;
+      q.place = s.place;
+      q.target = s.target;
+      q.M = rows;
+      q.V = V;
+      e = launch(reinterpret_cast<const void*>(&prep_kernel), 1, 1024, &q, stream);
+    }
+    if (e == hipSuccess) e = launch_logits<false>(p, fp8, stream);
+    if (e == hipSuccess) {
+      JoinParams j;
+      memset(&j, 0, sizeof(j));
+      j.part = s.part;
+      j.at_target = s.at_target;
+      j.place = s.place;
+      j.targets = p.targets;
+      j.loss = a->loss + m0;
+      j.lse = a->lse ? a->lse + m0 : nullptr;
+      j.M = rows;
+      j.V = V;
+      j.strip_step = s.strip_step;
+      j.row_step = s.row_step;
+      j.strips = s.strips;
+      j.z = a->z_loss;
+      e = s.list ? launch(reinterpret_cast<const void*>(&loss_join_kernel), up(rows, 16), 256, &j, stream)
+                 : launch(reinterpret_cast<const void*>(&loss_join_few_kernel), rows, 64, &j, stream);
+    }
+  }
+  return e == hipSuccess ? COAT_OK : hip_fail(e);
+}
+
+int64_t coat_fp8_cross_entropy_bwd_workspace(int64_t rows, int64_t vocab, int64_t cols, int64_t piece,
+                                             int32_t codes, int32_t f32) {
+  if (!loss_sizes_ok(rows, vocab, cols, codes != 0) || piece < 1) return -1;
+  if (rows == 0 || vocab == 0 || cols == 0) return 0;
+  const GradShape h = {rows, vocab, cols, codes != 0, true, true, f32 != 0};
+  return grad_space_of(nullptr, h, up(vocab, piece < vocab ? round_up(piece, 256) : vocab)).bytes;
+}
+
+coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a, hipStream_t stream) {
+  if (!a) return COAT_ERR_NULL_POINTER;
+  bool fp8;
+  const coat_status_t st = check_common(a, fp8);
+  if (st != COAT_OK) return st;
+  if (a->dw_bf16 && (a->dw_f32 || a->accumulate)) return COAT_ERR_INVALID_VALUE;
+  const int64_t M = a->rows, V = a->vocab, K = a->cols;
+  if (V == 0 || K == 0) return M == 0 ? COAT_OK : COAT_ERR_INVALID_VALUE;
+  const bool dw = a->dw_bf16 || a->dw_f32;
+  if (!dw && !a->dx) return M == 0 ? COAT_OK : COAT_ERR_NULL_POINTER;
+  if (M > 0 && (operands_missing(a, fp8) || !a->targets || !a->lse || !a->d_loss)) return COAT_ERR_NULL_POINTER;
+  if (M > 0 && !a->workspace) return COAT_ERR_NULL_POINTER;
+  const uint8_t* x = fp8 ? a->x_codes : (const uint8_t*)a->x;
+  const uint8_t* w = fp8 ? a->weight_codes : (const uint8_t*)a->weight;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(a->targets, 8) || !aligned(a->lse, 4) || !aligned(a->d_loss, 4) ||
+      !aligned(a->dx, 16) || !aligned(a->dw_bf16, 16) || !aligned(a->dw_f32, 16) || !aligned(a->workspace, 16))
+    return COAT_ERR_MISALIGNED;
+  if (M == 0) {
+    if (!dw || a->accumulate) return COAT_OK;
+    uint8_t* dst = a->dw_bf16 ? (uint8_t*)a->dw_bf16 : (uint8_t*)a->dw_f32;
+    int64_t bytes = V * K * (a->dw_bf16 ? 2 : 4);
+    const int64_t blocks = up(bytes, 4096);
+    void* args[] = {&dst, &bytes};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void*>(&zero_kernel),
+                                         dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), args, 0, stream);
+    return e == hipSuccess ? COAT_OK : hip_fail(e);
+  }
+  const GradShape h = {M, V, K, fp8, a->dx != nullptr, dw, a->dw_f32 != nullptr};
+  const GradSpace s = grad_space(a->workspace, a->workspace_bytes, h);
+  if (s.pieces == 0) return COAT_ERR_INVALID_VALUE;
+
+  PrepParams q;
+  memset(&q, 0, sizeof(q));
+  q.targets = a->targets;
+  q.d_loss = a->d_loss;
+  q.lse = a->lse;
+  q.header = s.header;
+  q.list = s.list;
+  q.place = s.place;
+  q.info = s.info;
+  q.M = M;
+  q.V = V;
+  q.z = a->z_loss;
+  hipError_t e = launch(reinterpret_cast<const void*>(&prep_kernel), 1, 1024, &q, stream);
+  if (e == hipSuccess) {
+    GatherParams g;
+    memset(&g, 0, sizeof(g));
+    g.x = x;
+    g.place = s.place;
+    g.x_bf16 = s.x_bf16;
+    g.x_codes = s.x_codes;
+    g.dx = a->dx;
+    g.K = K;
+    g.fp8 = fp8;
+    e = launch(reinterpret_cast<const void*>(&gather_kernel), M, 256, &g, stream);
+  }
+  const float scale = a->x_scale * a->weight_scale * a->logit_scale;
+  for (int64_t n = 0; n < s.pieces && e == hipSuccess; ++n) {
+    const int64_t v0 = n * s.piece, rows = V - v0 < s.piece ? V - v0 : s.piece, ld = round_up(rows, 64);
+    const uint8_t* wp = w + v0 * K * (fp8 ? 1 : 2);
+    {
+      LogitParams p;
+      memset(&p, 0, sizeof(p));
+      p.x = fp8 ? s.x_codes : (const uint8_t*)s.x_bf16;
+      p.w = wp;
+      p.header = s.header;
+      p.M = M;
+      p.N = rows;
+      p.V = V;
+      p.stride = (uint32_t)(fp8 ? K : 2 * K);
+      p.steps = (int32_t)(p.stride / 128);
+      p.scale2 = scale * kLog2e;
+      p.ld = ld;
+      p.info = s.info;
+      p.g = s.g;
+      p.g_rest = s.g_rest;
+      p.v0 = (int32_t)v0;
+      e = launch_logits<true>(p, fp8, stream);
+    }
+    if (e == hipSuccess && a->dx) {
+      if (fp8) {
+        const int64_t chunks = rows * K / 8;
+        void* args[] = {(void*)&wp, (void*)&chunks, (void*)&s.w_bf16};
+        e = hipLaunchKernel(reinterpret_cast<const void*>(&expand_kernel), dim3((unsigned)up(chunks, 256)), dim3(256), args,
+                            0, stream);
+      }
+      ProductParams p;
+      memset(&p, 0, sizeof(p));
+      p.a = (const uint8_t*)s.g;
+      p.b = fp8 ? (const uint8_t*)s.w_bf16 : wp;
+      p.header = s.header;
+      p.list = s.list;
+      p.out = a->dx;
+      p.partial = s.dx_sum;
+      p.M = M;
+      p.N = K;
+      p.lda = (uint32_t)(2 * ld);
+      p.ldb = (uint32_t)(2 * K);
+      p.k_rows = (int32_t)rows;
+      p.splits = s.dx_splits;
+      p.mode = kBF16;
+      p.add = n > 0;
+      p.scale = a->weight_scale * a->logit_scale;
+      if (e == hipSuccess) e = launch_product<false>(p, stream);
+    }
+    if (e == hipSuccess && dw) {
+      const int out = a->dw_bf16 ? kBF16 : a->accumulate ? kF32Add : kF32;
+      void* dst = a->dw_bf16 ? (void*)(a->dw_bf16 + v0 * K) : (void*)(a->dw_f32 + v0 * K);
+      ProductParams p;
+      memset(&p, 0, sizeof(p));
+      p.a = (const uint8_t*)s.g;
+      p.a_rest = (const uint8_t*)s.g_rest;
+      p.b = (const uint8_t*)s.x_bf16;
+      p.header = s.header;
+      p.out = dst;
+      p.partial = s.dw_sum;
+      p.M = rows;
+      p.N = K;
+      p.lda = (uint32_t)(2 * ld);
+      p.ldb = (uint32_t)(2 * K);
+      p.splits = s.dw_splits;
+      p.mode = out;
+      p.scale = a->x_scale * a->logit_scale;
+      e = launch_product<true>(p, stream);
+      if (e == hipSuccess && s.dw_sum) {
+        FinishParams f;
+        memset(&f, 0, sizeof(f));
+        f.partial = s.dw_sum;
+        f.header = s.header;
+        f.out = dst;
+        f.M = rows;
+        f.N = K;
+        f.splits = s.dw_splits;
+        f.mode = out;
+        f.scale = p.scale;
+        e = launch_finish(f, stream);
+      }
+    }
+  }
+  if (e == hipSuccess && s.dx_sum) {
+    FinishParams f;
+    memset(&f, 0, sizeof(f));
+    f.partial = s.dx_sum;
+    f.header = s.header;
+    f.list = s.list;
+    f.out = a->dx;
+    f.M = M;
+    f.N = K;
+    f.splits = s.dx_splits;
+    f.mode = kBF16;
+    f.scale = a->weight_scale * a->logit_scale;
+    e = launch_finish(f, stream);
+  }
+  return e == hipSuccess ? COAT_OK : hip_fail(e);
+}
+
+}  // extern "C"
