@@ -96,50 +96,60 @@ __device__ __forceinline__ RowInfo row_info(const PrepParams& p, int64_t r, floa
   return f;
 }
 
-// One block: a running count over 8192 rows at a time, in order.
+// One block: a running count over 8192 rows at a time, in order.  Row
+// 1024 e + t of them is thread t's e-th.
 __global__ __launch_bounds__(1024) void prep_kernel(const PrepParams p) {
-  __shared__ int32_t wave_count[16];
+  constexpr int kEach = 8, kCounts = 16 * kEach;
+  __shared__ int32_t before[kCounts + 1];   // rows of the 64s before each
   __shared__ float wave_max[16];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  constexpr int kEach = 8;
   int32_t base = 0;
   float top = 0.0f;
   for (int64_t first = 0; first < p.M; first += 1024 * kEach) {
-    const int64_t r0 = first + (int64_t)t * kEach;
     int64_t target[kEach];
+    float d[kEach];
 #pragma unroll
-    for (int e = 0; e < kEach; ++e) target[e] = r0 + e < p.M ? p.targets[r0 + e] : -1;
-    int32_t mine = 0;
+    for (int e = 0; e < kEach; ++e) {
+      const int64_t r = first + 1024 * e + t;
+      target[e] = r < p.M ? p.targets[r] : -1;
+      d[e] = p.d_loss && r < p.M ? p.d_loss[r] : 0.0f;
+    }
+    uint64_t lives[kEach];
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const bool live = target[e] >= 0 && target[e] < p.V;
-      mine += live;
-      if (live && p.d_loss) top = fmaxf(top, fabsf(p.d_loss[r0 + e]));
+      lives[e] = __ballot(live);
+      top = live ? fmaxf(top, fabsf(d[e])) : top;
+      if (lane == 0) before[16 * e + wave] = __popcll(lives[e]);
     }
-    int32_t upto = mine;   // of the wave's lanes up to this one
-#pragma unroll
-    for (int s = 1; s < 64; s *= 2) {
-      const int32_t o = __shfl_up(upto, s);
-      if (lane >= s) upto += o;
-    }
-    if (lane == 63) wave_count[wave] = upto;
     __syncthreads();
-    int32_t at = base + upto - mine;
-    for (int w = 0; w < 16; ++w) {
-      if (w < wave) at += wave_count[w];
-      base += wave_count[w];
+    if (wave == 0) {   // their running sum, two a lane
+      static_assert(kCounts == 128, "two a lane");
+      const int32_t a = before[2 * lane], both = a + before[2 * lane + 1];
+      int32_t upto = both;
+#pragma unroll
+      for (int s = 1; s < 64; s *= 2) {
+        const int32_t o = __shfl_up(upto, s);
+        if (lane >= s) upto += o;
+      }
+      before[2 * lane] = upto - both;
+      before[2 * lane + 1] = upto - both + a;
+      if (lane == 63) before[kCounts] = upto;
     }
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      if (r0 + e >= p.M) continue;
-      const bool live = target[e] >= 0 && target[e] < p.V;
-      p.place[r0 + e] = live ? at : -1;
+      const int64_t r = first + 1024 * e + t;
+      if (r >= p.M) continue;
+      const bool live = (lives[e] >> lane) & 1;
+      const int32_t at = base + before[16 * e + wave] + __popcll(lives[e] & (((uint64_t)1 << lane) - 1));
+      p.place[r] = live ? at : -1;
       if (!live) continue;
-      p.list[at] = (int32_t)(r0 + e);
+      p.list[at] = (int32_t)r;
       if (p.target) p.target[at] = (int32_t)target[e];
-      ++at;
     }
-    __syncthreads();   // wave_count is read
+    base += before[kCounts];
+    __syncthreads();   // `before` is read
   }
   if (t == 0) p.header->live = base;
   if (!p.d_loss) return;
@@ -147,19 +157,13 @@ __global__ __launch_bounds__(1024) void prep_kernel(const PrepParams p) {
   for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
   if (lane == 0) wave_max[wave] = top;
   __syncthreads();
+  if (t > 0) return;
   for (int w = 0; w < 16; ++w) top = fmaxf(top, wave_max[w]);
-  const float d_max = top > 0.0f && top <= FLT_MAX ? top : 1.0f;
-  if (t == 0) p.header->d_max = d_max;
-  for (int64_t r = t; r < p.M; r += 1024) {
-    const int32_t at = p.place[r];
-    if (at < 0) continue;
-    p.info[at] = row_info(p, r, d_max);
-  }
+  p.header->d_max = top > 0.0f && top <= FLT_MAX ? top : 1.0f;
 }
 
 struct GatherParams {
   const uint8_t* x;          // M x K BF16, or codes
-  const int32_t* place;
   uint16_t* x_bf16;          // listed rows (written), or NULL
   uint8_t* x_codes;          // or NULL
   uint16_t* dx;              // zeros for rows without a target, or NULL
@@ -194,8 +198,10 @@ __device__ __forceinline__ void gather_row(const GatherParams& p, int64_t r, int
   }
 }
 
-__global__ __launch_bounds__(256) void gather_kernel(const GatherParams p) {
-  gather_row(p, blockIdx.x, p.place[blockIdx.x]);
+__global__ __launch_bounds__(256) void gather_kernel(const PrepParams p, const GatherParams g) {
+  const int32_t at = p.place[blockIdx.x];
+  if (at >= 0 && threadIdx.x == 0) p.info[at] = row_info(p, blockIdx.x, p.header->d_max);
+  gather_row(g, blockIdx.x, at);
 }
 
 // Both for at most 64 rows, a block each.
@@ -456,20 +462,25 @@ __global__ __launch_bounds__(Large::kThreads) void logit_large_kernel(const Logi
   else if (t.m0 < live) logit_tile<Half, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
 }
 
-// At most 128 rows.
-template <bool kFP8, bool kGrad>
-__global__ __launch_bounds__(Small::kThreads) void logit_small_kernel(const LogitParams p) {
+// Smaller tiles where whole ones would be few.
+template <class T, bool kFP8, bool kGrad>
+__device__ __forceinline__ void logit_tiles(const LogitParams& p) {
   const int64_t live = p.header ? p.header->live : p.M;
-  if (live == 0) return;
-  logit_tile<Small, kFP8, kGrad>(p, live, 0, (int64_t)xcd_contiguous32(blockIdx.x, gridDim.x) * Small::kBN);
+  const uint32_t m_tiles = (uint32_t)((live + T::kBM - 1) / T::kBM), tiles = m_tiles * (uint32_t)p.n_tiles;
+  if (blockIdx.x >= tiles) return;
+  uint32_t tm, tn;
+  tile_at(xcd_contiguous32(blockIdx.x, tiles), m_tiles, (uint32_t)p.n_tiles, tm, tn);
+  logit_tile<T, kFP8, kGrad>(p, live, (int64_t)tm * T::kBM, (int64_t)tn * T::kBN);
 }
 
-// At most 32 kI rows.
+template <bool kFP8, bool kGrad>
+__global__ __launch_bounds__(Small::kThreads) void logit_small_kernel(const LogitParams p) {
+  logit_tiles<Small, kFP8, kGrad>(p);
+}
+
 template <bool kFP8, bool kGrad, int kI>
 __global__ __launch_bounds__(128) void logit_thin_kernel(const LogitParams p) {
-  const int64_t live = p.header ? p.header->live : p.M;
-  if (live == 0) return;
-  logit_tile<Thin<kI>, kFP8, kGrad>(p, live, 0, (int64_t)xcd_contiguous32(blockIdx.x, gridDim.x) * kThinCols);
+  logit_tiles<Thin<kI>, kFP8, kGrad>(p);
 }
 
 // The matrix cores align a group of products of codes to the largest with
@@ -877,6 +888,20 @@ struct Cutter {
   }
 };
 
+// The logits' tiles.  Where whole ones are few, most of the device is idle and
+// each waits for its loads: up to an eighth of the compute units thin ones are
+// faster (155 rows x 3070 x 4288: 24 us, 46 in small and 59 in whole tiles;
+// with 64 whole tiles, 1000 x 4000 x 2048, 34, 30 and 35), up to a half small
+// ones (129 x 32000 x 4096, 125 whole tiles: 69 us against 74; 144 of them,
+// 1500 x 6000 x 4096: 99 against 79).
+enum Tiles { kThinTiles, kSmallTiles, kLargeTiles };
+
+Tiles tiles_for(int64_t M, int64_t N) {
+  const int64_t large = up(M, Large::kBM) * up(N, Large::kBN);
+  if (M <= kThinRows || large <= kUnits / 8) return kThinTiles;
+  return M <= kFewRows || large <= kUnits / 2 ? kSmallTiles : kLargeTiles;
+}
+
 struct LossSpace {
   Header* header;
   int32_t *list, *place, *target;
@@ -896,7 +921,8 @@ LossSpace loss_space(void* base, int64_t M, int64_t V) {
   Cutter c{(uint8_t*)base};
   LossSpace s;
   memset(&s, 0, sizeof(s));
-  const bool thin = M <= kThinRows, few = M <= kFewRows;
+  const bool few = M <= kFewRows;
+  const Tiles tiles = tiles_for(M, V);
   s.at_target = c.take<float>(4 * M);
   s.exact = c.take<float>(4 * M);
   if (!few) {
@@ -905,8 +931,9 @@ LossSpace loss_space(void* base, int64_t M, int64_t V) {
     s.place = c.take<int32_t>(4 * M);
     s.target = c.take<int32_t>(4 * M);
   }
-  s.strips = (int32_t)(thin ? up(V, kThinCols) * (kThinCols / kThinStrip)
-                      : few ? up(V, kStrip) : up(V, Large::kBN) * (Large::kBN / kStrip));
+  s.strips = (int32_t)(tiles == kThinTiles    ? up(V, kThinCols) * (kThinCols / kThinStrip)
+                       : tiles == kSmallTiles ? up(V, kStrip)
+                                              : up(V, Large::kBN) * (Large::kBN / kStrip));
   s.row_step = few ? s.strips : 1;
   s.strip_step = few ? 1 : round_up(M, 16);
   s.part = c.take<float2>(8 * (few ? M : s.strip_step) * s.strips);
@@ -968,8 +995,15 @@ GradSpace grad_space_of(void* base, const GradShape& h, int64_t pieces) {
   if (h.fp8) s.x_codes = c.take<uint8_t>(h.M * h.K);
   s.g = c.take<uint16_t>((two ? 4 : 2) * rows * p);
   if (h.fp8 && h.dx) s.w_bf16 = c.take<uint16_t>(2 * p * h.K);
-  if (h.dx && s.dx_splits.room > 0) s.dx_sum = c.take<float>(4 * s.dx_splits.room * h.K);
-  if (h.dw && s.dw_splits.room > 0) s.dw_sum = c.take<float>(4 * s.dw_splits.room * h.K);
+  const int64_t dx_room = h.dx ? s.dx_splits.room : 0, dw_room = h.dw ? s.dw_splits.room : 0;
+  if (s.pieces == 1) {   // dx is done before dw begins: one array for both
+    float* sums = c.take<float>(4 * (dx_room > dw_room ? dx_room : dw_room) * h.K);
+    s.dx_sum = dx_room > 0 ? sums : nullptr;
+    s.dw_sum = dw_room > 0 ? sums : nullptr;
+  } else {
+    if (dx_room > 0) s.dx_sum = c.take<float>(4 * dx_room * h.K);
+    if (dw_room > 0) s.dw_sum = c.take<float>(4 * dw_room * h.K);
+  }
   s.bytes = c.used;
   return s;
 }
@@ -1018,19 +1052,22 @@ hipError_t launch(const void* fn, int64_t blocks, int threads, void* params, hip
 
 template <bool kGrad>
 hipError_t launch_logits(LogitParams& p, bool fp8, hipStream_t stream) {
-  if (p.M <= kThinRows) {
+  const Tiles tiles = tiles_for(p.M, p.N);
+  if (tiles == kThinTiles) {
     // (g has 64 rows for the products at least)
     constexpr int kLeast = kGrad ? 2 : 1;
     const void* fns[] = {reinterpret_cast<const void*>(&logit_thin_kernel<false, kGrad, kLeast>),
                          reinterpret_cast<const void*>(&logit_thin_kernel<false, kGrad, 2>),
                          reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad, kLeast>),
                          reinterpret_cast<const void*>(&logit_thin_kernel<true, kGrad, 2>)};
-    return launch(fns[2 * fp8 + (p.M > 32)], up(p.N, kThinCols), 128, &p, stream);
+    p.n_tiles = (int32_t)up(p.N, kThinCols);
+    return launch(fns[2 * fp8 + (p.M > 32)], up(p.M, kThinRows) * p.n_tiles, 128, &p, stream);
   }
-  if (p.M <= kFewRows) {
+  if (tiles == kSmallTiles) {
     const void* fn = fp8 ? reinterpret_cast<const void*>(&logit_small_kernel<true, kGrad>)
                          : reinterpret_cast<const void*>(&logit_small_kernel<false, kGrad>);
-    return launch(fn, up(p.N, Small::kBN), Small::kThreads, &p, stream);
+    p.n_tiles = (int32_t)up(p.N, Small::kBN);
+    return launch(fn, up(p.M, Small::kBM) * p.n_tiles, Small::kThreads, &p, stream);
   }
   const void* fn = fp8 ? reinterpret_cast<const void*>(&logit_large_kernel<true, kGrad>)
                        : reinterpret_cast<const void*>(&logit_large_kernel<false, kGrad>);
@@ -1198,20 +1235,18 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
   GatherParams g;
   memset(&g, 0, sizeof(g));
   g.x = x;
-  g.place = s.place;
   g.x_bf16 = s.x_bf16;
   g.x_codes = s.x_codes;
   g.dx = a->dx;
   g.K = K;
   g.fp8 = fp8;
-  hipError_t e;
-  if (M <= kThinRows) {
-    void* args[] = {&q, &g};
-    e = hipLaunchKernel(reinterpret_cast<const void*>(&prep_few_kernel), dim3((unsigned)M), dim3(256), args, 0, stream);
-  } else {
-    e = launch(reinterpret_cast<const void*>(&prep_kernel), 1, 1024, &q, stream);
-    if (e == hipSuccess) e = launch(reinterpret_cast<const void*>(&gather_kernel), M, 256, &g, stream);
-  }
+  void* both[] = {&q, &g};
+  hipError_t e = hipSuccess;
+  if (M > kThinRows) e = launch(reinterpret_cast<const void*>(&prep_kernel), 1, 1024, &q, stream);
+  if (e == hipSuccess)
+    e = hipLaunchKernel(M > kThinRows ? reinterpret_cast<const void*>(&gather_kernel)
+                                      : reinterpret_cast<const void*>(&prep_few_kernel),
+                        dim3((unsigned)M), dim3(256), both, 0, stream);
   const float scale = a->x_scale * a->weight_scale * a->logit_scale;
   const bool thin = M <= kThinRows, two = thin || h.f32;
   for (int64_t n = 0; n < s.pieces && e == hipSuccess; ++n) {
@@ -1261,6 +1296,20 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.add = n > 0;
       p.scale = a->weight_scale * a->logit_scale;
       if (e == hipSuccess) e = launch_product(p, false, M, stream);
+      if (e == hipSuccess && s.dx_sum && n == s.pieces - 1) {
+        FinishParams f;
+        memset(&f, 0, sizeof(f));
+        f.partial = s.dx_sum;
+        f.header = s.header;
+        f.list = s.list;
+        f.out = a->dx;
+        f.M = M;
+        f.N = K;
+        f.splits = s.dx_splits;
+        f.mode = kBF16;
+        f.scale = a->weight_scale * a->logit_scale;
+        e = launch_finish(f, M, stream);
+      }
     }
     if (e == hipSuccess && dw) {
       const int out = a->dw_bf16 ? kBF16 : a->accumulate ? kF32Add : kF32;
@@ -1295,20 +1344,6 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
         e = launch_finish(f, rows, stream);
       }
     }
-  }
-  if (e == hipSuccess && s.dx_sum) {
-    FinishParams f;
-    memset(&f, 0, sizeof(f));
-    f.partial = s.dx_sum;
-    f.header = s.header;
-    f.list = s.list;
-    f.out = a->dx;
-    f.M = M;
-    f.N = K;
-    f.splits = s.dx_splits;
-    f.mode = kBF16;
-    f.scale = a->weight_scale * a->logit_scale;
-    e = launch_finish(f, M, stream);
   }
   return e == hipSuccess ? COAT_OK : hip_fail(e);
 }
