@@ -41,7 +41,8 @@ class Case:
 
     def reference(self):
         x = ref.values(self.x, self.scales[0])
-        return ref.Entropy(x, ref.values(self.w, self.scales[1]), self.targets, self.logit_scale, self.z)
+        return ref.Entropy(x, ref.values(self.w, self.scales[1]), self.targets, self.logit_scale, self.z,
+                           codes=self.kind == "fp8")
 
     def scale_args(self):
         return dict(x_scale=self.scales[0], weight_scale=self.scales[1], logit_scale=self.logit_scale, z_loss=self.z)
