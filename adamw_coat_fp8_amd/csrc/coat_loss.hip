@@ -1040,7 +1040,8 @@ coat_status_t check_common(const Args* a, bool& fp8) {
   if (fp8 && (a->x || a->weight)) return COAT_ERR_INVALID_VALUE;
   if (!scale_ok(a->x_scale) || !scale_ok(a->weight_scale) || !scale_ok(a->logit_scale) ||
       !scale_ok(times(a->x_scale, a->weight_scale, a->logit_scale)) || !scale_ok(times(a->x_scale, a->logit_scale)) ||
-      !scale_ok(times(a->weight_scale, a->logit_scale)) || !(fabsf(a->z_loss) <= FLT_MAX))
+      !scale_ok(times(a->weight_scale, a->logit_scale)) ||
+      !scale_ok(times(a->x_scale, a->weight_scale, a->logit_scale) * kLog2e) || !(fabsf(a->z_loss) <= FLT_MAX))
     return COAT_ERR_INVALID_VALUE;
   return COAT_OK;
 }

@@ -107,6 +107,23 @@ def test_cross_entropy_bwd(coat, change, status):
     assert call(coat, "cross_entropy_bwd", coat.CrossEntropyBwdArgs, LOSS_BWD, **change) == status
 
 
+@pytest.mark.parametrize("scales", [(1.0, 1.0, 3e38), (1e19, 1e19, 3.0), (3e38, 1.0, 1.0)])
+def test_scales_whose_exponents_overflow(coat, scales):
+    """Finite, but not in powers of two: 3e38 log2(e) passes 2^128."""
+    change = dict(zip(("x_scale", "weight_scale", "logit_scale"), scales))
+    assert call(coat, "cross_entropy", coat.CrossEntropyArgs, LOSS, **change) == INVAL
+    assert call(coat, "cross_entropy_bwd", coat.CrossEntropyBwdArgs, LOSS_BWD, **change) == INVAL
+
+
+def test_most_tiles(coat):
+    """2^22 tiles of 256 x 256 are taken, one row more is not."""
+    assert coat.cross_entropy_workspace(1 << 20, 1 << 18, 64) > 0
+    assert coat.cross_entropy_bwd_workspace(1 << 20, 1 << 18, 64) > 0
+    for f in (coat.cross_entropy_workspace, coat.cross_entropy_bwd_workspace):
+        with pytest.raises(coat.CoatError):
+            f((1 << 20) + 1, 1 << 18, 64)
+
+
 def test_null_arguments(coat):
     for name in ("embedding", "embedding_bwd", "cross_entropy", "cross_entropy_bwd"):
         assert getattr(coat.lib, f"coat_fp8_{name}")(None, None) == NULLP
