@@ -218,6 +218,14 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
   };
   constexpr int kTiles = kI * kJ, kMF = kFP8 ? kTiles : 2 * kTiles;
   constexpr int kRF = kMF - kMF / 8;   // MFMAs that reads go out behind
+  // Loads behind an MFMA.  All waves' loads go out after the same barrier, and
+  // a wave whose load has to queue issues nothing else: one behind each of a
+  // phase's 16 MFMAs of BF16 rather than two takes 4% fewer cycles (loss of
+  // 8192 x 32000 x 4096: 1581 -> 1561 us at a lower clock, with the gradients
+  // 4925 -> 4851; behind every second 1572 and 4906).  Of codes, with half the
+  // MFMAs, two (795 us, one 802).
+  constexpr int kPer = kFP8 ? 2 : 1;
+  static_assert(kPer * kMF >= kL, "a phase issues a stage's loads");
   auto mma1 = [&](int f, int n) __attribute__((always_inline)) {
     const int i = n % kTiles / kJ, j = n % kJ, e = n / kTiles;
     if constexpr (kFP8)
@@ -248,9 +256,8 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
 #pragma unroll
       for (int r = n * kR / kRF; r < (n + 1) * kR / kRF; ++r)
         if (r < kR) read1(0, An, Bn, 0, r);
-      // (two at a time: the sooner they go out, the longer they have)
 #pragma unroll
-      for (int q = 2 * n; q < 2 * n + 2; ++q)
+      for (int q = kPer * n; q < kPer * n + kPer; ++q)
         if (q < kL) load1(next, S, q);
       __builtin_amdgcn_sched_barrier(0);
     }
