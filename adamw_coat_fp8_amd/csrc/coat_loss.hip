@@ -35,13 +35,20 @@ namespace {
 
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
-using Large = MmaTile<4, 2, 2, 4>;              // 256 x 256, eight waves of 64 x 128
-using Half = MmaTile<2, 4, 2, 2, Large::kA>;    // 128 x 256, eight waves of 64 x 64
+constexpr int mf_of(bool fp8) { return fp8 ? 32 : 16; }
+template <bool kFP8>
+using LargeOf = MmaTile<mf_of(kFP8), 4, 2, 2, 4>;                        // 256 x 256, eight waves of 64 x 128
+template <bool kFP8>
+using HalfOf = MmaTile<mf_of(kFP8), 2, 4, 2, 2, LargeOf<kFP8>::kA>;      // 128 x 256, eight waves of 64 x 64
+template <bool kFP8>
+using SmallOf = MmaTile<mf_of(kFP8), 2, 2, 2, 2>;                        // 128 x 128, four waves of 64 x 64
+using Large = LargeOf<false>;
+using Half = HalfOf<false>;
+using Small = SmallOf<false>;
 template <int kI>
-using Thin = MmaTile<1, 2, kI, 1, 0, 5>;        // 32 kI x 64, two waves, five stages
+using Thin = MmaTile<32, 1, 2, kI, 1, 0, 5>;    // 32 kI x 64, two waves, five stages
 constexpr int kThinCols = 64, kThinStrip = 32;
-using Small = MmaTile<2, 2, 2, 2>;              // 128 x 128, four waves of 64 x 64
-using ThinDx = MmaTile<1, 4, 4, 1>;             // 128 x 128, four waves of 128 x 32
+using ThinDx = MmaTile<16, 1, 4, 4, 1>;         // 128 x 128, four waves of 128 x 32
 constexpr int64_t kThinRows = 64, kFewRows = 128, kSmallSteps = 8;
 
 constexpr int kStrip = 128;       // columns of a partial softmax, but for thin tiles
@@ -61,14 +68,30 @@ struct Header {
   int32_t pad[14];
 };
 
-__device__ __forceinline__ float pair_max(float x) {
+// Over the kL lanes that share a row of a tile.
+template <class Op>
+__device__ __forceinline__ float halves_join(float x, Op op) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  return op(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
-__device__ __forceinline__ float pair_sum(float x) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+template <int kL, class Op>
+__device__ __forceinline__ float row_join(float x, Op op) {
+  if constexpr (kL == 4) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = op(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return halves_join(x, op);
+}
+
+template <int kL>
+__device__ __forceinline__ float row_max(float x) {
+  return row_join<kL>(x, [](float a, float b) { return fmaxf(a, b); });
+}
+
+template <int kL>
+__device__ __forceinline__ float row_sum(float x) {
+  return row_join<kL>(x, [](float a, float b) { return a + b; });
 }
 
 // ------------------------------------------------------ rows with a target
@@ -318,7 +341,7 @@ __device__ __forceinline__ bool tile_of(uint32_t b, const TilePlan& p, uint32_t 
 template <class T, bool kFP8, bool kGrad>
 __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t live, const int64_t m0, const int64_t n0) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
+  const int wm = wave % T::kWM, wn = wave / T::kWM, lr = lane % T::kMf, share = lane / T::kMf;
   // rows and columns past the last re-load it
   uint32_t aoff[T::kLA], boff[T::kLB];
   const uint8_t* a0 = p.list ? p.x : p.x + m0 * p.stride;
@@ -330,50 +353,50 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
   minor_offsets(wave, lane, [&](int r) __attribute__((always_inline)) {
     return (uint32_t)(n0 + r < p.N ? r : (int)(p.N - 1 - n0)) * p.stride;
   }, boff);
-  v16f acc[T::kI][T::kJ];
+  typename T::Acc acc;
   mma_zero<T>(acc);
   if constexpr (T::kStages > 2)
     mma_stream<T, kFP8>(acc, p.steps, a0, aoff, b0, boff);
   else
-    mma_run<T, kFP8, false, false>(acc, p.steps, [&](int s) { return a0 + 128 * (int64_t)s; }, aoff,
-                                   [&](int s) { return b0 + 128 * (int64_t)s; }, boff, boff, [](int) { return false; });
+    mma_run<T, kFP8, false, false>(acc, p.steps, [&](int s) { return a0 + 128 * (int64_t)s; }, aoff, 0,
+                                   [&](int s) { return b0 + 128 * (int64_t)s; }, boff, 0, [](int) { return 0; });
 
   const int64_t col0 = n0 + 32 * T::kJ * wn;          // the wave's first column
   const int64_t valid = p.N - col0;                    // of its columns
   if constexpr (!kGrad) {
     if (valid < 32 * T::kJ) {
 #pragma unroll
-      for (int i = 0; i < T::kI; ++i)
+      for (int i = 0; i < T::kRT; ++i)
 #pragma unroll
-        for (int j = 0; j < T::kJ; ++j)
+        for (int u = 0; u < T::kRuns; ++u)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (32 * j + 8 * (r / 4) + 4 * half + r % 4 >= valid) acc[i][j][r] = -INFINITY;
+          for (int s = 0; s < 4; ++s)
+            if (4 * T::kL * u + 4 * share + s >= valid) set_quad<T>(acc, i, u, s, -INFINITY);
     }
 #pragma unroll
-    for (int i = 0; i < T::kI; ++i) {
-      const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
+    for (int i = 0; i < T::kRT; ++i) {
+      const int64_t row = m0 + 32 * T::kI * wm + T::kMf * i + lr;
       // (a NaN is left to the sum)
       float top = -FLT_MAX;
 #pragma unroll
-      for (int j = 0; j < T::kJ; ++j)
+      for (int u = 0; u < T::kRuns; ++u)
 #pragma unroll
-        for (int r = 0; r < 16; r += 2) top = fmaxf(fmaxf(top, acc[i][j][r]), acc[i][j][r + 1]);
-      top = fmaxf(pair_max(top) * p.scale2, -FLT_MAX);
+        for (int s = 0; s < 4; s += 2) top = fmaxf(fmaxf(top, quad<T>(acc, i, u, s)), quad<T>(acc, i, u, s + 1));
+      top = fmaxf(row_max<T::kL>(top) * p.scale2, -FLT_MAX);
       float sum[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < T::kJ; ++j)
+      for (int u = 0; u < T::kRuns; ++u)
 #pragma unroll
-        for (int r = 0; r < 16; ++r)
-          sum[r % 4] += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], p.scale2, -top));
-      float all = pair_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        for (int s = 0; s < 4; ++s)
+          sum[s] += __builtin_amdgcn_exp2f(__builtin_fmaf(quad<T>(acc, i, u, s), p.scale2, -top));
+      float all = row_sum<T::kL>((sum[0] + sum[1]) + (sum[2] + sum[3]));
       const bool stored = row < live;
       int strip = wn;
       if constexpr (32 * T::kJ < kStrip && T::kStages == 2) {
         // two waves share a strip: the odd one hands its part over
         static_assert(64 * T::kJ == kStrip, "two waves");
-        float2* shared = reinterpret_cast<float2*>(mma_part<T, 0>()) + 32 * (T::kI * wm + i) + l32 + T::kBM * (wn >> 1);
-        if ((wn & 1) && half == 0) *shared = make_float2(top, all);
+        float2* shared = reinterpret_cast<float2*>(mma_part<T, 0>()) + 32 * T::kI * wm + T::kMf * i + lr + T::kBM * (wn >> 1);
+        if ((wn & 1) && share == 0) *shared = make_float2(top, all);
         __syncthreads();
         if (!(wn & 1)) {
           const float2 o = *shared;
@@ -383,13 +406,13 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
         }
         strip = wn & 1 ? -1 : wn >> 1;
       }
-      if (stored && half == 0 && strip >= 0)
+      if (stored && share == 0 && strip >= 0)
         p.part[(n0 / (T::kStages == 2 ? kStrip : 32 * T::kJ) + strip) * p.strip_step + row * p.row_step] = make_float2(top, all);
       // the target's logit, where it lies in the lane's columns
       int64_t t = -1;
       if (stored) t = p.target ? (int64_t)p.target[row] : p.targets[row];
       const int64_t at = t - col0;
-      const bool mine = t >= 0 && t < p.V && at >= 0 && at < 32 * T::kJ && ((at >> 2) & 1) == half;
+      const bool mine = t >= 0 && t < p.V && at >= 0 && at < 32 * T::kJ && ((at >> 2) & (T::kL - 1)) == share;
       if (__any(mine)) {
         const float v = value_at<T>(acc, i, (int)at);
         if (mine) p.at_target[row] = v * p.scale2;
@@ -397,13 +420,13 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
     }
   } else {
     const int64_t padded = (live + 63) / 64 * 64;   // rows of g that the products read
-    RowInfo f[T::kI];
+    RowInfo f[T::kRT];
 #pragma unroll
-    for (int i = 0; i < T::kI; ++i) {
-      const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
+    for (int i = 0; i < T::kRT; ++i) {
+      const int64_t row = m0 + 32 * T::kI * wm + T::kMf * i + lr;
       f[i] = row < live ? p.info[row] : RowInfo{0.0f, 0.0f, 0.0f, -1};
     }
-    auto share = [&](int i, float product) __attribute__((always_inline)) {
+    auto part_of = [&](int i, float product) __attribute__((always_inline)) {
       return f[i].coef * __builtin_amdgcn_exp2f(__builtin_fmaf(product, p.scale2, -f[i].lse2));
     };
     // kRest: what BF16 leaves of the value
@@ -414,9 +437,9 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
     };
     auto write = [&](uint16_t* g, auto kRest) __attribute__((always_inline)) {
       tile_out_bf16<T>(
-          [&](int i, int j, int q) __attribute__((always_inline)) {
-            const float v0 = share(i, acc[i][j][4 * q]), v1 = share(i, acc[i][j][4 * q + 1]);
-            const float v2 = share(i, acc[i][j][4 * q + 2]), v3 = share(i, acc[i][j][4 * q + 3]);
+          [&](int i, int u) __attribute__((always_inline)) {
+            const float v0 = part_of(i, quad<T>(acc, i, u, 0)), v1 = part_of(i, quad<T>(acc, i, u, 1));
+            const float v2 = part_of(i, quad<T>(acc, i, u, 2)), v3 = part_of(i, quad<T>(acc, i, u, 3));
             return make_uint2(pair(v0, v1, kRest), pair(v2, v3, kRest));
           },
           // rows and columns past the last are zero
@@ -433,10 +456,10 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
           // the target's value, where it lies in the lane's columns
           [&](int i, auto set) __attribute__((always_inline)) {
             const int64_t at = (int64_t)f[i].target - p.v0 - col0;
-            const bool mine = f[i].target >= 0 && at >= 0 && at < 32 * T::kJ && ((at >> 2) & 1) == half;
+            const bool mine = f[i].target >= 0 && at >= 0 && at < 32 * T::kJ && ((at >> 2) & (T::kL - 1)) == share;
             if (!__any(mine)) return;
             const float product = value_at<T>(acc, i, (int)at);
-            if (mine) set((int)at + 32 * T::kJ * wn, pair(share(i, product) - f[i].d, 0.0f, kRest) & 0xFFFFu);
+            if (mine) set((int)at + 32 * T::kJ * wn, pair(part_of(i, product) - f[i].d, 0.0f, kRest) & 0xFFFFu);
           });
     };
     write(p.g, std::false_type{});
@@ -445,7 +468,7 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
       // (values are formed again: kept since the first pass they would not fit
       // the registers)
 #pragma unroll
-      for (int i = 0; i < T::kI; ++i) asm volatile("" : "+v"(f[i].lse2));
+      for (int i = 0; i < T::kRT; ++i) asm volatile("" : "+v"(f[i].lse2));
       write(p.g_rest, std::true_type{});
     }
   }
@@ -458,8 +481,8 @@ __global__ __launch_bounds__(Large::kThreads) void logit_large_kernel(const Logi
   const int64_t live = p.header ? p.header->live : p.M;
   TileAt t;
   if (!tile_of(blockIdx.x, TilePlan(live, (uint32_t)p.n_tiles), (uint32_t)p.n_tiles, t)) return;
-  if (!t.half) logit_tile<Large, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
-  else if (t.m0 < live) logit_tile<Half, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
+  if (!t.half) logit_tile<LargeOf<kFP8>, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
+  else if (t.m0 < live) logit_tile<HalfOf<kFP8>, kFP8, kGrad>(p, live, t.m0, (int64_t)t.tn * Large::kBN);
 }
 
 // Smaller tiles where whole ones would be few.
@@ -475,7 +498,7 @@ __device__ __forceinline__ void logit_tiles(const LogitParams& p) {
 
 template <bool kFP8, bool kGrad>
 __global__ __launch_bounds__(Small::kThreads) void logit_small_kernel(const LogitParams p) {
-  logit_tiles<Small, kFP8, kGrad>(p);
+  logit_tiles<SmallOf<kFP8>, kFP8, kGrad>(p);
 }
 
 template <bool kFP8, bool kGrad, int kI>
@@ -663,64 +686,62 @@ template <class T, bool kGT>
 __device__ __forceinline__ void product_tile(const ProductParams& p, const int64_t live, const int64_t m0, const int64_t n0,
                                              const int part, const int parts) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
+  const int wm = wave % T::kWM, wn = wave / T::kWM, lr = lane % T::kMf, share = lane / T::kMf;
   const int64_t M = kGT ? p.M : live;
   const int k_rows = kGT ? (int)live : p.k_rows;
   const int each = (k_rows + 63) / 64, all = p.a_rest ? 2 * each : each;
   const int first = (int)((int64_t)all * part / parts), last = (int)((int64_t)all * (part + 1) / parts);
-  uint32_t aoff[T::kLA], boff[T::kLB], blast[T::kLB];
-  const int64_t cols = p.N - n0;
+  uint32_t aoff[kGT ? kSlowDistinct<T::kLA, T::kBM> : T::kLA], boff[kSlowDistinct<T::kLB, T::kBN>];
   if constexpr (kGT) {
-    slow_offsets<T::kLA, T::kBM>(wave, lane, p.lda, p.lda / 2 - m0, 64, aoff);
+    slow_offsets<T::kLA, T::kBM>(wave, lane, p.lda, p.lda / 2 - m0, aoff);
   } else {
     minor_offsets(wave, lane, [&](int r) __attribute__((always_inline)) {
       return (uint32_t)(m0 + r < M ? r : (int)(M - 1 - m0)) * p.lda;
     }, aoff);
   }
-  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, cols, 64, boff);
-  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, cols, k_rows - 64 * (each - 1), blast);
-  v16f acc[T::kI][T::kJ];
+  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, p.N - n0, boff);
+  typename T::Acc acc;
   mma_zero<T>(acc);
   const uint8_t* a0 = kGT ? p.a + 2 * m0 : p.a + m0 * p.lda;
   const uint8_t* a1 = kGT ? p.a_rest + 2 * m0 : p.a_rest + m0 * p.lda;
   const uint8_t* b0 = p.b + 2 * n0;
   const int64_t a_step = kGT ? 64 * (int64_t)p.lda : 128, b_step = 64 * (int64_t)p.ldb;
+  // the last panel's rows (b0 is not at their first column)
+  const uint32_t last_bytes = (uint32_t)(k_rows - 64 * (each - 1)) * p.ldb - 2 * (uint32_t)n0;
   mma_run<T, false, kGT, true>(
       acc, last - first,
-      [&](int s) { return first + s < each ? a0 + (first + s) * a_step : a1 + (first + s - each) * a_step; }, aoff,
-      [&](int s) { return b0 + (first + s < each ? first + s : first + s - each) * b_step; }, boff, blast,
-      [&](int s) { return first + s == each - 1 || first + s == 2 * each - 1; });
+      [&](int s) { return first + s < each ? a0 + (first + s) * a_step : a1 + (first + s - each) * a_step; }, aoff, p.lda,
+      [&](int s) { return b0 + (first + s < each ? first + s : first + s - each) * b_step; }, boff, p.ldb,
+      [&](int s) { return first + s == each - 1 || first + s == 2 * each - 1 ? last_bytes : 0xFFFFFFFFu; });
   const bool partial = parts > 1 || p.splits.always;
   if (partial || p.mode != kBF16) {
     const float scale = partial ? 1.0f : p.scale * p.header->d_max;
     const bool add = partial ? p.add : p.mode == kF32Add;
     float* out = partial ? p.partial + part * M * p.N : (float*)p.out;
 #pragma unroll
-    for (int i = 0; i < T::kI; ++i) {
-      const int64_t row = m0 + 32 * (T::kI * wm + i) + l32;
+    for (int i = 0; i < T::kRT; ++i) {
+      const int64_t row = m0 + 32 * T::kI * wm + T::kMf * i + lr;
       if (row >= M) continue;
 #pragma unroll
-      for (int j = 0; j < T::kJ; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t col = n0 + 32 * (T::kJ * wn + j) + 8 * q + 4 * half;
-          if (col >= p.N) continue;
-          float4* dst = reinterpret_cast<float4*>(out + row * p.N + col);
-          float4 v = make_float4(acc[i][j][4 * q] * scale, acc[i][j][4 * q + 1] * scale, acc[i][j][4 * q + 2] * scale,
-                                 acc[i][j][4 * q + 3] * scale);
-          if (add) {
-            const float4 o = *dst;
-            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-          }
-          *dst = v;
+      for (int u = 0; u < T::kRuns; ++u) {
+        const int64_t col = n0 + 32 * T::kJ * wn + 4 * T::kL * u + 4 * share;
+        if (col >= p.N) continue;
+        float4* dst = reinterpret_cast<float4*>(out + row * p.N + col);
+        float4 v = make_float4(quad<T>(acc, i, u, 0) * scale, quad<T>(acc, i, u, 1) * scale, quad<T>(acc, i, u, 2) * scale,
+                               quad<T>(acc, i, u, 3) * scale);
+        if (add) {
+          const float4 o = *dst;
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
         }
+        *dst = v;
+      }
     }
     return;
   }
   const float scale = p.scale * p.header->d_max;
-  tile_out_bf16<T>([&](int i, int j, int q) __attribute__((always_inline)) {
-    return make_uint2(bf16_pack2(acc[i][j][4 * q] * scale, acc[i][j][4 * q + 1] * scale),
-                      bf16_pack2(acc[i][j][4 * q + 2] * scale, acc[i][j][4 * q + 3] * scale));
+  tile_out_bf16<T>([&](int i, int u) __attribute__((always_inline)) {
+    return make_uint2(bf16_pack2(quad<T>(acc, i, u, 0) * scale, quad<T>(acc, i, u, 1) * scale),
+                      bf16_pack2(quad<T>(acc, i, u, 2) * scale, quad<T>(acc, i, u, 3) * scale));
   }, [&](int row, int c, uint4 v) __attribute__((always_inline)) {
     const int64_t m = m0 + row, n = n0 + 8 * c;
     if (m < M && n < p.N) store_stream16((uint16_t*)p.out + (p.list ? (int64_t)p.list[m] : m) * p.N + n, v);
@@ -766,33 +787,31 @@ __global__ __launch_bounds__(ThinDx::kThreads) void product_thin_kernel(const Pr
   const uint32_t order = xcd_contiguous32(blockIdx.x, blocks), part = order / p.splits.n_tiles;
   const int64_t n0 = (int64_t)(order - part * p.splits.n_tiles) * T::kBN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int half = lane >> 5, l32 = lane & 31;
   const int all = (p.k_rows + 63) / 64;
   const int first = (int)((int64_t)all * part / parts), last = (int)((int64_t)all * (part + 1) / parts);
-  uint32_t aoff[T::kLA], boff[T::kLB], blast[T::kLB];
+  uint32_t aoff[T::kLA], boff[kSlowDistinct<T::kLB, T::kBN>];
   minor_offsets(wave, lane, [&](int r) __attribute__((always_inline)) { return (uint32_t)r * p.lda; }, aoff);
-  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, p.N - n0, 64, boff);
-  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, p.N - n0, p.k_rows - 64 * (all - 1), blast);
-  v16f acc[T::kI][T::kJ];
+  slow_offsets<T::kLB, T::kBN>(wave, lane, p.ldb, p.N - n0, boff);
+  typename T::Acc acc;
   mma_zero<T>(acc);
   const uint8_t* b0 = p.b + 2 * n0;
   const int64_t b_step = 64 * (int64_t)p.ldb;
-  mma_run<T, false, false, true>(acc, last - first, [&](int s) { return p.a + 128 * (int64_t)(first + s); }, aoff,
-                                 [&](int s) { return b0 + (first + s) * b_step; }, boff, blast,
-                                 [&](int s) { return first + s == all - 1; });
+  const uint32_t last_bytes = (uint32_t)(p.k_rows - 64 * (all - 1)) * p.ldb - 2 * (uint32_t)n0;
+  mma_run<T, false, false, true>(acc, last - first, [&](int s) { return p.a + 128 * (int64_t)(first + s); }, aoff, 0,
+                                 [&](int s) { return b0 + (first + s) * b_step; }, boff, p.ldb,
+                                 [&](int s) { return first + s == all - 1 ? last_bytes : 0xFFFFFFFFu; });
   const bool partial = parts > 1 || p.splits.always;
   const float scale = p.scale * p.header->d_max;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int64_t row = 32 * i + l32;
+  for (int i = 0; i < T::kRT / 2; ++i) {
+    const int64_t row = T::kMf * i + lane % T::kMf;
     if (row >= live) continue;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t col = n0 + 32 * wave + 8 * q + 4 * half;
+    for (int u = 0; u < T::kRuns; ++u) {
+      const int64_t col = n0 + 32 * wave + 4 * T::kL * u + 4 * (lane / T::kMf);
       if (col >= p.N) continue;
-      float4 v;
-      v.x = acc[i][0][4 * q] + acc[i + 2][0][4 * q], v.y = acc[i][0][4 * q + 1] + acc[i + 2][0][4 * q + 1];
-      v.z = acc[i][0][4 * q + 2] + acc[i + 2][0][4 * q + 2], v.w = acc[i][0][4 * q + 3] + acc[i + 2][0][4 * q + 3];
+      auto both = [&](int s) __attribute__((always_inline)) { return quad<T>(acc, i, u, s) + quad<T>(acc, i + T::kRT / 2, u, s); };
+      float4 v = make_float4(both(0), both(1), both(2), both(3));
       if (partial) {
         float4* dst = reinterpret_cast<float4*>(p.partial + (part * live + row) * p.N + col);
         if (p.add) {

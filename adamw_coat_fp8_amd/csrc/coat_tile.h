@@ -16,11 +16,18 @@
 // set 1 while set 0 of the next step is read from the other stage and the
 // loads of the step after next go into this one.
 //
-// The MFMA takes B as its first operand, so each 32 x 32 result is a tile of
-// C^T: register 4 q + s of acc[i][j] is C[row][col] with
-//   row = 32 kI wm + 32 i + lane % 32,  col = 32 kJ wn + 32 j + 8 q + 4 (lane / 32) + s,
-// runs of four columns a lane, and lanes l and l ^ 32 hold all the wave's
-// columns of a row.
+// The MFMA takes B as its first operand, so each result is a tile of C^T.  With
+// results of kMf x kMf (32 or 16), L = 64 / kMf lanes share a row, and lane l
+// holds of the wave's row tile i
+//   row = kMf i + l % kMf,  columns 4 L u + 4 (l / kMf) + 0..3 for u < kRuns,
+// in runs of four (quad()).
+//
+// BF16 products use the 16 x 16 x 32 instruction, codes 32 x 32 x 64.  Large
+// products are bound by the card's power, and 32 x 32 x 16 takes more of it: it
+// reads and writes twice the accumulators for a product, for half the
+// operands.  The same tile with it needs fewer cycles (matrix cores busy for
+// 77% of them, not 72%), at 1.66 GHz instead of 1.89: loss of
+// 8192 x 32000 x 4096 1593 us, with 16 x 16 x 32 1519; gradients 4897 and 4765.
 #ifndef COAT_TILE_H
 #define COAT_TILE_H
 
@@ -35,16 +42,20 @@
 namespace coat {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef short v4s __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 
 // kWM x kWN waves of kI x kJ tiles of 32 x 32.  kArrA: bytes of an LDS array
 // of A, for tiles that share a kernel's arrays with a larger one.  kStages: of
-// mma_stream; 2 for mma_run.
-template <int kWM_, int kWN_, int kI_, int kJ_, int kArrA_ = 0, int kStages_ = 2>
+// mma_stream; 2 for mma_run.  kMf: of the MFMA's results.
+template <int kMf_, int kWM_, int kWN_, int kI_, int kJ_, int kArrA_ = 0, int kStages_ = 2>
 struct MmaTile {
-  static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kJ = kJ_, kStages = kStages_;
+  static constexpr int kWM = kWM_, kWN = kWN_, kI = kI_, kJ = kJ_, kStages = kStages_, kMf = kMf_;
+  static constexpr int kRT = 32 * kI / kMf, kCT = 32 * kJ / kMf;     // results of a wave
+  static constexpr int kL = 64 / kMf, kRuns = 8 * kJ / kL;           // lanes of a row, and their runs of columns
+  using Acc = std::conditional_t<kMf == 32, v16f, v4f>[kRT][kCT];
   static constexpr int kWaves = kWM * kWN, kThreads = 64 * kWaves;
   static constexpr int kBM = 32 * kWM * kI, kBN = 32 * kWN * kJ;
   static constexpr int kA = 128 * kBM, kB = 128 * kBN;               // bytes of a stage's panels
@@ -74,10 +85,10 @@ __device__ __forceinline__ uint8_t* mma_part() {
 }
 
 // Minor panels: the 16-byte chunk of a 128-byte row is XORed with (row / 2) % 8,
-// slow ones: the 64-byte chunk of a row with k % 4; then no read meets a bank
-// twice (slow rows are multiples of 256 bytes).
+// slow ones: the 32-byte chunk of a row with 2 (k % 4) + k / 8 % 2; then no read
+// meets a bank twice (slow rows are multiples of 256 bytes).
 __device__ __forceinline__ int minor_swz(int row) { return (row >> 1) & 7; }
-__device__ __forceinline__ int slow_chunk(int k, int c64) { return c64 ^ (k & 3); }
+__device__ __forceinline__ int slow_chunk(int k, int c32) { return c32 ^ (2 * (k & 3) + ((k >> 3) & 1)); }
 
 // Byte offsets of a lane's loads into a minor panel of kBlock rows: row(r)
 // gives the byte offset of the panel's row r.
@@ -91,149 +102,171 @@ __device__ __forceinline__ void minor_offsets(int wave, int lane, Row row, uint3
 }
 
 // Those of a slow panel of kCols columns: k rows of `stride` bytes; columns
-// from `valid` on (a multiple of 8) re-load the last chunk, and rows from
-// `k_rows` on the last row.
+// from `valid` on (a multiple of 8) re-load the last chunk.  Loads whose rows
+// have their chunks alike share an offset: load i takes
+// off[i % kSlowDistinct], and 4 rows more for each time round.
 template <int kLoads, int kCols>
-__device__ __forceinline__ void slow_offsets(int wave, int lane, uint32_t stride, int64_t valid, int k_rows,
-                                             uint32_t (&off)[kLoads]) {
+constexpr int kSlowDistinct = kCols == 256 && kLoads == 4 ? 2 : kLoads;   // (two rows a load, alike four rows apart)
+
+template <int kLoads, int kCols>
+__device__ __forceinline__ void slow_offsets(int wave, int lane, uint32_t stride, int64_t valid,
+                                             uint32_t (&off)[kSlowDistinct<kLoads, kCols>]) {
 #pragma unroll
-  for (int i = 0; i < kLoads; ++i) {
+  for (int i = 0; i < kSlowDistinct<kLoads, kCols>; ++i) {
     const int byte = 1024 * (kLoads * wave + i) + 16 * lane, k = byte / (2 * kCols), c16 = byte % (2 * kCols) / 16;
-    const int col = 8 * (4 * slow_chunk(k, c16 >> 2) + (c16 & 3));
-    off[i] = (uint32_t)(k < k_rows ? k : k_rows - 1) * stride + 2u * (uint32_t)(col < valid ? col : (int)valid - 8);
+    const int col = 8 * (2 * slow_chunk(k, c16 >> 1) + (c16 & 1));
+    off[i] = (uint32_t)k * stride + 2u * (uint32_t)(col < valid ? col : (int)valid - 8);
   }
 }
 
 template <class T>
-__device__ __forceinline__ void mma_zero(v16f (&acc)[T::kI][T::kJ]) {
+__device__ __forceinline__ void mma_zero(typename T::Acc& acc) {
 #pragma unroll
-  for (int i = 0; i < T::kI; ++i)
+  for (int i = 0; i < T::kRT; ++i)
 #pragma unroll
-    for (int j = 0; j < T::kJ; ++j)
+    for (int j = 0; j < T::kCT; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      for (int r = 0; r < T::kMf * T::kMf / 64; ++r) acc[i][j][r] = 0.0f;
+}
+
+// Value s of the lane's run u of row tile i.
+template <class T>
+__device__ __forceinline__ float quad(const typename T::Acc& acc, int i, int u, int s) {
+  if constexpr (T::kMf == 32) return acc[i][u / 4][4 * (u % 4) + s];
+  else return acc[i][u][s];
+}
+
+template <class T>
+__device__ __forceinline__ void set_quad(typename T::Acc& acc, int i, int u, int s, float v) {
+  if constexpr (T::kMf == 32) acc[i][u / 4][4 * (u % 4) + s] = v;
+  else acc[i][u][s] = v;
 }
 
 // Adds the products of `steps` steps.  a(step), b(step): the panels' base
-// addresses (uniform); aoff, boff: the lane's offsets; blast: those of B in
-// steps for which b_last(step) holds.  The block has met at the end, and no
-// load is in flight.
-template <class T, bool kFP8, bool kASlow, bool kBSlow, class A, class B, class Last>
-__device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A a, const uint32_t (&aoff)[T::kLA], B b,
-                                        const uint32_t (&boff)[T::kLB], const uint32_t (&blast)[T::kLB], Last b_last) {
+// addresses (uniform); aoff, boff: the lane's offsets, where slow those of rows
+// of a_stride, b_stride bytes; b_bytes(step): bytes behind b(step) that may be
+// read (what lies behind them is taken as zero).  The block has met at the end,
+// and no load is in flight.
+template <class T, bool kFP8, bool kASlow, bool kBSlow, class A, int kDA, class B, int kDB, class Bytes>
+__device__ __forceinline__ void mma_run(typename T::Acc& acc, int steps, A a, const uint32_t (&aoff)[kDA], uint32_t a_stride,
+                                        B b, const uint32_t (&boff)[kDB], uint32_t b_stride, Bytes b_bytes) {
 #if __HIP_DEVICE_COMPILE__   // (the host has no type for a buffer's description)
   constexpr int kI = T::kI, kJ = T::kJ, kLA = T::kLA, kLB = T::kLB, kL = kLA + kLB;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::kWM, wn = wave / T::kWM;
-  const int half = lane >> 5, l32 = lane & 31;
+  static_assert(kFP8 == (T::kMf == 32), "the instructions used");
   if (steps <= 0) {
     __syncthreads();
     return;
   }
-  auto rsrc = [](const void* p) __attribute__((always_inline)) {
-    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)0xFFFFFFFF, 0x00020000);
+  static_assert(kDA == (kASlow ? kSlowDistinct<kLA, T::kBM> : kLA) && kDB == (kBSlow ? kSlowDistinct<kLB, T::kBN> : kLB), "");
+  auto rsrc = [](const void* p, uint32_t bytes) __attribute__((always_inline)) {
+    return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
   };
   struct From {
     __amdgpu_buffer_rsrc_t a, b;
-    bool last;
   };
   // (past the last step the last one is fetched again, into a stage that is not read)
   auto from = [&](int step) __attribute__((always_inline)) {
     const int s = step < steps ? step : steps - 1;
-    return From{rsrc(a(s)), rsrc(b(s)), kBSlow ? (bool)b_last(s) : false};
+    return From{rsrc(a(s), 0xFFFFFFFFu), rsrc(b(s), kBSlow ? (uint32_t)b_bytes(s) : 0xFFFFFFFFu)};
   };
   auto load1 = [&](const From& f, auto S, int q) __attribute__((always_inline)) {
     constexpr int st = decltype(S)::value;
     if (q < kLA) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(f.a, mma_part<T, 2 * st>() + 1024 * (kLA * wave + q), 16, (int)aoff[q],
-                                               0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(f.a, mma_part<T, 2 * st>() + 1024 * (kLA * wave + q), 16,
+                                               (int)aoff[q % kDA], (int)(4 * (q / kDA) * a_stride), 0, 0);
     } else {
       const int i = q - kLA;
-      const uint32_t off = kBSlow && f.last ? blast[i] : boff[i];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(f.b, mma_part<T, 2 * st + 1>() + 1024 * (kLB * wave + i), 16, (int)off,
-                                               0, 0, 0);
+      // (a load whose two offsets reach the description's bytes puts zeros into
+      // the LDS, also where the scalar one alone does)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(f.b, mma_part<T, 2 * st + 1>() + 1024 * (kLB * wave + i), 16,
+                                               (int)boff[i % kDB], (int)(4 * (i / kDB) * b_stride), 0, 0);
     }
   };
 
-  // Fragments: [set][tile][chunk].  Phase kk of a step takes 32 bytes a lane
-  // and tile, the chunks 4 kk + 2 half + {0, 1} of a minor row: for BF16 the
-  // k 32 kk + 16 half + 8 {0, 1} + 0..7, which slow panels are read at too.
+  // Fragments, 16 rows of 16 bytes a lane.  A phase takes 64 bytes of each row,
+  // chunks 4 kk + 0..3.  16 x 16 x 32 (BF16): row 16 i + lane % 16, chunk
+  // 4 kk + lane / 16, so k = 32 kk + 8 (lane / 16) + 0..7, which slow panels are
+  // read at too.  32 x 32 x 64 (codes): two for row 32 i + lane % 32, chunks
+  // 4 kk + 2 (lane / 32) + {0, 1}.
   // (Offsets are single opaque values: the compiler follows an address back
   // over a few additions only.)
-  uint4 fa[2][kI][2], fb[2][kJ][2];
-  const int t16 = lane & 15, col16 = (lane >> 4) & 1;
-  // minor: the first tile's chunks of phase 0 ([e]; phase 1 flips bit 6), other
-  // tiles 4096 bytes further; slow: the tiles ([i], [j]), phases and chunks
-  // whole rows further
-  int a_at[kASlow ? kI : 2], b_at[kBSlow ? kJ : 2];
+  constexpr int kFA = 2 * kI, kFB = 2 * kJ;
+  uint4 fa[2][kFA], fb[2][kFB];
+  // minor: the first rows' chunks of phase 0 (of codes, the two; phase 1 flips
+  // bit 6), other rows whole tiles further; slow: the first tile's (tile i flips
+  // the bits of 32 i), phases and the second half whole rows further
+  constexpr int kChunks = T::kMf == 32 ? 2 : 1;
+  int a_at[kASlow ? 1 : kChunks], b_at[kBSlow ? 1 : kChunks];
   auto slow_at = [&](int first, int cols) __attribute__((always_inline)) {
-    const int c = first + 16 * col16 + 4 * (t16 & 3), k = 16 * half + (t16 >> 2);
-    return k * 2 * cols + 64 * slow_chunk(k, c >> 5) + 2 * (c & 31);
+    const int c = first + 4 * (lane & 3), k = 8 * (lane >> 4) + ((lane & 15) >> 2);
+    return k * 2 * cols + 32 * slow_chunk(k, c >> 4) + 2 * (c & 15);
   };
   auto minor_at = [&](int first, int e) __attribute__((always_inline)) {
-    return 128 * (first + l32) + 16 * ((2 * half + e) ^ minor_swz(l32));
+    const int row = lane % T::kMf;
+    return 128 * (first + row) + 16 * ((kChunks * (lane / T::kMf) + e) ^ minor_swz(row));
   };
 #pragma unroll
-  for (int i = 0; i < (kASlow ? kI : 2); ++i) {
-    a_at[i] = kASlow ? slow_at(32 * (kI * wm + i), T::kBM) : minor_at(32 * kI * wm, i);
+  for (int i = 0; i < (kASlow ? 1 : kChunks); ++i) {
+    a_at[i] = kASlow ? slow_at(32 * kI * wm, T::kBM) : minor_at(32 * kI * wm, i);
     asm volatile("" : "+v"(a_at[i]));
   }
 #pragma unroll
-  for (int j = 0; j < (kBSlow ? kJ : 2); ++j) {
-    b_at[j] = kBSlow ? slow_at(32 * (kJ * wn + j), T::kBN) : minor_at(32 * kJ * wn, j);
+  for (int j = 0; j < (kBSlow ? 1 : kChunks); ++j) {
+    b_at[j] = kBSlow ? slow_at(32 * kJ * wn, T::kBN) : minor_at(32 * kJ * wn, j);
     asm volatile("" : "+v"(b_at[j]));
   }
   auto slow4 = [&](const uint8_t* panel, int at) __attribute__((always_inline)) {
     const v4s v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s*)(panel + at));
     return __builtin_bit_cast(uint2, v);
   };
-  // Reads of a phase: first the chunks 0 of every tile, B before A, then the
-  // chunks 1; a chunk of a slow panel is two reads.
-  constexpr int kNA = kASlow ? 2 : 1, kNB = kBSlow ? 2 : 1, kSet = kJ * kNB + kI * kNA, kR = 2 * kSet;
-  auto read1 = [&](int f, const uint8_t* As, const uint8_t* Bs, int kk, int r) __attribute__((always_inline)) {
-    const int e = r / kSet, t = r % kSet;
-    if (t < kJ * kNB) {
-      const int j = t / kNB;
-      if constexpr (kBSlow) {
-        const uint2 v = slow4(Bs, b_at[j] + (32 * kk + 8 * e + 4 * (t % 2)) * 2 * T::kBN);
-        if (t % 2 == 0) fb[f][j][e].x = v.x, fb[f][j][e].y = v.y;
-        else fb[f][j][e].z = v.x, fb[f][j][e].w = v.y;
-      } else {
-        fb[f][j][e] = *reinterpret_cast<const uint4*>(Bs + (b_at[e] ^ (64 * kk)) + 4096 * j);
-      }
+  // Reads of a phase: A before B; a fragment of a slow panel is two reads.  (The
+  // MFMAs go column by column: of the set at hand all A fragments stay to the
+  // end and B's, which are more, are done with one after the other.)
+  constexpr int kNA = kASlow ? 2 : 1, kNB = kBSlow ? 2 : 1, kR = kFB * kNB + kFA * kNA;
+  int tile = 0;
+  auto read_to = [&](uint4& to, const uint8_t* panel, const int* at, auto Slow, int cols, int kk, int t) __attribute__((always_inline)) {
+    if constexpr (decltype(Slow)::value) {
+      static_assert((kFA & (kFA - 1)) == 0 && (kFB & (kFB - 1)) == 0 && kFA <= 8 && kFB <= 8, "flipped bits of a tile's chunk");
+      // (formed for its two reads: kept, they would not fit the registers)
+      if (t == 0) tile = at[0];
+      else if (t % 2 == 0) asm volatile("v_xor_b32 %0, %1, %2" : "=v"(tile) : "s"(32 * (t / 2)), "v"(at[0]));
+      const uint2 v = slow4(panel, tile + (32 * kk + 4 * (t % 2)) * 2 * cols);
+      if (t % 2 == 0) to.x = v.x, to.y = v.y;
+      else to.z = v.x, to.w = v.y;
     } else {
-      const int u = t - kJ * kNB, i = u / kNA;
-      if constexpr (kASlow) {
-        const uint2 v = slow4(As, a_at[i] + (32 * kk + 8 * e + 4 * (u % 2)) * 2 * T::kBM);
-        if (u % 2 == 0) fa[f][i][e].x = v.x, fa[f][i][e].y = v.y;
-        else fa[f][i][e].z = v.x, fa[f][i][e].w = v.y;
-      } else {
-        fa[f][i][e] = *reinterpret_cast<const uint4*>(As + (a_at[e] ^ (64 * kk)) + 4096 * i);
-      }
+      to = *reinterpret_cast<const uint4*>(panel + (at[t % kChunks] ^ (64 * kk)) + 128 * T::kMf * (t / kChunks));
     }
+  };
+  auto read1 = [&](int f, const uint8_t* As, const uint8_t* Bs, int kk, int r) __attribute__((always_inline)) {
+    if (r < kFA * kNA) read_to(fa[f][r / kNA], As, a_at, std::bool_constant<kASlow>{}, T::kBM, kk, r);
+    else read_to(fb[f][(r - kFA * kNA) / kNB], Bs, b_at, std::bool_constant<kBSlow>{}, T::kBN, kk, r - kFA * kNA);
   };
   auto as_v8 = [](const uint4* v) __attribute__((always_inline)) {
     return v8i{(int)v[0].x, (int)v[0].y, (int)v[0].z, (int)v[0].w,
                (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
   };
-  constexpr int kTiles = kI * kJ, kMF = kFP8 ? kTiles : 2 * kTiles;
+  constexpr int kMF = T::kRT * T::kCT;
   constexpr int kRF = kMF - kMF / 8;   // MFMAs that reads go out behind
-  // Loads behind an MFMA.  All waves' loads go out after the same barrier, and
-  // a wave whose load has to queue issues nothing else: one behind each of a
-  // phase's 16 MFMAs of BF16 rather than two takes 4% fewer cycles (loss of
-  // 8192 x 32000 x 4096: 1581 -> 1561 us at a lower clock, with the gradients
-  // 4925 -> 4851; behind every second 1572 and 4906).  Of codes, with half the
-  // MFMAs, two (795 us, one 802).
-  constexpr int kPer = kFP8 ? 2 : 1;
-  static_assert(kPer * kMF >= kL, "a phase issues a stage's loads");
+  // Loads go out kPer at a time behind every kGap-th MFMA.  All waves begin with
+  // theirs after the same barrier, and a wave whose load has to queue issues
+  // nothing else.  Of codes, with 8 MFMAs a phase, two behind each (loss of
+  // 8192 x 32000 x 4096: 795 us, 802 with one); of BF16, with 32, one behind
+  // every second (1519 us, 1528 behind every fourth, 1531 behind each), and one
+  // behind every fourth where slow panels' reads, twice as many, go out too
+  // (gradients of that loss: 4765, 4804 behind every third).
+  constexpr int kMost = kBSlow ? 4 : 2;
+  constexpr int kPer = kFP8 ? 2 : 1, kGap = kFP8 ? 1 : kMF / kL < kMost ? kMF / kL : kMost;
+  static_assert(kPer * kMF >= kGap * kL, "a phase issues a stage's loads");
   auto mma1 = [&](int f, int n) __attribute__((always_inline)) {
-    const int i = n % kTiles / kJ, j = n % kJ, e = n / kTiles;
+    const int i = n % T::kRT, j = n / T::kRT;
     if constexpr (kFP8)
-      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(as_v8(fb[f][j]), as_v8(fa[f][i]), acc[i][j], 0, 0, 0,
-                                                                  0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(as_v8(&fb[f][2 * j]), as_v8(&fa[f][2 * i]), acc[i][j], 0, 0,
+                                                                  0, 0, 0, 0);
     else
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, fb[f][j][e]),
-                                                          __builtin_bit_cast(v8bf, fa[f][i][e]), acc[i][j], 0, 0, 0);
+      acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, fb[f][j]),
+                                                          __builtin_bit_cast(v8bf, fa[f][i]), acc[i][j], 0, 0, 0);
   };
   auto kstep = [&](int step, auto S) __attribute__((always_inline)) {
     constexpr int st = decltype(S)::value;
@@ -257,8 +290,8 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
       for (int r = n * kR / kRF; r < (n + 1) * kR / kRF; ++r)
         if (r < kR) read1(0, An, Bn, 0, r);
 #pragma unroll
-      for (int q = kPer * n; q < kPer * n + kPer; ++q)
-        if (q < kL) load1(next, S, q);
+      for (int q = 0; q < kL; ++q)
+        if (q / kPer * kGap == n) load1(next, S, q);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
@@ -298,11 +331,12 @@ __device__ __forceinline__ void mma_run(v16f (&acc)[T::kI][T::kJ], int steps, A 
 // for the MFMAs: kStages stages in a ring, kStages - 1 steps of loads in
 // flight, one barrier a step.
 template <class T, bool kFP8>
-__device__ __forceinline__ void mma_stream(v16f (&acc)[T::kI][T::kJ], int steps, const uint8_t* a,
+__device__ __forceinline__ void mma_stream(typename T::Acc& acc, int steps, const uint8_t* a,
                                            const uint32_t (&aoff)[T::kLA], const uint8_t* b,
                                            const uint32_t (&boff)[T::kLB]) {
 #if __HIP_DEVICE_COMPILE__
   constexpr int kI = T::kI, kJ = T::kJ, kLA = T::kLA, kLB = T::kLB, kL = kLA + kLB, kS = T::kStages;
+  static_assert(T::kMf == 32, "the instructions used");
   static_assert(kS > 2 && kS <= 7 && kL * (kS - 1) < 64, "stages and loads in flight");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
@@ -393,7 +427,7 @@ __device__ __forceinline__ void mma_stream(v16f (&acc)[T::kI][T::kJ], int steps,
 }
 
 // A BF16 tile through the LDS, so that it leaves in whole 16-byte chunks of
-// rows.  word(i, j, q) gives the four values of a run, packed; out(row, chunk,
+// rows.  word(i, u) gives the four values of a run, packed; out(row, chunk,
 // bytes) takes chunk `chunk` (8 columns) of row `row` of the tile.  The block
 // must have met before and meets inside; patch(i, set) may replace single
 // values of the lane's row of tile i before it does, by set(column, bits).
@@ -406,22 +440,20 @@ __device__ __forceinline__ void tile_out_bf16(Word word, Out out, Patch patch) {
   constexpr int kPart = mma_part_bytes<T>(0), kRows = kPart / kRowBytes / 32 * 32;   // rows of an LDS array
   static_assert(kRows >= 32 && kRows * 4 >= T::kBM && mma_part_bytes<T>(1) >= kPart, "the tile fits the arrays");
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave % T::kWM, wn = wave / T::kWM, half = lane >> 5, l32 = lane & 31;
+  const int wm = wave % T::kWM, wn = wave / T::kWM, share = lane / T::kMf;
   auto part = [](int q) __attribute__((always_inline)) {
     return q == 0 ? mma_part<T, 0>() : q == 1 ? mma_part<T, 1>() : q == 2 ? mma_part<T, 2>() : mma_part<T, 3>();
   };
   auto at = [](int row, int c) __attribute__((always_inline)) { return row % kRows * kRowBytes + 16 * (c ^ (row & kMask)); };
 #pragma unroll
-  for (int i = 0; i < T::kI; ++i) {
-    const int first = 32 * (T::kI * wm + i), row = first + l32;
+  for (int i = 0; i < T::kRT; ++i) {
+    const int first = 32 * T::kI * wm + T::kMf * i, row = first + lane % T::kMf;
     uint8_t* tile = part(first / kRows);
 #pragma unroll
-    for (int j = 0; j < T::kJ; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        *reinterpret_cast<uint2*>(tile + at(row, 4 * (T::kJ * wn + j) + q) + 8 * half) = word(i, j, q);
-        if (q % 2) __builtin_amdgcn_sched_barrier(0);   // (or every word is begun before one is stored)
-      }
+    for (int u = 0; u < T::kRuns; ++u) {
+      *reinterpret_cast<uint2*>(tile + at(row, 4 * T::kJ * wn + T::kL / 2 * u + share / 2) + 8 * (share & 1)) = word(i, u);
+      if (u % 2) __builtin_amdgcn_sched_barrier(0);   // (or every word is begun before one is stored)
+    }
     patch(i, [&](int col, uint32_t bits) __attribute__((always_inline)) {
       *reinterpret_cast<uint16_t*>(tile + at(row, col >> 3) + 2 * (col & 7)) = (uint16_t)bits;
     });
@@ -434,36 +466,34 @@ __device__ __forceinline__ void tile_out_bf16(Word word, Out out, Patch patch) {
   }
 }
 
-// The value at column `col` (of the wave's 32 kJ, in the lane's half) of the
-// lane's row of tile i: a tree of selections by the column's bits, each a
+// The value at column `col` (of the wave's 32 kJ, in one of the lane's runs) of
+// the lane's row of tile i: a tree of selections by the column's bits, each a
 // mask.  (Of conditions the compiler makes searches through whole vectors.)
 template <class T>
-__device__ __forceinline__ float value_at(const v16f (&acc)[T::kI][T::kJ], int i, int col) {
-  static_assert(T::kJ == 1 || T::kJ == 2 || T::kJ == 4, "a power of two");
-  uint32_t mask[6];
-  constexpr int kBit[6] = {0, 1, 3, 4, 5, 6};
-#pragma unroll
-  for (int b = 0; b < 6; ++b) {
-    mask[b] = 0u - (uint32_t)((col >> kBit[b]) & 1);
-    asm volatile("" : "+v"(mask[b]));
-  }
-  auto pick = [&](int b, uint32_t zero, uint32_t one) __attribute__((always_inline)) {
-    return (one & mask[b]) | (zero & ~mask[b]);
+__device__ __forceinline__ float value_at(const typename T::Acc& acc, int i, int col) {
+  constexpr int kRuns = T::kRuns;
+  static_assert((kRuns & (kRuns - 1)) == 0 && kRuns <= 16, "a power of two");
+  auto mask_of = [&](int bit) __attribute__((always_inline)) {
+    uint32_t m = 0u - (uint32_t)((col >> bit) & 1);
+    asm volatile("" : "+v"(m));
+    return m;
   };
-  uint32_t of_j[T::kJ];
+  auto pick = [](uint32_t m, uint32_t zero, uint32_t one) __attribute__((always_inline)) { return (one & m) | (zero & ~m); };
+  const uint32_t m0 = mask_of(0), m1 = mask_of(1);
+  uint32_t v[kRuns];
 #pragma unroll
-  for (int j = 0; j < T::kJ; ++j) {
-    uint32_t of_q[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      auto bits = [&](int e) __attribute__((always_inline)) { return __float_as_uint(acc[i][j][4 * q + e]); };
-      of_q[q] = pick(1, pick(0, bits(0), bits(1)), pick(0, bits(2), bits(3)));
-    }
-    of_j[j] = pick(3, pick(2, of_q[0], of_q[1]), pick(2, of_q[2], of_q[3]));
+  for (int u = 0; u < kRuns; ++u) {
+    auto bits = [&](int s) __attribute__((always_inline)) { return __float_as_uint(quad<T>(acc, i, u, s)); };
+    v[u] = pick(m1, pick(m0, bits(0), bits(1)), pick(m0, bits(2), bits(3)));
   }
-  if constexpr (T::kJ == 4) return __uint_as_float(pick(5, pick(4, of_j[0], of_j[1]), pick(4, of_j[2], of_j[3])));
-  if constexpr (T::kJ == 2) return __uint_as_float(pick(4, of_j[0], of_j[1]));
-  return __uint_as_float(of_j[0]);
+  constexpr int kFirst = T::kL == 2 ? 3 : 4;   // the column's bits: 2 of the run, those of the lane, those of u
+#pragma unroll
+  for (int b = 0; (1 << b) < kRuns; ++b) {
+    const uint32_t m = mask_of(kFirst + b);
+#pragma unroll
+    for (int u = 0; u < kRuns; u += 2 << b) v[u] = pick(m, v[u], v[u + (1 << b)]);
+  }
+  return __uint_as_float(v[0]);
 }
 
 template <class T, class Word, class Out>
