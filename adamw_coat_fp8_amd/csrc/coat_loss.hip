@@ -49,7 +49,7 @@ template <int kI>
 using Thin = MmaTile<32, 1, 2, kI, 1, 0, 5>;    // 32 kI x 64, two waves, five stages
 constexpr int kThinCols = 64, kThinStrip = 32;
 using ThinDx = MmaTile<16, 1, 4, 4, 1>;         // 128 x 128, four waves of 128 x 32
-constexpr int64_t kThinRows = 64, kFewRows = 128, kSmallSteps = 8;
+constexpr int64_t kThinRows = 64, kFewRows = 128, kSmallSteps = 2, kSmallCols = 2048;
 
 constexpr int kStrip = 128;       // columns of a partial softmax, but for thin tiles
 constexpr int kGroupM = 4;        // tile rows that are walked together
@@ -767,8 +767,13 @@ __global__ __launch_bounds__(Large::kThreads) void product_kernel(const ProductP
   else if (t.m0 < M) product_tile<Half, kGT>(p, live, t.m0, (int64_t)t.tn * Large::kBN, 0, 1);
 }
 
-// g^T x with few steps to a tile: small tiles, two blocks to a compute unit,
-// so that one's loads and stores run beside the other's.
+// g^T x of one or two steps: a tile is its first loads and its stores.  With up
+// to 2048 columns small tiles, two blocks to a compute unit, so that one's run
+// beside the other's (gradients of 61 x 32000 x 1024: 65.2 us, 66.5 in whole
+// tiles; of 128 x 50001 x 2048 187.5 and 189.1); rows of more columns are
+// written faster in whole ones' longer pieces (64 x 32000 x 4096: 219.6 small,
+// 213.9 whole), and more steps go faster there (200 x 32000 x 2048, four steps:
+// 165.4 and 159.5).
 __global__ __launch_bounds__(Small::kThreads) void product_small_kernel(const ProductParams p) {
   const uint32_t n_tiles = (uint32_t)((p.N + Small::kBN - 1) / Small::kBN), m_tiles = (uint32_t)((p.M + Small::kBM - 1) / Small::kBM);
   uint32_t tm, tn;
@@ -910,10 +915,10 @@ struct Cutter {
 
 // The logits' tiles.  Where whole ones are few, most of the device is idle and
 // each waits for its loads: up to an eighth of the compute units thin ones are
-// faster (155 rows x 3070 x 4288: 24 us, 46 in small and 59 in whole tiles;
-// with 64 whole tiles, 1000 x 4000 x 2048, 34, 30 and 35), up to a half small
-// ones (129 x 32000 x 4096, 125 whole tiles: 69 us against 74; 144 of them,
-// 1500 x 6000 x 4096: 99 against 79).
+// faster (155 rows x 3070 x 4288: 24 us, 47 in small and 60 in whole tiles;
+// with 64 whole tiles, 1000 x 4000 x 2048, 34, 32 and 36), up to a half small
+// ones (129 x 32000 x 4096, 125 whole tiles: 82 us against 90; 144 of them,
+// 1500 x 6000 x 4096: 99 against 82).
 enum Tiles { kThinTiles, kSmallTiles, kLargeTiles };
 
 Tiles tiles_for(int64_t M, int64_t N) {
@@ -1104,7 +1109,7 @@ hipError_t launch_product(ProductParams& p, bool gt, int64_t rows, hipStream_t s
   if (!gt && rows <= kThinRows)
     return launch(reinterpret_cast<const void*>(&product_thin_kernel),
                   (int64_t)p.splits.n_tiles * (p.splits.most > 1 ? p.splits.most : 1), ThinDx::kThreads, &p, stream);
-  if (gt && p.splits.room == 0 && up(rows, 64) * (p.a_rest ? 2 : 1) <= kSmallSteps)
+  if (gt && p.splits.room == 0 && p.N <= kSmallCols && up(rows, 64) * (p.a_rest ? 2 : 1) <= kSmallSteps)
     return launch(reinterpret_cast<const void*>(&product_small_kernel), up(p.M, Small::kBM) * up(p.N, Small::kBN),
                   Small::kThreads, &p, stream);
   p.n_tiles = (uint32_t)up(p.N, Large::kBN);
