@@ -25,7 +25,12 @@ struct LookupParams {
 };
 
 // out[r] = bf16(scale * table[token of r]), zeros for a token outside the
-// table.  A thread copies two chunks of eight values.
+// table.  The one rounding is the result's; codes and BF16 are exact in FP32.
+// A thread copies two chunks of eight values, 4 KB apart in the output, so that
+// two chains of loads (token, row) are in flight.  Bound by the writes and by
+// the table's rows that are not in a cache: 8191 rows of 4096 columns from an
+// 8-bit table 13.6 us (5.9 TB/s of 80 MB, of which counters see 20 MB read),
+// from BF16 17.5 (5.4); one row 1.8 us, in 5.2 from call to call.
 template <bool kFP8>
 __global__ __launch_bounds__(256) void embedding_kernel(const LookupParams p) {
   uint32_t at[2];
@@ -57,6 +62,13 @@ __global__ __launch_bounds__(256) void embedding_kernel(const LookupParams p) {
 // order: the rows are sorted by (token, row), runs of one token are summed in
 // FP32 from that order, 32 rows to a part, and runs that span parts are joined
 // from partial sums.  No atomics: the result does not depend on timing.
+//
+// It cannot do without reading dy and writing dW once, 329 MB for 8192 rows of
+// 4096 columns over 32000 rows of BF16: 64 us at a copy's rate.  Measured 74.5
+// (under the profiler sort 23, sums 40, join 15), a part of dW's zeros written
+// in each of the three.  What is left is the sort's and the join's latency,
+// where the memory is not busy all the time.  2048 columns and 4099 rows over
+// 50001 rows of FP32: 85.6 (sort 16, sums 55, join 15), 80 at a copy's rate.
 
 enum Out { kBF16 = 0, kF32 = 1, kF32Add = 2 };
 
@@ -77,7 +89,9 @@ struct SortParams {
 
 constexpr int kSortBlock = 32;     // rows that a block places
 
-// A row's place in its run: how many keys are smaller, or equal and earlier.
+// A row's place in its run: how many keys are smaller, or equal and earlier:
+// rows^2 comparisons, but 64 of them an instruction and all rows at once, where
+// a sort in passes is a chain of launches or barriers.
 // A block of 16 waves places 32 rows: a wave holds a sixteenth of the run's
 // keys in its lanes' registers (kEach each), and for each row compares 64 at a
 // time and counts the bits of the result.  key_of(i): the key of the run's row
