@@ -254,7 +254,9 @@ __device__ __forceinline__ void mma_run(typename T::Acc& acc, int steps, A a, co
                (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
   };
   constexpr int kMF = T::kRT * T::kCT;
-  constexpr int kRF = kMF - kMF / 8;   // MFMAs that reads go out behind
+  // MFMAs that reads go out behind, the rest give them time to arrive (loss of
+  // 8192 x 32000 x 4096: 1531 us behind 7/8, 1524 behind 3/4, 1514, 1534 behind 1/2)
+  constexpr int kRF = kMF * 5 / 8;
   // Loads go out kPer at a time behind every kGap-th MFMA.  All waves begin with
   // theirs after the same barrier, and a wave whose load has to queue issues
   // nothing else.  Of codes, with 8 MFMAs a phase, two behind each (loss of
