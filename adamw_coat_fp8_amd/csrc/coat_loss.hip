@@ -783,20 +783,6 @@ __global__ __launch_bounds__(Large::kThreads) void product_kernel(const ProductP
   else if (t.m0 < M) product_tile<Half, kGT>(p, live, t.m0, (int64_t)t.tn * Large::kBN, 0, 1);
 }
 
-// g^T x of one or two steps: a tile is its first loads and its stores.  With up
-// to 2048 columns small tiles, two blocks to a compute unit, so that one's run
-// beside the other's (gradients of 61 x 32000 x 1024: 65.2 us, 66.5 in whole
-// tiles; of 128 x 50001 x 2048 187.5 and 189.1); rows of more columns are
-// written faster in whole ones' longer pieces (64 x 32000 x 4096: 219.6 small,
-// 213.9 whole), and more steps go faster there (200 x 32000 x 2048, four steps:
-// 165.4 and 159.5).
-__global__ __launch_bounds__(Small::kThreads) void product_small_kernel(const ProductParams p) {
-  const uint32_t n_tiles = (uint32_t)((p.N + Small::kBN - 1) / Small::kBN), m_tiles = (uint32_t)((p.M + Small::kBM - 1) / Small::kBM);
-  uint32_t tm, tn;
-  tile_at(xcd_contiguous32(blockIdx.x, m_tiles * n_tiles), m_tiles, n_tiles, tm, tn);
-  product_tile<Small, true>(p, p.header->live, (int64_t)tm * Small::kBM, (int64_t)tn * Small::kBN, 0, 1);
-}
-
 // g W for at most 64 rows: g's two parts are rows 0 to 63 and 64 to 127 of a
 // tile, and are added where they meet, in the registers.
 __global__ __launch_bounds__(ThinDx::kThreads) void product_thin_kernel(const ProductParams p) {
@@ -862,13 +848,13 @@ struct FinishParams {
 // Sums of the splits, scaled; four columns a thread, and with kBy > 1 every
 // kBy-th split a thread, joined in a fixed order.
 template <int kBy>
-__global__ __launch_bounds__(256) void finish_kernel(const FinishParams p) {
+__device__ __forceinline__ void finish_block(const FinishParams& p, const int64_t block) {
   __shared__ float4 part[kBy][256 / kBy];
   const int64_t rows = p.list ? (int64_t)p.header->live : p.M, quads = p.N / 4;
   const int parts = rows > 0 ? p.splits.parts(rows) : 1;
   if (rows == 0 || (parts == 1 && !p.splits.always)) return;   // the product wrote the result
   const int t = threadIdx.x % (256 / kBy), by = threadIdx.x / (256 / kBy);
-  const int64_t at = (int64_t)blockIdx.x * (256 / kBy) + t, row = at / quads, col = 4 * (at - row * quads);
+  const int64_t at = block * (256 / kBy) + t, row = at / quads, col = 4 * (at - row * quads);
   float4 v = make_float4(0, 0, 0, 0);
   if (row < rows) {
     const float* src = p.partial + row * p.N + col;
@@ -902,6 +888,35 @@ __global__ __launch_bounds__(256) void finish_kernel(const FinishParams p) {
     }
     *dst = v;
   }
+}
+
+template <int kBy>
+__global__ __launch_bounds__(256) void finish_kernel(const FinishParams p) {
+  finish_block<kBy>(p, blockIdx.x);
+}
+
+// g^T x of one or two steps: a tile is its first loads and its stores.  With up
+// to 2048 columns small tiles, two blocks to a compute unit, so that one's run
+// beside the other's (gradients of 61 x 32000 x 1024: 65.2 us, 66.5 in whole
+// tiles; of 128 x 50001 x 2048 187.5 and 189.1); rows of more columns are
+// written faster in whole ones' longer pieces (64 x 32000 x 4096: 219.6 small,
+// 213.9 whole), and more steps go faster there (200 x 32000 x 2048, four steps:
+// 165.4 and 159.5).
+//
+// The blocks ahead of the tiles', if there are any, finish dx (f): neither reads
+// what the other writes, and dx's needs no launch of its own (61 x 32000 x 1024:
+// 64.4 us with one, 63.1 with the blocks behind the tiles', 61.7 so).
+__global__ __launch_bounds__(Small::kThreads) void product_small_kernel(const ProductParams p, const FinishParams f) {
+  static_assert(Small::kThreads == 256, "of a block that finishes too");
+  const uint32_t n_tiles = (uint32_t)((p.N + Small::kBN - 1) / Small::kBN), m_tiles = (uint32_t)((p.M + Small::kBM - 1) / Small::kBM);
+  const uint32_t ahead = gridDim.x - m_tiles * n_tiles;
+  if (blockIdx.x < ahead) {
+    finish_block<8>(f, blockIdx.x);
+    return;
+  }
+  uint32_t tm, tn;
+  tile_at(xcd_contiguous32(blockIdx.x - ahead, m_tiles * n_tiles), m_tiles, n_tiles, tm, tn);
+  product_tile<Small, true>(p, p.header->live, (int64_t)tm * Small::kBM, (int64_t)tn * Small::kBN, 0, 1);
 }
 
 // No rows: a gradient of zeros.
@@ -1121,13 +1136,26 @@ hipError_t launch_logits(LogitParams& p, bool fp8, hipStream_t stream) {
   return launch(fn, up(p.M, Large::kBM) * p.n_tiles + kUnits / 2, Large::kThreads, &p, stream);
 }
 
-hipError_t launch_product(ProductParams& p, bool gt, int64_t rows, hipStream_t stream) {
+// Whether g^T x takes small tiles; two: g in two parts.
+bool small_product(const Splits& s, int64_t cols, int64_t rows, bool two) {
+  return s.room == 0 && cols <= kSmallCols && up(rows, 64) * (two ? 2 : 1) <= kSmallSteps;
+}
+
+int64_t few_finish_blocks(const FinishParams& p) { return up(p.M * (p.N / 4), 32); }
+
+// f: dx to be finished beside a product of small tiles, or NULL.
+hipError_t launch_product(ProductParams& p, bool gt, int64_t rows, hipStream_t stream, FinishParams* f = nullptr) {
   if (!gt && rows <= kThinRows)
     return launch(reinterpret_cast<const void*>(&product_thin_kernel),
                   (int64_t)p.splits.n_tiles * (p.splits.most > 1 ? p.splits.most : 1), ThinDx::kThreads, &p, stream);
-  if (gt && p.splits.room == 0 && p.N <= kSmallCols && up(rows, 64) * (p.a_rest ? 2 : 1) <= kSmallSteps)
-    return launch(reinterpret_cast<const void*>(&product_small_kernel), up(p.M, Small::kBM) * up(p.N, Small::kBN),
-                  Small::kThreads, &p, stream);
+  if (gt && small_product(p.splits, p.N, rows, p.a_rest)) {
+    FinishParams none;
+    memset(&none, 0, sizeof(none));
+    void* args[] = {&p, f ? f : &none};
+    const int64_t blocks = up(p.M, Small::kBM) * up(p.N, Small::kBN) + (f ? few_finish_blocks(*f) : 0);
+    return hipLaunchKernel(reinterpret_cast<const void*>(&product_small_kernel), dim3((unsigned)blocks),
+                           dim3((unsigned)Small::kThreads), args, 0, stream);
+  }
   p.n_tiles = (uint32_t)up(p.N, Large::kBN);
   // (parts times tiles are at most kUnits)
   const int64_t tiles = up(p.M, Large::kBM) * p.n_tiles + kUnits / 2;
@@ -1138,7 +1166,7 @@ hipError_t launch_product(ProductParams& p, bool gt, int64_t rows, hipStream_t s
 // rows: at most.
 hipError_t launch_finish(FinishParams& p, int64_t rows, hipStream_t stream) {
   if (rows <= kThinRows)
-    return launch(reinterpret_cast<const void*>(&finish_kernel<8>), up(rows * (p.N / 4), 32), 256, &p, stream);
+    return launch(reinterpret_cast<const void*>(&finish_kernel<8>), few_finish_blocks(p), 256, &p, stream);
   return launch(reinterpret_cast<const void*>(&finish_kernel<1>), up(rows * (p.N / 4), 256), 256, &p, stream);
 }
 
@@ -1317,6 +1345,9 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.v0 = (int32_t)v0;
       e = launch_logits<true>(p, fp8, stream);
     }
+    FinishParams f;        // dx's
+    memset(&f, 0, sizeof(f));
+    bool beside = false;   // finished beside dW's product
     if (e == hipSuccess && a->dx) {
       if (fp8) {
         const int64_t chunks = rows * K / 8;
@@ -1343,8 +1374,6 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.scale = times(a->weight_scale, a->logit_scale);
       if (e == hipSuccess) e = launch_product(p, false, M, stream);
       if (e == hipSuccess && s.dx_sum && n == s.pieces - 1) {
-        FinishParams f;
-        memset(&f, 0, sizeof(f));
         f.partial = s.dx_sum;
         f.header = s.header;
         f.list = s.list;
@@ -1354,7 +1383,8 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
         f.splits = s.dx_splits;
         f.mode = kBF16;
         f.scale = times(a->weight_scale, a->logit_scale);
-        e = launch_finish(f, M, stream);
+        beside = M <= kThinRows && dw && small_product(s.dw_splits, K, M, two);
+        if (!beside) e = launch_finish(f, M, stream);
       }
     }
     if (e == hipSuccess && dw) {
@@ -1375,19 +1405,19 @@ coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a,
       p.splits = s.dw_splits;
       p.mode = out;
       p.scale = times(a->x_scale, a->logit_scale);
-      e = launch_product(p, true, M, stream);
+      e = launch_product(p, true, M, stream, beside ? &f : nullptr);
       if (e == hipSuccess && s.dw_sum) {
-        FinishParams f;
-        memset(&f, 0, sizeof(f));
-        f.partial = s.dw_sum;
-        f.header = s.header;
-        f.out = dst;
-        f.M = rows;
-        f.N = K;
-        f.splits = s.dw_splits;
-        f.mode = out;
-        f.scale = p.scale;
-        e = launch_finish(f, rows, stream);
+        FinishParams q;
+        memset(&q, 0, sizeof(q));
+        q.partial = s.dw_sum;
+        q.header = s.header;
+        q.out = dst;
+        q.M = rows;
+        q.N = K;
+        q.splits = s.dw_splits;
+        q.mode = out;
+        q.scale = p.scale;
+        e = launch_finish(q, rows, stream);
       }
     }
   }

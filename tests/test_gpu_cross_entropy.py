@@ -145,6 +145,17 @@ def test_no_targets(rows, kind):
     assert torch.equal(c.backward(lse, torch.float32, base=base)[1], base)
 
 
+@pytest.mark.parametrize("kind,rows,vocab,cols", [("bf16", 61, 5000, 1024), ("bf16", 40, 3000, 2112), ("fp8", 33, 4100, 512),
+                                                 ("bf16", 64, 2500, 2048), ("bf16", 100, 3000, 1024)])
+def test_gradients_apart(kind, rows, vocab, cols):
+    """dx and dw are the same bits asked for together or alone (few rows finish dx beside dw's product)."""
+    c = Case(rows, vocab, cols, kind, padding=3, z=1e-3)
+    lse = c.forward()[1]
+    both = c.backward(lse)
+    assert torch.equal(c.backward(lse, dw=False)[0], both[0])
+    assert torch.equal(c.backward(lse, dx=False)[1], both[1])
+
+
 def test_no_rows():
     c = Case(0, 300, 64)
     c.forward()
