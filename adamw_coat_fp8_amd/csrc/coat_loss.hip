@@ -36,8 +36,8 @@ namespace {
 // Large calls are bound by the matrix cores and, within those, by the card's
 // power (coat_tile.h); the logits never leave the chip, so that the forward
 // pass reads x and W and writes 8 bytes a row and strip.  8192 x 32000 x 4096 in
-// BF16: loss 1519 to 1550 us (1.39 PFLOP/s; the library's product of these
-// sizes, which writes logits, 1440 to 1540), gradients 4765 to 4810 (three
+// BF16: loss 1514 to 1550 us (1.39 PFLOP/s; the library's product of these
+// sizes, which writes logits, 1440 to 1540), gradients 4760 to 4825 (three
 // products, 1.34; the library's three 4920 to 5140); of codes 795 to 830 (2.6).
 // Of a tile's 99 us some 12 are its beginning, where nothing is loaded yet, and
 // its end: exponentials, 16 cycles each, and g's way out.  One row is bound by reading W: 57 us for 262 MB (4.6 TB/s).
