@@ -279,7 +279,7 @@ struct LogitParams {
   // loss
   float2* part;             // largest logit and sum of exponentials of each strip and row
   int64_t strip_step, row_step;
-  float* at_target;         // the target's logit of each row
+  float* at_target;         // the target's logit of each row (BF16)
   const int32_t* target;    // of listed rows, or NULL
   const int64_t* targets;
   // gradient
@@ -385,6 +385,21 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
 #pragma unroll
     for (int i = 0; i < T::kRT; ++i) {
       const int64_t row = m0 + 32 * T::kI * wm + T::kMf * i + lr;
+      const bool stored = row < live;
+      // the target, where it lies in the lane's columns
+      int64_t t = -1;
+      if (stored) t = p.target ? (int64_t)p.target[row] : p.targets[row];
+      const int64_t at = t - col0;
+      const bool mine = t >= 0 && t < p.V && at >= 0 && at < 32 * T::kJ && ((at >> 2) & (T::kL - 1)) == share;
+      if constexpr (kFP8) {
+        if (__any(mine)) {   // left out (TargetDot)
+          const int out = mine ? (int)at - 4 * share : -1;
+#pragma unroll
+          for (int u = 0; u < T::kRuns; ++u)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) set_quad<T>(acc, i, u, s, 4 * T::kL * u + s == out ? -INFINITY : quad<T>(acc, i, u, s));
+        }
+      }
       // (a NaN is left to the sum)
       float top = -FLT_MAX;
 #pragma unroll
@@ -399,7 +414,6 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
         for (int s = 0; s < 4; ++s)
           sum[s] += __builtin_amdgcn_exp2f(__builtin_fmaf(quad<T>(acc, i, u, s), p.scale2, -top));
       float all = row_sum<T::kL>((sum[0] + sum[1]) + (sum[2] + sum[3]));
-      const bool stored = row < live;
       int strip = wn;
       if constexpr (32 * T::kJ < kStrip && T::kStages == 2) {
         // two waves share a strip: the odd one hands its part over
@@ -417,14 +431,11 @@ __device__ __forceinline__ void logit_tile(const LogitParams& p, const int64_t l
       }
       if (stored && share == 0 && strip >= 0)
         p.part[(n0 / (T::kStages == 2 ? kStrip : 32 * T::kJ) + strip) * p.strip_step + row * p.row_step] = make_float2(top, all);
-      // the target's logit, where it lies in the lane's columns
-      int64_t t = -1;
-      if (stored) t = p.target ? (int64_t)p.target[row] : p.targets[row];
-      const int64_t at = t - col0;
-      const bool mine = t >= 0 && t < p.V && at >= 0 && at < 32 * T::kJ && ((at >> 2) & (T::kL - 1)) == share;
-      if (__any(mine)) {
-        const float v = value_at<T>(acc, i, (int)at);
-        if (mine) p.at_target[row] = v * p.scale2;
+      if constexpr (!kFP8) {
+        if (__any(mine)) {
+          const float v = value_at<T>(acc, i, (int)at);
+          if (mine) p.at_target[row] = v * p.scale2;
+        }
       }
     }
   } else {
@@ -523,11 +534,13 @@ __global__ __launch_bounds__(128) void logit_thin_kernel(const LogitParams p) {
 // and cut them 13 bits below it.  That leaves a logit of 4096 products about
 // 1e-5 off, where each is exact and FP32 sums would leave 1e-6.  Among the
 // exponentials it averages out; the target's logit enters the loss by itself.
-// So for codes it is formed again in FP32, and its exponential in the sum
-// replaced, which keeps the loss of a likely target (a small difference of the
-// two) right.  Loss of 8192 x 32000 x 4096: 2.4e-6 -> 1e-7 of it off, for 1% of
-// the time; products in BF16 on the matrix cores, which hold FP32, would take
-// twice the time.
+// So for codes it is formed in FP32, and the tiles leave it out of their maxima
+// and sums: the join adds its exponential, which keeps the loss of a likely
+// target (a small difference of the two) right, and finite however far the two
+// forms lie apart (a sum that the tile's exponential is taken from again can be
+// left with less than nothing).  Loss of 8192 x 32000 x 4096: 2.4e-6 -> 1e-7 of
+// it off, for 1% of the time; products in BF16 on the matrix cores, which hold
+// FP32, would take twice the time.
 struct TargetDot {
   const uint8_t* x;     // codes, or NULL: not for these inputs
   const uint8_t* w;
@@ -558,8 +571,7 @@ __device__ __forceinline__ float target_dot(const TargetDot& d, int64_t row, int
 struct JoinParams {
   const float2* part;
   int64_t strip_step, row_step;
-  const float* at_target;
-  float* exact;             // target_dot of each row, or NULL
+  float* at_target;         // as the tiles write it, or for codes target_kernel
   TargetDot dot;
   const int32_t* place;     // of each row in the list, or NULL
   const int64_t* targets;
@@ -591,14 +603,14 @@ __device__ __forceinline__ float2 join_strips(const JoinParams& p, int64_t at, i
   return make_float2(top, sum);
 }
 
-// exact: the target's logit as target_dot has it.
-__device__ __forceinline__ void store_loss(const JoinParams& p, int64_t row, int64_t at, float top, float sum, float exact) {
+// target: its logit, for codes not among those of top and sum.
+__device__ __forceinline__ void store_loss(const JoinParams& p, int64_t row, int64_t at, float top, float sum, float target) {
   float loss = 0.0f, lse = 0.0f;
   if (at >= 0) {
-    float target = p.at_target[at];
     if (p.dot.x) {
-      sum += __builtin_amdgcn_exp2f(exact - top) - __builtin_amdgcn_exp2f(target - top);
-      target = exact;
+      const float m = fmaxf(top, target);
+      sum = sum * __builtin_amdgcn_exp2f(top - m) + __builtin_amdgcn_exp2f(target - m);
+      top = m;
     }
     const float log2s = __builtin_amdgcn_logf(sum);
     lse = kLn2 * (top + log2s);
@@ -617,9 +629,10 @@ __device__ __forceinline__ int64_t place_of(const JoinParams& p, int64_t row) {
 // A wave each row, for codes.
 __global__ __launch_bounds__(256) void target_kernel(const JoinParams p) {
   const int64_t row = 4 * (int64_t)blockIdx.x + (threadIdx.x >> 6);
-  if (row >= p.M || place_of(p, row) < 0) return;
+  const int64_t at = row < p.M ? place_of(p, row) : -1;
+  if (at < 0) return;
   const float v = target_dot(p.dot, row, p.targets[row]);
-  if ((threadIdx.x & 63) == 0) p.exact[row] = v;
+  if ((threadIdx.x & 63) == 0) p.at_target[at] = v;
 }
 
 // 16 rows, 16 threads each.
@@ -636,22 +649,22 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const JoinParams p) {
   for (int i = 0; i < 16; ++i) top = fmaxf(top, part[r16][i].x);
 #pragma unroll
   for (int i = 0; i < 16; ++i) sum += part[r16][i].y * __builtin_amdgcn_exp2f(part[r16][i].x - top);
-  store_loss(p, row, at, top, sum, at >= 0 && p.dot.x ? p.exact[row] : 0.0f);
+  store_loss(p, row, at, top, sum, at >= 0 ? p.at_target[at] : 0.0f);
 }
 
 // Few rows: a wave each.
 __global__ __launch_bounds__(64) void loss_join_few_kernel(const JoinParams p) {
   const int64_t row = blockIdx.x, at = place_of(p, row);
-  float top = -FLT_MAX, sum = 0.0f, exact = 0.0f;
+  float top = -FLT_MAX, sum = 0.0f, target = 0.0f;
   if (at >= 0) {
-    if (p.dot.x) exact = target_dot(p.dot, row, p.targets[row]);
+    target = p.dot.x ? target_dot(p.dot, row, p.targets[row]) : p.at_target[at];
     const float2 v = join_strips<64>(p, at, threadIdx.x);
     top = v.x;
 #pragma unroll
     for (int s = 1; s < 64; s *= 2) top = fmaxf(top, __shfl_xor(top, s));
     sum = lanes_sum<64>(v.y * __builtin_amdgcn_exp2f(v.x - top));
   }
-  if (threadIdx.x == 0) store_loss(p, row, at, top, sum, exact);
+  if (threadIdx.x == 0) store_loss(p, row, at, top, sum, target);
 }
 
 // -------------------------------------------------- products with g
@@ -961,7 +974,7 @@ Tiles tiles_for(int64_t M, int64_t N) {
 struct LossSpace {
   Header* header;
   int32_t *list, *place, *target;
-  float *at_target, *exact;
+  float* at_target;
   float2* part;
   int64_t strip_step, row_step, bytes;
   int32_t strips;
@@ -980,7 +993,6 @@ LossSpace loss_space(void* base, int64_t M, int64_t V) {
   const bool few = M <= kFewRows;
   const Tiles tiles = tiles_for(M, V);
   s.at_target = c.take<float>(4 * M);
-  s.exact = c.take<float>(4 * M);
   if (!few) {
     s.header = c.take<Header>(sizeof(Header));
     s.list = c.take<int32_t>(4 * M);
@@ -1244,7 +1256,6 @@ coat_status_t coat_fp8_cross_entropy(const coat_cross_entropy_args_t* a, hipStre
       j.row_step = s.row_step;
       j.strips = s.strips;
       j.z = a->z_loss;
-      j.exact = s.exact;
       if (fp8) j.dot = TargetDot{p.x, w, K, p.scale2};
       if (fp8 && s.list) e = launch(reinterpret_cast<const void*>(&target_kernel), up(rows, 4), 256, &j, stream);
       if (e == hipSuccess)
