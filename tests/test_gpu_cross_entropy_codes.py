@@ -129,3 +129,28 @@ def test_only_the_target():
         want = c.reference.spread(c.lse)
         assert not loss.any()
         assert_between(lse.double(), want - 8 * F * want.abs(), want + 8 * F * want.abs(), "lse")
+
+
+@pytest.mark.parametrize("rows,padding", [(1, 0), (40, 3), (64, 0), (65, 2), (400, 30)])
+@pytest.mark.parametrize("cut,others", [(0.01, -15.0), (-0.01, -15.0), (0.5, -9.0), (-3.0, -9.0), (30.0, -40.0)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradients_of_a_likely_target(rows, padding, cut, others, dtype):
+    """g of the target is p - 1, a small difference: what the cut takes from its logit may not enter it."""
+    coat = lib()
+    scale = abs(cut) / 13440.0
+    w = float(ref.values(codes(torch.tensor([others / (448.0 * 128 * scale)]).clamp(-448, 448)), 1.0)[0])
+    c = Cut(rows, scale, 1 if cut > 0 else -1, other_w=w, padding=padding)
+    r = c.reference
+    lse = r.spread(r.lse).float()
+    for piece in (1, c.vocab):
+        dx = torch.full((rows, c.cols), 5.0, dtype=torch.bfloat16, device=DEV)
+        dw = torch.full((c.vocab, c.cols), 5.0, dtype=dtype, device=DEV)
+        ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)[:max(
+            coat.cross_entropy_bwd_workspace(rows, c.vocab, c.cols, piece=p, codes=True, f32=dtype == torch.float32)
+            for p in (1, piece))]
+        coat.cross_entropy_bwd(c.d_loss.to(DEV), c.x.to(DEV), c.w.to(DEV), c.targets.to(DEV), lse.to(DEV), dx, dw,
+                               workspace=ws, **c.args())
+        parts = 2 if dtype == torch.float32 else 1
+        want_dx, want_dw, dx_err, dw_err = r.gradients(c.d_loss, lse, parts, -(-c.vocab // piece))
+        assert_close(dx.cpu(), want_dx, dx_err, "dx")
+        assert_close(dw.cpu(), want_dw, dw_err, "dw", rounding=BF16 if parts == 1 else F)
