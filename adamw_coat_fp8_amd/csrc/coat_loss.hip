@@ -1094,10 +1094,10 @@ GradSpace grad_space_of(void* base, const GradShape& h, int64_t pieces) {
 GradSpace grad_space(void* base, int64_t bytes, const GradShape& h) {
   const int64_t most = up(h.V, 256);
   GradSpace s;
-  for (int64_t n = 1; n <= most; ++n) {
+  for (int64_t n = 1; n <= most;) {
     s = grad_space_of(base, h, n);
     if (s.bytes <= bytes) return s;
-    n = s.pieces > n ? s.pieces : n;
+    n = s.piece > 256 ? up(h.V, s.piece - 256) : most + 1;   // the next number that makes them smaller
   }
   s.pieces = 0;
   return s;
