@@ -891,8 +891,9 @@ def cross_entropy(x: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor, 
 def cross_entropy_bwd_workspace(rows: int, vocab: int, cols: int, *, piece: int = 8192, codes: bool = False,
                                 f32: bool = False) -> int:
     """Bytes of workspace cross_entropy_bwd needs to go through the vocabulary
-    in pieces of `piece` rows (codes: x and weight are E4M3; f32: dw is
-    float32).  Larger pieces are faster; the least it takes is piece=1's."""
+    in no more pieces than `piece` rows each make (codes: x and weight are
+    E4M3; f32: dw is float32).  Larger pieces are faster; piece=1 gives the
+    least that any number of them takes."""
     if not 0 < piece < 1 << 63:
         raise ValueError("piece must be positive")
     return _workspace_bytes(lambda *sizes: lib.coat_fp8_cross_entropy_bwd_workspace(*sizes, piece, codes, f32),

@@ -1090,17 +1090,34 @@ GradSpace grad_space_of(void* base, const GradShape& h, int64_t pieces) {
   return s;
 }
 
+// The next number of pieces that makes them smaller than those of s, past
+// 256-row ones more than there are.
+int64_t next_pieces(const GradShape& h, const GradSpace& s) {
+  return s.piece > 256 ? up(h.V, s.piece - 256) : up(h.V, 256) + 1;
+}
+
 // The space of as few pieces as `bytes` hold; pieces 0 if none fit.
 GradSpace grad_space(void* base, int64_t bytes, const GradShape& h) {
   const int64_t most = up(h.V, 256);
   GradSpace s;
-  for (int64_t n = 1; n <= most;) {
+  for (int64_t n = 1; n <= most; n = next_pieces(h, s)) {
     s = grad_space_of(base, h, n);
     if (s.bytes <= bytes) return s;
-    n = s.piece > 256 ? up(h.V, s.piece - 256) : most + 1;   // the next number that makes them smaller
   }
   s.pieces = 0;
   return s;
+}
+
+// The least space that `most` pieces or fewer take.  (Fewer may take less: one
+// piece has no sums of dx to keep, and splits of dw go by a piece's tiles.)
+int64_t least_space(const GradShape& h, int64_t most) {
+  GradSpace s = grad_space_of(nullptr, h, 1);
+  int64_t least = s.bytes;
+  for (int64_t n = next_pieces(h, s); n <= most; n = next_pieces(h, s)) {
+    s = grad_space_of(nullptr, h, n);
+    if (s.bytes < least) least = s.bytes;
+  }
+  return least;
 }
 
 bool loss_sizes_ok(int64_t M, int64_t V, int64_t K, bool fp8) {
@@ -1285,7 +1302,7 @@ int64_t coat_fp8_cross_entropy_bwd_workspace(int64_t rows, int64_t vocab, int64_
   if (!loss_sizes_ok(rows, vocab, cols, codes != 0) || piece < 1) return -1;
   if (rows == 0 || vocab == 0 || cols == 0) return 0;
   const GradShape h = {rows, vocab, cols, codes != 0, true, true, f32 != 0};
-  return grad_space_of(nullptr, h, up(vocab, piece < vocab ? round_up(piece, 256) : vocab)).bytes;
+  return least_space(h, up(vocab, piece < vocab ? round_up(piece, 256) : vocab));
 }
 
 coat_status_t coat_fp8_cross_entropy_bwd(const coat_cross_entropy_bwd_args_t* a, hipStream_t stream) {

@@ -620,10 +620,11 @@ coat_status_t coat_fp8_cross_entropy_bwd(
     const coat_cross_entropy_bwd_args_t* args, hipStream_t stream);
 
 /*
- * Bytes of workspace for that call with pieces of `piece` vocabulary rows
- * (rounded up to a multiple of 256; 1 gives the least that it takes, vocab
- * what one piece takes), or -1 for sizes it refuses.  codes: x and weight are
- * E4M3; f32: dw is FP32.
+ * Bytes of workspace for that call in no more pieces of the vocabulary than
+ * `piece` rows each make (rounded up to a multiple of 256), or -1 for sizes it
+ * refuses.  vocab gives what one piece takes, 1 the least that any number of
+ * them takes; a larger `piece` never gives less.  codes: x and weight are E4M3;
+ * f32: dw is FP32.
  */
 int64_t coat_fp8_cross_entropy_bwd_workspace(int64_t rows, int64_t vocab,
                                              int64_t cols, int64_t piece,

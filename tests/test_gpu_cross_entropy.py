@@ -254,3 +254,30 @@ def test_captured(rows):
         ws.fill_(255)
         step()
         assert all(torch.equal(a, b) for a, b in zip(first, (loss, lse, dx, dw)))
+
+
+@pytest.mark.parametrize("kind,rows,vocab,cols", [("bf16", 700, 300, 2048), ("bf16", 2049, 1000, 1024), ("fp8", 600, 500, 1024),
+                                                  ("bf16", 64, 300, 1024), ("bf16", 1000, 2100, 2048)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_workspaces_of_the_size_asked_for(kind, rows, vocab, cols, dtype):
+    """Few vocabulary rows beside the columns, where one piece takes less than several (their sums of dx): every
+    query's size is taken, and nothing behind it is written."""
+    coat = lib()
+    c = Case(rows, vocab, cols, kind, padding=rows // 9)
+    r = c.reference()
+    lse = r.spread(r.lse).float()
+    dx, dw, dx_err, dw_err = r.gradients(c.d_loss, lse, 2 if dtype == torch.float32 else 1, -(-vocab // 256))
+    done = set()
+    for piece in (8192, 1024, 512, 1):
+        n = coat.cross_entropy_bwd_workspace(rows, vocab, cols, piece=piece, codes=kind == "fp8", f32=dtype == torch.float32)
+        if n in done:
+            continue
+        done.add(n)
+        whole = torch.full((n + 4096,), 77, dtype=torch.uint8, device=DEV)
+        d_x = torch.full((rows, cols), 5.0, dtype=torch.bfloat16, device=DEV)
+        d_w = torch.full((vocab, cols), 5.0, dtype=dtype, device=DEV)
+        coat.cross_entropy_bwd(c.d_loss.to(DEV), c.x.to(DEV), c.w.to(DEV), c.targets.to(DEV), lse.to(DEV), d_x, d_w,
+                               workspace=whole[:n], **c.scale_args())
+        assert_close(d_x.cpu(), dx, dx_err, "dx")
+        assert_close(d_w.cpu(), dw, dw_err, "dw", rounding=BF16 if dtype == torch.bfloat16 else F)
+        assert bool((whole[n:] == 77).all())

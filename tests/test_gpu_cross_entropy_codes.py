@@ -145,9 +145,8 @@ def test_gradients_of_a_likely_target(rows, padding, cut, others, dtype):
     for piece in (1, c.vocab):
         dx = torch.full((rows, c.cols), 5.0, dtype=torch.bfloat16, device=DEV)
         dw = torch.full((c.vocab, c.cols), 5.0, dtype=dtype, device=DEV)
-        ws = torch.full((1 << 26,), 255, dtype=torch.uint8, device=DEV)[:max(
-            coat.cross_entropy_bwd_workspace(rows, c.vocab, c.cols, piece=p, codes=True, f32=dtype == torch.float32)
-            for p in (1, piece))]
+        ws = torch.full((coat.cross_entropy_bwd_workspace(rows, c.vocab, c.cols, piece=piece, codes=True,
+                                                          f32=dtype == torch.float32),), 255, dtype=torch.uint8, device=DEV)
         coat.cross_entropy_bwd(c.d_loss.to(DEV), c.x.to(DEV), c.w.to(DEV), c.targets.to(DEV), lse.to(DEV), dx, dw,
                                workspace=ws, **c.args())
         parts = 2 if dtype == torch.float32 else 1
