@@ -281,3 +281,75 @@ def test_workspaces_of_the_size_asked_for(kind, rows, vocab, cols, dtype):
         assert_close(d_x.cpu(), dx, dx_err, "dx")
         assert_close(d_w.cpu(), dw, dw_err, "dw", rounding=BF16 if dtype == torch.bfloat16 else F)
         assert bool((whole[n:] == 77).all())
+
+
+SIGNS = ("negative", "zeros", "none", "wide", "infinite", "nan", "tiny")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("rows", [1, 30, 64, 65, 900])
+@pytest.mark.parametrize("what", SIGNS)
+def test_gradients_of_any_d_loss(kind, rows, what):
+    """d_loss of both signs, the largest magnitude negative; zeros among them or alone; from 1e-6 to 1e4; of 2^-100;
+    an infinity or a NaN, which stays in its row."""
+    c = Case(rows, 700, 128, kind, padding=rows // 10, z=1e-3)
+    g = torch.Generator().manual_seed(rows)
+    live = torch.nonzero(ref.live_rows(c.targets, c.vocab))[:, 0]
+    n = len(live)
+    d = torch.rand(n, generator=g) + 0.1
+    d[torch.rand(n, generator=g) < 0.5] *= -1.0
+    d[0] = -3.0
+    if what == "zeros":
+        d[::3] = 0.0
+    elif what == "none":
+        d[:] = 0.0
+    elif what == "wide":
+        d *= 10.0 ** (torch.rand(n, generator=g) * 10 - 6)
+    elif what == "tiny":
+        d *= 2.0 ** -100
+    bad = live[n // 2]
+    c.d_loss[live] = d
+    r = c.reference()
+    lse = r.spread(r.lse).float()
+    if what in ("infinite", "nan"):
+        others = torch.arange(rows) != bad
+        want = r.gradients(torch.where(others, c.d_loss, torch.zeros(())), lse, 1)
+        c.d_loss[bad] = -float(what[:3])
+        for dtype in (torch.bfloat16, torch.float32):
+            dx, dw = c.backward(lse, dtype)
+            assert not torch.isfinite(dx[bad]).any() and not torch.isfinite(dw[c.targets[bad]]).any()
+            assert_close(dx[others], want[0][others], want[2][others], "dx")
+        return
+    c.check_backward(r, lse)
+    c.check_backward(r, lse, dtype=torch.float32, piece=256)
+    if what == "none":
+        dx, dw = c.backward(lse)
+        assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("kind,cols", [("bf16", 64), ("fp8", 128)])
+@pytest.mark.parametrize("rows", [1, 30, 64, 65, 900])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_equal_d_loss_is_not_rounded(kind, cols, rows, sign):
+    """Equal d, of either sign, that lie between two BF16 values: g holds their share of the largest |d|, which is
+    exact.  All of the probability is on row 0 of the vocabulary, nothing on the target."""
+    coat = lib()
+    vocab, d = 300, sign * (1.0 + 2.0 ** -8 - 2.0 ** -20)
+    x, w = torch.ones(rows, cols), torch.full((vocab, cols), -3.25)
+    w[0] = 0.0
+    cast = (lambda t: t.bfloat16()) if kind == "bf16" else (lambda t: t.to(torch.float8_e4m3fn).view(torch.uint8))
+    x, w = cast(x).to(DEV), cast(w).to(DEV)
+    targets = torch.full((rows,), 7, device=DEV)
+    loss, lse = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    coat.cross_entropy(x, w, targets, loss, lse, workspace=torch.empty(coat.cross_entropy_workspace(rows, vocab, cols),
+                                                                     dtype=torch.uint8, device=DEV))
+    # the scale in powers of two, a logit, ln 2 and the product with it: four roundings
+    assert not lse.any() and bool(((loss.double() - 3.25 * cols).abs() <= 5 * F * 3.25 * cols).all())
+    dx, dw = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV), torch.empty(vocab, cols, device=DEV)
+    ws = torch.empty(coat.cross_entropy_bwd_workspace(rows, vocab, cols, codes=kind == "fp8", f32=True), dtype=torch.uint8,
+                     device=DEV)
+    coat.cross_entropy_bwd(torch.full((rows,), d, device=DEV), x, w, targets, lse, dx, dw, workspace=ws)
+    assert bool((dx == torch.tensor(3.25 * d, dtype=torch.float64).bfloat16().to(DEV)).all())
+    want = torch.zeros(vocab, cols, dtype=torch.float64, device=DEV)
+    want[0], want[7] = rows * d, -rows * d
+    assert bool(((dw.double() - want).abs() <= F * want.abs()).all())

@@ -192,3 +192,38 @@ def test_two_streams():
     torch.cuda.synchronize()
     for j, ws in zip(jobs, want):
         assert all(torch.equal(j[k], t) for k, t in zip(("loss", "lse", "dx", "dw"), ws))
+
+
+def test_far_weights_dx():
+    """dx from 4.9 GB of weights, whose last rows lie past 4 GiB, in one piece and in five."""
+    coat = lib()
+    rows, vocab, cols = 70, 300_000, 8192
+    x, w = randn(rows, cols), randn(vocab, cols, seed=1, scale=cols ** -0.5)
+    targets = torch.randint(vocab - LAST, vocab, (rows,), generator=torch.Generator().manual_seed(1))
+    pieces = [slice(v, v + 25_000) for v in range(0, vocab, 25_000)]
+    logits = torch.cat([x.double() @ w[p].double().t() for p in pieces], 1)
+    lse = torch.logsumexp(logits, 1)
+    d = torch.rand(rows, device=DEV) - 0.5
+    # as vocabulary_ref.Entropy has it, with the lse that the call is given
+    size = (x.double().abs() @ w[-LAST:].double().abs().t()).amax() * 2
+    l_err = float((cols / 16 + 64) * 2 * F * size)
+    given = lse.float()
+    g = torch.exp(logits - given.double()[:, None])
+    rel = l_err + 6 * F * (logits.abs() + given.double().abs()[:, None]) + 8 * F
+    err = d.double().abs()[:, None] * g * (1.01 * rel)
+    hot = torch.arange(rows, device=DEV), targets.to(DEV)
+    g[hot] -= 1.0
+    g *= d.double()[:, None]
+    err[hot] += 8 * F * d.double().abs()
+    want = torch.zeros(rows, cols, dtype=torch.float64, device=DEV)
+    room = torch.zeros_like(want)
+    for p in pieces:
+        wide = w[p].double()
+        want += g[:, p] @ wide
+        room += (err[:, p] + BF16 * (g[:, p].abs() + err[:, p]) + (vocab / 16 + 128 + 5) * 2 * F * g[:, p].abs()) @ wide.abs()
+        del wide
+    for piece in (65536, vocab):
+        dx = torch.full_like(x, 3.0)
+        ws = torch.empty(coat.cross_entropy_bwd_workspace(rows, vocab, cols, piece=piece), dtype=torch.uint8, device=DEV)
+        coat.cross_entropy_bwd(d, x, w, targets.to(DEV), given, dx, None, workspace=ws)
+        assert_close(dx.cpu(), want.cpu(), room.cpu(), "dx")
