@@ -31,14 +31,17 @@ namespace {
 // g is stored divided by the largest |d| of the call, which multiplies the
 // products' FP32 results: with one d for all rows, a mean's, the target's
 // value 1 - p of an unlikely target then lies near 1, where BF16 is exact, and
-// is not rounded alike in every row.
+// is not rounded alike in every row.  In BF16, as the matrix cores take it at
+// their rate: with one part the gradients of 8192 x 32000 x 4096 are 1.9e-3 of
+// their norm off, 1.65e-3 if only the results are rounded, and a second part
+// takes a product more for each of dx and dW (1.5 to 1.7 ms of 4.8).
 //
 // Large calls are bound by the matrix cores and, within those, by the card's
 // power (coat_tile.h); the logits never leave the chip, so that the forward
 // pass reads x and W and writes 8 bytes a row and strip.  8192 x 32000 x 4096 in
-// BF16: loss 1514 to 1550 us (1.39 PFLOP/s; the library's product of these
-// sizes, which writes logits, 1440 to 1540), gradients 4760 to 4825 (three
-// products, 1.34; the library's three 4920 to 5140); of codes 795 to 830 (2.6).
+// BF16: loss 1508 to 1550 us (1.40 PFLOP/s; the library's product of these
+// sizes, which writes logits, 1440 to 1540), gradients 4730 to 4825 (three
+// products, 1.34; the library's three 4900 to 5140); of codes 808 to 855 (2.6).
 // Of a tile's 99 us some 12 are its beginning, where nothing is loaded yet, and
 // its end: exponentials, 16 cycles each, and g's way out.  One row is bound by reading W: 57 us for 262 MB (4.6 TB/s).
 

@@ -16,11 +16,9 @@
 // set 1 while set 0 of the next step is read from the other stage and the
 // loads of the step after next go into this one.
 //
-// What it waits for (loss of 8192 x 32000 x 4096): with the loop's loads left
-// out a tenth of the cycles goes, with its LDS reads left out none; each takes
-// power.  Fetching the neighbours' common panels into the L2 some steps ahead
-// does not help (2.79e6 cycles, 2.87e6 with it), nor does taking turns with the
-// loads (2.76e6, 2.97e6).
+// Not taken (loss of 8192 x 32000 x 4096): the neighbours' common panels fetched
+// into the L2 some steps ahead (2.79e6 cycles, 2.87e6 with it), waves that take
+// turns with their loads (2.76e6, 2.97e6).
 //
 // The MFMA takes B as its first operand, so each result is a tile of C^T.  With
 // results of kMf x kMf (32 or 16), L = 64 / kMf lanes share a row, and lane l
